@@ -280,7 +280,9 @@ int tp_partial_reduce_ex(const float *const *partials, int64_t P, int64_t rows, 
                          int64_t ld_out, int32_t op, const float *bias, tp_stream_t stream);
 
 /* ---- one rank's column->row MLP ------------------------------------ */
-enum { TP_ACT_NONE = 0, TP_ACT_GELU_ERF = 1 };
+/* GELU_TANH, SILU and RELU are activations of tp_linear and tp_gated_linear
+ * (and their backward passes) only. */
+enum { TP_ACT_NONE = 0, TP_ACT_GELU_ERF = 1, TP_ACT_GELU_TANH = 2, TP_ACT_SILU = 3, TP_ACT_RELU = 4 };
 
 typedef struct {
   int32_t dtype;     /* TP_BF16: X, A_i, B_i, Y_ws bf16 (fp32 accumulate);
@@ -525,6 +527,180 @@ typedef struct {
  */
 int tp_colrow_mlp_backward(const tp_mlp_bwd_args *args, tp_stream_t s_compute, tp_stream_t s_reduce);
 
+/* ---- linear layer: bias, activation and residual in the product ---------- */
+/* Activations of this section, on fp32 values:
+ *   TP_ACT_NONE       x
+ *   TP_ACT_GELU_ERF   x/2 (1 + erf(x / sqrt 2))
+ *   TP_ACT_GELU_TANH  x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)))
+ *   TP_ACT_SILU       x / (1 + e^-x)
+ *   TP_ACT_RELU       max(x, 0) (a NaN stays one; derivative 0 at 0)
+ * Row strides (`_ld`) are in elements; 0 = contiguous.  A weight may be a column
+ * slice of a full weight (a rank's shard), read in place through its stride.
+ * Pointers need their element's alignment only; 16-byte aligned rows are
+ * fastest. */
+typedef struct {
+  int32_t dtype;         /* TP_BF16 or TP_F32: X, W, residual, pre_out (fp32 accumulation) */
+  int32_t act;           /* TP_ACT_* */
+  int32_t weight_layout; /* TP_WEIGHTS_MATH: W is [K, N]; TP_WEIGHTS_LINEAR: [N, K] */
+  int32_t out_dtype;     /* of `out`: dtype, or TP_F32 (e.g. a row-parallel layer's partial) */
+  int64_t M, N, K;       /* M >= 0 (0 = nothing to do), N, K >= 1 */
+  const void *X;         /* [M, K] */
+  int64_t X_ld;
+  const void *W;
+  int64_t W_ld;
+  const float *bias;     /* optional [N] fp32 */
+  const void *residual;  /* optional [M, N] */
+  int64_t residual_ld;
+  void *out;             /* [M, N]; may be `residual` itself (same stride, out_dtype = dtype) */
+  int64_t out_ld;
+  void *pre_out;         /* optional [M, N]: X W + bias rounded to dtype, kept for the backward */
+  int64_t pre_ld;
+} tp_linear_args;
+
+/*
+ * out = act(X W + bias) + residual, in one launch; the value is rounded once, when
+ * it is stored.  Rows are independent: a row's result does not depend on the
+ * other rows' values.  Capturable into a HIP graph.
+ * Errors: TP_ERR_ARG (NULL or overlapping buffers, unknown dtype / act / layout,
+ *         bad sizes or strides), TP_ERR_UNSUPPORTED (sizes beyond the kernels'
+ *         32-bit indexes or the grid), TP_ERR_HIP.
+ */
+int tp_linear(const tp_linear_args *args, tp_stream_t stream);
+
+typedef struct {
+  int32_t dtype;         /* as the forward: X, W, dOut, pre */
+  int32_t act;
+  int32_t weight_layout;
+  int32_t dx_dtype;      /* of dX: dtype, or TP_F32 (a rank's partial, for tp_partial_reduce) */
+  int32_t dw_dtype;      /* of dW: dtype, or TP_F32 */
+  int32_t accumulate;    /* 1: dW and dbias are added to (needs TP_F32 dW, if dW is asked for) */
+  int64_t M, N, K;       /* M >= 0: with M = 0 the gradients are zero (or unchanged: accumulate) */
+  const void *X;         /* [M, K]; may be NULL without dW */
+  int64_t X_ld;
+  const void *W;         /* as in the forward; may be NULL without dX */
+  int64_t W_ld;
+  const void *dOut;      /* [M, N]: the gradient at `out` (and so the residual's gradient) */
+  int64_t dOut_ld;
+  const void *pre;       /* [M, N]: the forward's pre_out; ignored for TP_ACT_NONE */
+  int64_t pre_ld;
+  void *dX;              /* optional [M, K] */
+  int64_t dX_ld;
+  void *dW;              /* optional, in W's layout */
+  int64_t dW_ld;
+  float *dbias;          /* optional [N] fp32 */
+  void *ws;              /* workspace of tp_linear_backward_ws bytes, 16-byte aligned */
+  int64_t ws_bytes;
+} tp_linear_bwd_args;
+
+/* Bytes of workspace the call needs (0: none).  Reads dtype, act, M, N and which
+ * of dX, dW, dbias are asked for (non-NULL).  Host only. */
+int tp_linear_backward_ws(const tp_linear_bwd_args *args, int64_t *bytes);
+
+/*
+ * dPre = dOut * act'(pre) (rounded to dtype for the two products);
+ * dX = dPre W^T;  dW (+)= X^T dPre;  dbias (+)= column sums of the unrounded dPre.
+ * Deterministic: no atomics.  Capturable into a HIP graph.
+ * Errors: as tp_linear, plus TP_ERR_ARG for a missing or too small workspace.
+ */
+int tp_linear_backward(const tp_linear_bwd_args *args, tp_stream_t stream);
+
+/* ---- gated linear block ------------------------------------------------- */
+typedef struct {
+  int32_t dtype;         /* X, W_gate, W_up, gate_out, up_out, out */
+  int32_t act;
+  int32_t weight_layout; /* of both weights */
+  int64_t M, F, K;       /* M >= 0 (0 = nothing to do), F, K >= 1 */
+  const void *X;         /* [M, K] */
+  int64_t X_ld;
+  const void *W_gate;    /* [K, F] or, linear, [F, K] */
+  const void *W_up;
+  int64_t W_ld;          /* of both: halves of one merged weight have its stride */
+  void *out;             /* [M, F] */
+  int64_t out_ld;
+  void *gate_out;        /* optional [M, F]: X W_gate and X W_up, rounded, kept for the */
+  void *up_out;          /* backward (both or neither) */
+  int64_t keep_ld;       /* of both */
+} tp_gated_args;
+
+/*
+ * out = act(X W_gate) * (X W_up): both projections, the activation and the
+ * product in one launch (SwiGLU with TP_ACT_SILU, GEGLU with a GELU).  The down
+ * projection with the block's residual is tp_linear.  Capturable.
+ * Errors: as tp_linear.
+ */
+int tp_gated_linear(const tp_gated_args *args, tp_stream_t stream);
+
+typedef struct {
+  int32_t dtype;
+  int32_t act;
+  int32_t weight_layout;
+  int32_t dx_dtype;      /* as in tp_linear_bwd_args */
+  int32_t dw_dtype;
+  int32_t accumulate;
+  int64_t M, F, K;
+  const void *X;         /* [M, K]; may be NULL without the weight gradients */
+  int64_t X_ld;
+  const void *W_gate;    /* may be NULL without dX */
+  const void *W_up;
+  int64_t W_ld;
+  const void *gate;      /* [M, F]: the forward's gate_out and up_out */
+  const void *up;
+  int64_t keep_ld;
+  const void *dOut;      /* [M, F] */
+  int64_t dOut_ld;
+  void *dX;              /* optional [M, K] */
+  int64_t dX_ld;
+  void *dW_gate;         /* optional, in the weights' layout (both or neither) */
+  void *dW_up;
+  int64_t dW_ld;
+  void *ws;              /* workspace of tp_gated_linear_backward_ws bytes, 16-byte aligned */
+  int64_t ws_bytes;
+} tp_gated_bwd_args;
+
+/* Bytes of workspace the call needs (reads dtype, M and F).  Host only. */
+int tp_gated_linear_backward_ws(const tp_gated_bwd_args *args, int64_t *bytes);
+
+/*
+ * dUp = dOut * act(gate);  dGate = dOut * up * act'(gate) (each rounded to dtype);
+ * dX = dGate W_gate^T + dUp W_up^T in one accumulator;
+ * dW_gate (+)= X^T dGate;  dW_up (+)= X^T dUp, in one launch.
+ * Errors: as tp_linear_backward.
+ */
+int tp_gated_linear_backward(const tp_gated_bwd_args *args, tp_stream_t stream);
+
+/* ---- global gradient norm and clipping ----------------------------------- */
+/* Partial sums of squares that one tp_grad_sumsq call leaves. */
+enum { TP_GRAD_PARTS = 1024 };
+
+typedef struct {
+  const void *grad;      /* contiguous, its element's alignment; NULL only with n = 0 */
+  void *out;             /* tp_grad_clip's output: `grad` itself (in place) or a buffer apart
+                            from every gradient; ignored by tp_grad_sumsq */
+  int64_t n;             /* elements, >= 0 */
+  int32_t dtype;         /* TP_F32 or TP_BF16, of grad and out */
+} tp_grad_tensor;
+
+/*
+ * parts[0 .. TP_GRAD_PARTS) <- partial sums of the squares of every element of
+ * the tensors, in 64 bits (device memory, overwritten).  Their sum is the sum of
+ * squares; across ranks the vectors add elementwise (one all-reduce), or stand
+ * one after another.  Deterministic.
+ * Errors: TP_ERR_ARG, TP_ERR_HIP.
+ */
+int tp_grad_sumsq(const tp_grad_tensor *tensors, int64_t num, double *parts, tp_stream_t stream);
+
+/*
+ * norm = sqrt(sum of parts[0 .. ranks * TP_GRAD_PARTS)), and every tensor
+ * out = grad * min(1, max_norm / (norm + eps)), the factor rounded to fp32.
+ * norm_out (optional, device) receives the norm in fp32.  An infinite norm makes
+ * the factor 0, a NaN one NaN, as the formula does; the caller reads norm_out.
+ * num = 0 computes the norm alone.
+ * Errors: TP_ERR_ARG (max_norm or eps negative or NaN, ranks outside [1, 64],
+ *         NULL or overlapping buffers), TP_ERR_HIP.
+ */
+int tp_grad_clip(const tp_grad_tensor *tensors, int64_t num, const double *parts, int64_t ranks, double max_norm,
+                 double eps, float *norm_out, tp_stream_t stream);
+
 /* ---- per-kernel timing (measurement support) ---------------------------- */
 /* Kernel families timed by the optional instrumentation below: the forward's
  * GEMMs, the backward's input-gradient GEMMs (dH and dX) and its
@@ -534,7 +710,11 @@ int tp_colrow_mlp_backward(const tp_mlp_bwd_args *args, tp_stream_t s_compute, t
  * bytes, the operands and the peers' partials read once and each output
  * written once).  TP_KERNEL_REDUCE_TAIL is the forward's last-block reduction
  * on a chunked two-stream schedule, which no GEMM runs beside (a one-shot
- * grid over the whole chip); every other reduction is TP_KERNEL_REDUCE. */
+ * grid over the whole chip); every other reduction is TP_KERNEL_REDUCE.
+ * The products of tp_linear and tp_gated_linear are filed under GEMM1, those of
+ * their backward passes under GEMM_DGRAD and GEMM_WGRAD, and the passes that
+ * only stream (gradients at the activation, bias gradients, the gradient norm
+ * and clipping) under REDUCE. */
 enum { TP_KERNEL_MATERIALIZE = 0, TP_KERNEL_GEMM1 = 1, TP_KERNEL_GEMM2 = 2, TP_KERNEL_REDUCE = 3,
        TP_KERNEL_GEMM_DGRAD = 4, TP_KERNEL_GEMM_WGRAD = 5, TP_KERNEL_GATHER = 6,
        TP_KERNEL_GEMM2_REDUCE = 7, TP_KERNEL_GEMM_DGRAD_REDUCE = 8, TP_KERNEL_REDUCE_TAIL = 9,

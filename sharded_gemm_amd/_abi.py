@@ -32,19 +32,26 @@ TP_REDUCE_FULL = 0
 TP_REDUCE_SPLIT = 1
 TP_ACT_NONE = 0
 TP_ACT_GELU_ERF = 1
+TP_ACT_GELU_TANH = 2
+TP_ACT_SILU = 3
+TP_ACT_RELU = 4
 TP_REDUCE_OP_SUM = 0
 TP_REDUCE_OP_MAX = 1
 TP_REDUCE_OP_MIN = 2
 
 # Every symbol include/tpshard.h declares.
 EXPORTS = ("tp_last_error", "tp_version", "tp_layout_plan", "tp_check_broadcast_binary", "tp_infer_matmul_dims_mapping", "tp_shard_materialize", "tp_shard_materialize_batch", "tp_shard_gather",
-           "tp_partial_reduce", "tp_partial_reduce_ex", "tp_colrow_mlp", "tp_colrow_mlp_noalloc", "tp_colrow_mlp_stack", "tp_colrow_mlp_backward", "tp_timing_enable", "tp_timing_read")
+           "tp_partial_reduce", "tp_partial_reduce_ex", "tp_colrow_mlp", "tp_colrow_mlp_noalloc", "tp_colrow_mlp_stack", "tp_colrow_mlp_backward",
+           "tp_linear", "tp_linear_backward_ws", "tp_linear_backward", "tp_gated_linear", "tp_gated_linear_backward_ws",
+           "tp_gated_linear_backward", "tp_grad_sumsq", "tp_grad_clip", "tp_timing_enable", "tp_timing_read")
 
 TP_KERNEL_NAMES = ("materialize", "gemm1", "gemm2", "reduce", "gemm_dgrad", "gemm_wgrad", "gather", "gemm2_reduce",
                    "gemm_dgrad_reduce", "reduce_tail")
 
 TP_REDUCE_FUSION_AUTO = 0
 TP_REDUCE_FUSION_OFF = 1
+
+TP_GRAD_PARTS = 1024
 
 TP_WEIGHTS_MATH = 0
 TP_WEIGHTS_LINEAR = 1
@@ -117,6 +124,47 @@ class tp_materialize_item(C.Structure):
                 ("local_only", C.c_int32), ("local_device", C.c_int64)]
 
 
+class tp_linear_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("act", C.c_int32), ("weight_layout", C.c_int32), ("out_dtype", C.c_int32),
+                ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64),
+                ("X", C.c_void_p), ("X_ld", C.c_int64), ("W", C.c_void_p), ("W_ld", C.c_int64),
+                ("bias", C.c_void_p), ("residual", C.c_void_p), ("residual_ld", C.c_int64),
+                ("out", C.c_void_p), ("out_ld", C.c_int64), ("pre_out", C.c_void_p), ("pre_ld", C.c_int64)]
+
+
+class tp_linear_bwd_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("act", C.c_int32), ("weight_layout", C.c_int32), ("dx_dtype", C.c_int32),
+                ("dw_dtype", C.c_int32), ("accumulate", C.c_int32),
+                ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64),
+                ("X", C.c_void_p), ("X_ld", C.c_int64), ("W", C.c_void_p), ("W_ld", C.c_int64),
+                ("dOut", C.c_void_p), ("dOut_ld", C.c_int64), ("pre", C.c_void_p), ("pre_ld", C.c_int64),
+                ("dX", C.c_void_p), ("dX_ld", C.c_int64), ("dW", C.c_void_p), ("dW_ld", C.c_int64),
+                ("dbias", C.c_void_p), ("ws", C.c_void_p), ("ws_bytes", C.c_int64)]
+
+
+class tp_gated_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("act", C.c_int32), ("weight_layout", C.c_int32),
+                ("M", C.c_int64), ("F", C.c_int64), ("K", C.c_int64),
+                ("X", C.c_void_p), ("X_ld", C.c_int64), ("W_gate", C.c_void_p), ("W_up", C.c_void_p),
+                ("W_ld", C.c_int64), ("out", C.c_void_p), ("out_ld", C.c_int64),
+                ("gate_out", C.c_void_p), ("up_out", C.c_void_p), ("keep_ld", C.c_int64)]
+
+
+class tp_gated_bwd_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("act", C.c_int32), ("weight_layout", C.c_int32), ("dx_dtype", C.c_int32),
+                ("dw_dtype", C.c_int32), ("accumulate", C.c_int32),
+                ("M", C.c_int64), ("F", C.c_int64), ("K", C.c_int64),
+                ("X", C.c_void_p), ("X_ld", C.c_int64), ("W_gate", C.c_void_p), ("W_up", C.c_void_p),
+                ("W_ld", C.c_int64), ("gate", C.c_void_p), ("up", C.c_void_p), ("keep_ld", C.c_int64),
+                ("dOut", C.c_void_p), ("dOut_ld", C.c_int64), ("dX", C.c_void_p), ("dX_ld", C.c_int64),
+                ("dW_gate", C.c_void_p), ("dW_up", C.c_void_p), ("dW_ld", C.c_int64),
+                ("ws", C.c_void_p), ("ws_bytes", C.c_int64)]
+
+
+class tp_grad_tensor(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
+
+
 class tp_kernel_stat(C.Structure):
     _fields_ = [("launches", C.c_int64), ("total_ms", C.c_double), ("min_ms", C.c_double),
                 ("max_ms", C.c_double), ("work", C.c_double)]
@@ -170,6 +218,19 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.tp_colrow_mlp_stack.argtypes = [C.POINTER(tp_mlp_args), C.c_int64, C.c_void_p, C.c_void_p]
     lib.tp_colrow_mlp_backward.argtypes = [C.POINTER(tp_mlp_bwd_args), C.c_void_p, C.c_void_p]
     lib.tp_colrow_mlp_backward.restype = C.c_int
+    for name, struct in (("tp_linear", tp_linear_args), ("tp_linear_backward", tp_linear_bwd_args),
+                         ("tp_gated_linear", tp_gated_args), ("tp_gated_linear_backward", tp_gated_bwd_args)):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = C.c_int, [C.POINTER(struct), C.c_void_p]
+    for name, struct in (("tp_linear_backward_ws", tp_linear_bwd_args),
+                         ("tp_gated_linear_backward_ws", tp_gated_bwd_args)):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = C.c_int, [C.POINTER(struct), i64p]
+    lib.tp_grad_sumsq.restype = C.c_int
+    lib.tp_grad_sumsq.argtypes = [C.POINTER(tp_grad_tensor), C.c_int64, C.c_void_p, C.c_void_p]
+    lib.tp_grad_clip.restype = C.c_int
+    lib.tp_grad_clip.argtypes = [C.POINTER(tp_grad_tensor), C.c_int64, C.c_void_p, C.c_int64, C.c_double, C.c_double,
+                                 C.c_void_p, C.c_void_p]
     lib.tp_timing_enable.restype = C.c_int
     lib.tp_timing_enable.argtypes = [C.c_int32]
     lib.tp_timing_read.restype = C.c_int
@@ -662,6 +723,260 @@ def tp_colrow_mlp_backward(X, A_i, B_i, H_i, Y_i, dZ, dH_ws, dX_i, dA_i, dB_i, *
                         _tensors(X, A_i, B_i, H_i, Y_i, dZ, dH_ws, dX_i, dA_i, dB_i, peers, dX_out, dZ_shards,
                                  dX_split))
     _check(lib.tp_colrow_mlp_backward(C.byref(args), sc, sr))
+
+
+def _mat(t, name, shape=None, dtype=None):
+    """(pointer, row stride; 0 = contiguous) of a 2-D tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if not hasattr(t, "data_ptr") or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be [{shape[0]}, {shape[1]}], not {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.is_contiguous() or t.numel() == 0:
+        return t.data_ptr(), 0
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name}: rows must be contiguous and apart (strides {t.stride()})")
+    return t.data_ptr(), int(t.stride(0)) if rows > 1 else 0
+
+
+def _on_gpu(*tensors):
+    """Every tensor lies on the current GPU (the kernels take its pointer)."""
+    import torch
+    for t in _tensors(*tensors):
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"every tensor must be on the current GPU, not {t.device}")
+
+
+def _either(t, name, dtype):
+    """The type code of an output that holds `dtype` or fp32."""
+    import torch
+    if t is None:
+        return TP_F32 if dtype == torch.float32 else TP_BF16
+    if t.dtype not in (dtype, torch.float32):
+        raise TypeError(f"{name} must be {dtype} or torch.float32, not {t.dtype}")
+    return _dtype_code(t)
+
+
+def _weight_dims(W, weight_layout, name="W"):
+    """(K, N) of a weight in its layout."""
+    if not hasattr(W, "data_ptr") or W.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D tensor")
+    a, b = int(W.shape[0]), int(W.shape[1])
+    return (b, a) if weight_layout == TP_WEIGHTS_LINEAR else (a, b)
+
+
+def _ws(ws):
+    """(pointer, bytes) of a workspace tensor."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _new_ws(fn, args, device):
+    import torch
+    n = C.c_int64()
+    _check(fn(C.byref(args), C.byref(n)))
+    return torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
+
+
+def _call(fn, args, stream, prepare, tensors):
+    """Run an entry point that takes one argument structure, or prepare it."""
+    _on_gpu(*tensors)
+    if prepare:
+        return Prepared(fn, (C.byref(args),), [args], [_stream_ptr(stream)], _tensors(*tensors))
+    _check(fn(C.byref(args), _stream_ptr(stream)))
+
+
+def tp_linear(X, W, out, *, bias=None, residual=None, pre_out=None, act=TP_ACT_NONE, weight_layout=TP_WEIGHTS_MATH,
+              stream=None, prepare=False):
+    """out = act(X W + bias) + residual, in one launch; ``pre_out`` keeps X W + bias
+    for the backward.
+
+    X [M, K], W [K, N] (or [N, K], TP_WEIGHTS_LINEAR) and residual share a dtype (bf16
+    or fp32); out is in it, or fp32, and may be the residual itself; bias is fp32
+    [N].  Rows may be strided (a weight may be a column slice of a full one).  With
+    ``prepare=True`` nothing runs; a ``Prepared`` call taking the stream is returned."""
+    lib = load()
+    M, K = (int(v) for v in X.shape)
+    N = _weight_dims(W, weight_layout)[1]
+    dt = X.dtype
+    args = tp_linear_args(dtype=_dtype_code(X), act=act, weight_layout=weight_layout,
+                          out_dtype=_either(out, "out", dt), M=M, N=N, K=K)
+    args.X, args.X_ld = _mat(X, "X")
+    args.W, args.W_ld = _mat(W, "W", (N, K) if weight_layout == TP_WEIGHTS_LINEAR else (K, N), dt)
+    args.out, args.out_ld = _mat(out, "out", (M, N))
+    args.residual, args.residual_ld = _mat(residual, "residual", (M, N), dt)
+    args.pre_out, args.pre_ld = _mat(pre_out, "pre_out", (M, N), dt)
+    _check_bias(bias, N)
+    args.bias = _ptr(bias)
+    return _call(lib.tp_linear, args, stream, prepare, (X, W, out, bias, residual, pre_out))
+
+
+def tp_linear_backward_ws(X, W, dOut, *, act=TP_ACT_NONE, weight_layout=TP_WEIGHTS_MATH, dbias=None):
+    """A workspace (uint8 tensor) for ``tp_linear_backward`` of these shapes."""
+    args = tp_linear_bwd_args(dtype=_dtype_code(X), act=act, weight_layout=weight_layout, M=int(X.shape[0]),
+                              N=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]), dX=16, dW=16, dbias=_ptr(dbias))
+    return _new_ws(load().tp_linear_backward_ws, args, dOut.device)
+
+
+def tp_linear_backward(X, W, dOut, *, pre=None, dX=None, dW=None, dbias=None, act=TP_ACT_NONE,
+                       weight_layout=TP_WEIGHTS_MATH, accumulate=False, ws=None, stream=None, prepare=False):
+    """The gradients of ``tp_linear``: dPre = dOut * act'(pre), dX = dPre W^T,
+    dW (+)= X^T dPre (in W's layout), dbias (+)= the column sums of dPre; the residual's
+    gradient is dOut itself.  Outputs left None are not computed.
+
+    dX and dW are in the inputs' dtype or fp32, dbias fp32; ``accumulate`` adds to
+    fp32 dW and dbias.  ``ws``: from ``tp_linear_backward_ws`` (not needed without an
+    activation and dbias)."""
+    lib = load()
+    M, K = (int(v) for v in X.shape)
+    N = _weight_dims(W, weight_layout)[1]
+    dt, wshape = X.dtype, (N, K) if weight_layout == TP_WEIGHTS_LINEAR else (K, N)
+    args = tp_linear_bwd_args(dtype=_dtype_code(X), act=act, weight_layout=weight_layout,
+                              dx_dtype=_either(dX, "dX", dt), dw_dtype=_either(dW, "dW", dt),
+                              accumulate=1 if accumulate else 0, M=M, N=N, K=K)
+    args.X, args.X_ld = _mat(X, "X")
+    args.W, args.W_ld = _mat(W, "W", wshape, dt)
+    args.dOut, args.dOut_ld = _mat(dOut, "dOut", (M, N), dt)
+    args.pre, args.pre_ld = _mat(pre, "pre", (M, N), dt)
+    args.dX, args.dX_ld = _mat(dX, "dX", (M, K))
+    args.dW, args.dW_ld = _mat(dW, "dW", wshape)
+    _check_bias(dbias, N)
+    args.dbias = _ptr(dbias)
+    args.ws, args.ws_bytes = _ws(ws)
+    return _call(lib.tp_linear_backward, args, stream, prepare, (X, W, dOut, pre, dX, dW, dbias, ws))
+
+
+def tp_gated_linear(X, W_gate, W_up, out, *, gate_out=None, up_out=None, act=TP_ACT_SILU,
+                    weight_layout=TP_WEIGHTS_MATH, stream=None, prepare=False):
+    """out = act(X W_gate) * (X W_up), in one launch; ``gate_out`` and ``up_out`` keep the
+    two products for the backward.
+
+    X [M, K]; W_gate, W_up [K, F] (or [F, K], TP_WEIGHTS_LINEAR), of one row stride (two
+    tensors, or the halves of a merged weight); everything in one dtype."""
+    lib = load()
+    M, K = (int(v) for v in X.shape)
+    F = _weight_dims(W_gate, weight_layout, "W_gate")[1]
+    dt, wshape = X.dtype, (F, K) if weight_layout == TP_WEIGHTS_LINEAR else (K, F)
+    args = tp_gated_args(dtype=_dtype_code(X), act=act, weight_layout=weight_layout, M=M, F=F, K=K)
+    args.X, args.X_ld = _mat(X, "X")
+    args.W_gate, args.W_ld = _mat(W_gate, "W_gate", wshape, dt)
+    args.W_up, ld = _mat(W_up, "W_up", wshape, dt)
+    _same_ld(args.W_ld, ld, wshape, "W_gate and W_up")
+    args.out, args.out_ld = _mat(out, "out", (M, F), dt)
+    args.gate_out, args.keep_ld = _mat(gate_out, "gate_out", (M, F), dt)
+    args.up_out, ld = _mat(up_out, "up_out", (M, F), dt)
+    if gate_out is not None and up_out is not None:
+        _same_ld(args.keep_ld, ld, (M, F), "gate_out and up_out")
+    return _call(lib.tp_gated_linear, args, stream, prepare, (X, W_gate, W_up, out, gate_out, up_out))
+
+
+def _same_ld(a, b, shape, names):
+    if (a or shape[1]) != (b or shape[1]) and shape[0] > 1:
+        raise ValueError(f"{names} must have one row stride")
+
+
+def tp_gated_linear_backward_ws(X, dOut):
+    """A workspace (uint8 tensor) for ``tp_gated_linear_backward`` of these shapes."""
+    args = tp_gated_bwd_args(dtype=_dtype_code(X), M=int(X.shape[0]), F=int(dOut.shape[1]), K=int(X.shape[1]))
+    return _new_ws(load().tp_gated_linear_backward_ws, args, dOut.device)
+
+
+def tp_gated_linear_backward(X, W_gate, W_up, gate, up, dOut, *, dX=None, dW_gate=None, dW_up=None, act=TP_ACT_SILU,
+                             weight_layout=TP_WEIGHTS_MATH, accumulate=False, ws=None, stream=None, prepare=False):
+    """The gradients of ``tp_gated_linear`` from its ``gate_out`` and ``up_out``:
+    dX = dGate W_gate^T + dUp W_up^T, dW_gate (+)= X^T dGate, dW_up (+)= X^T dUp, with
+    dUp = dOut * act(gate) and dGate = dOut * up * act'(gate).  Outputs left None are not
+    computed (the weight gradients come together); types and ``accumulate`` as in
+    ``tp_linear_backward``.  ``ws``: from ``tp_gated_linear_backward_ws``."""
+    lib = load()
+    M, K = (int(v) for v in X.shape)
+    F = _weight_dims(W_gate, weight_layout, "W_gate")[1]
+    dt, wshape = X.dtype, (F, K) if weight_layout == TP_WEIGHTS_LINEAR else (K, F)
+    args = tp_gated_bwd_args(dtype=_dtype_code(X), act=act, weight_layout=weight_layout,
+                             dx_dtype=_either(dX, "dX", dt), dw_dtype=_either(dW_gate, "dW_gate", dt),
+                             accumulate=1 if accumulate else 0, M=M, F=F, K=K)
+    args.X, args.X_ld = _mat(X, "X")
+    args.W_gate, args.W_ld = _mat(W_gate, "W_gate", wshape, dt)
+    args.W_up, ld = _mat(W_up, "W_up", wshape, dt)
+    _same_ld(args.W_ld, ld, wshape, "W_gate and W_up")
+    args.gate, args.keep_ld = _mat(gate, "gate", (M, F), dt)
+    args.up, ld = _mat(up, "up", (M, F), dt)
+    _same_ld(args.keep_ld, ld, (M, F), "gate and up")
+    args.dOut, args.dOut_ld = _mat(dOut, "dOut", (M, F), dt)
+    args.dX, args.dX_ld = _mat(dX, "dX", (M, K))
+    args.dW_gate, args.dW_ld = _mat(dW_gate, "dW_gate", wshape)
+    args.dW_up, ld = _mat(dW_up, "dW_up", wshape, dW_gate.dtype if dW_gate is not None else None)
+    if dW_gate is not None and dW_up is not None:
+        _same_ld(args.dW_ld, ld, wshape, "dW_gate and dW_up")
+    args.ws, args.ws_bytes = _ws(ws)
+    return _call(lib.tp_gated_linear_backward, args, stream, prepare,
+                 (X, W_gate, W_up, gate, up, dOut, dX, dW_gate, dW_up, ws))
+
+
+def tp_grad_parts(ranks=1, device="cuda"):
+    """The fp64 buffer that ``tp_grad_sumsq`` fills (one block of TP_GRAD_PARTS a rank)."""
+    import torch
+    return torch.empty(ranks * TP_GRAD_PARTS, dtype=torch.float64, device=device)
+
+
+def _grad_table(grads, outs):
+    grads = list(grads)
+    outs = [None] * len(grads) if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError("one output per gradient")
+    arr = (tp_grad_tensor * max(1, len(grads)))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if o is not None and (o.dtype != g.dtype or o.numel() != g.numel()):
+            raise ValueError(f"output {i} must have its gradient's dtype and size")
+        arr[i] = tp_grad_tensor(_ptr(g), _ptr(o), g.numel(), _dtype_code(g))
+    return arr, grads, [o for o in outs if o is not None]
+
+
+def _check_parts(parts, ranks):
+    import torch
+    if parts.dtype != torch.float64 or not parts.is_contiguous() or parts.numel() < ranks * TP_GRAD_PARTS:
+        raise ValueError(f"parts must be a contiguous fp64 tensor of at least {ranks * TP_GRAD_PARTS}")
+
+
+def tp_grad_sumsq(grads, parts, *, stream=None, prepare=False):
+    """parts (``tp_grad_parts()``) <- partial sums of the squares of every gradient, in 64
+    bits.  Across ranks, all-reduce ``parts`` (a replicated tensor counted on one rank
+    only) before ``tp_grad_clip``."""
+    lib = load()
+    arr, grads, _ = _grad_table(grads, None)
+    _check_parts(parts, 1)
+    _on_gpu(grads, parts)
+    args = (arr, len(grads), C.c_void_p(parts.data_ptr()))
+    if prepare:
+        return Prepared(lib.tp_grad_sumsq, args, [], [_stream_ptr(stream)], _tensors(grads, parts))
+    _check(lib.tp_grad_sumsq(*args, _stream_ptr(stream)))
+
+
+def tp_grad_clip(grads, outs, parts, *, max_norm, eps=1e-6, norm_out=None, ranks=1, stream=None, prepare=False):
+    """outs[i] = grads[i] * min(1, max_norm / (norm + eps)), norm = sqrt(sum of parts) over
+    ``ranks`` blocks.  ``outs`` None scales in place; ``norm_out`` (fp32 [1]) receives the norm."""
+    import torch
+    lib = load()
+    grads = list(grads)
+    arr, grads, written = _grad_table(grads, grads if outs is None else outs)
+    if len(written) != len(grads):
+        raise ValueError("one output per gradient")
+    _check_parts(parts, ranks)
+    if norm_out is not None and (norm_out.dtype != torch.float32 or norm_out.numel() != 1):
+        raise ValueError("norm_out must be one fp32 value")
+    _on_gpu(grads, written, parts, norm_out)
+    args = (arr, len(grads), C.c_void_p(parts.data_ptr()), int(ranks), float(max_norm), float(eps),
+            C.c_void_p(_ptr(norm_out)))
+    if prepare:
+        return Prepared(lib.tp_grad_clip, args, [], [_stream_ptr(stream)], _tensors(grads, written, parts, norm_out))
+    _check(lib.tp_grad_clip(*args, _stream_ptr(stream)))
 
 
 def tp_timing_enable(on: bool = True):

@@ -1,0 +1,216 @@
+// The global gradient norm over many tensors, and clipping by it.
+//
+//   n = sqrt(sum over ranks, tensors and elements of g^2)
+//   g' = g * min(1, max_norm / (n + eps))
+//
+// Two launches: the first leaves kGradParts partial sums of squares, the second
+// adds every rank's partials (each workgroup for itself: 8 KiB out of L2) and
+// scales.  The squares are summed in 64 bits: they span twice the exponent range
+// of the gradients (fp32 would overflow from 2^64 and lose those under 2^-75),
+// and the vector units add doubles at half the fp32 rate, far above what memory
+// delivers.  Workgroup b takes every kGradParts-th chunk of each tensor in turn,
+// so the order of every sum depends on the sizes alone.
+//
+// The tensors' pointers travel in the kernel's arguments, kMaxTensors a launch:
+// no table in device memory, nothing to copy, and a captured graph keeps them.
+#include "linear_dev.h"
+
+namespace tpshard {
+
+using namespace lin;
+
+namespace {
+
+constexpr int kMaxTensors = 64;
+constexpr int kThreads = 256;
+// Elements of a chunk: 16 per lane.
+constexpr int kPer = 16;
+constexpr int kChunk = kThreads * kPer;
+
+struct Table {
+  const void *g[kMaxTensors];
+  void *out[kMaxTensors];
+  int64_t first[kMaxTensors + 1];   // chunks before tensor i
+  int64_t n[kMaxTensors];
+  uint64_t f32;                     // bit i: tensor i holds fp32
+  int32_t num;
+};
+static_assert(sizeof(Table) < 3500, "kernel arguments");
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sum over the workgroup, in every lane.
+__device__ __forceinline__ double block_sum(double v, double *lds) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = lds[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) t += lds[w];
+  __syncthreads();
+  return t;
+}
+
+// The tensor that chunk `u` belongs to, from `i` on (chunks come in order).
+__device__ __forceinline__ int tensor_of(const Table& t, int64_t u, int i) {
+  while (u >= t.first[i + 1]) ++i;
+  return i;
+}
+
+__device__ __forceinline__ double sq(float v) { return static_cast<double>(v) * static_cast<double>(v); }
+
+__global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(Table t, double *parts, int add) {
+  __shared__ double lds[kThreads / 64];
+  double s0 = 0.0, s1 = 0.0;
+  int i = 0;
+  for (int64_t u = blockIdx.x; u < t.first[t.num]; u += kGradParts) {
+    i = tensor_of(t, u, i);
+    const int64_t at = (u - t.first[i]) * kChunk, left = t.n[i] - at;
+    if (t.f32 >> i & 1) {
+      const uint32_t *g = static_cast<const uint32_t *>(t.g[i]) + at;
+      if (left >= kChunk) {
+        u32x4 v[kPer / 4];
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q)
+          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 4);
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+          s0 += sq(__uint_as_float(v[q][0])) + sq(__uint_as_float(v[q][1]));
+          s1 += sq(__uint_as_float(v[q][2])) + sq(__uint_as_float(v[q][3]));
+        }
+      } else {
+        for (int64_t e = threadIdx.x; e < left; e += kThreads) s0 += sq(__uint_as_float(g[e]));
+      }
+    } else {
+      const uint16_t *g = static_cast<const uint16_t *>(t.g[i]) + at;
+      if (left >= kChunk) {
+        u32x4 v[kPer / 8];
+#pragma unroll
+        for (int q = 0; q < kPer / 8; ++q)
+          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 8);
+#pragma unroll
+        for (int q = 0; q < kPer / 8; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s0 += sq(from_bf16(v[q][e] & 0xffffu));
+            s1 += sq(from_bf16(v[q][e] >> 16));
+          }
+      } else {
+        for (int64_t e = threadIdx.x; e < left; e += kThreads) s0 += sq(from_bf16(g[e]));
+      }
+    }
+  }
+  const double s = block_sum(s0 + s1, lds);
+  if (threadIdx.x == 0) parts[blockIdx.x] = add ? parts[blockIdx.x] + s : s;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_clip_kernel(Table t, const double *parts, int64_t ranks,
+                                                             double max_norm, double eps, float *norm_out) {
+  __shared__ double lds[kThreads / 64];
+  double s = 0.0;
+  for (int64_t q = threadIdx.x; q < ranks * kGradParts; q += kThreads) s += parts[q];
+  const double norm = sqrt(block_sum(s, lds));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
+  // A NaN norm makes a NaN scale; an infinite one a scale of zero.
+  const double want = max_norm / (norm + eps);
+  const float scale = want >= 1.0 ? 1.0f : static_cast<float>(want);
+  int i = 0;
+  for (int64_t u = blockIdx.x; u < t.first[t.num]; u += gridDim.x) {
+    i = tensor_of(t, u, i);
+    // Nothing below its limit changes where it lies.
+    if (scale == 1.0f && t.out[i] == t.g[i]) continue;
+    const int64_t at = (u - t.first[i]) * kChunk, left = t.n[i] - at;
+    if (t.f32 >> i & 1) {
+      const uint32_t *g = static_cast<const uint32_t *>(t.g[i]) + at;
+      uint32_t *o = static_cast<uint32_t *>(t.out[i]) + at;
+      if (left >= kChunk) {
+        u32x4 v[kPer / 4];
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q)
+          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 4);
+#pragma unroll
+        for (int q = 0; q < kPer / 4; ++q) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[q][e] = __float_as_uint(__uint_as_float(v[q][e]) * scale);
+          *reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 4) = v[q];
+        }
+      } else {
+        for (int64_t e = threadIdx.x; e < left; e += kThreads) o[e] = __float_as_uint(__uint_as_float(g[e]) * scale);
+      }
+    } else {
+      const uint16_t *g = static_cast<const uint16_t *>(t.g[i]) + at;
+      uint16_t *o = static_cast<uint16_t *>(t.out[i]) + at;
+      if (left >= kChunk) {
+        u32x4 v[kPer / 8];
+#pragma unroll
+        for (int q = 0; q < kPer / 8; ++q)
+          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 8);
+#pragma unroll
+        for (int q = 0; q < kPer / 8; ++q) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[q][e] = pack2(from_bf16(v[q][e] & 0xffffu) * scale, from_bf16(v[q][e] >> 16) * scale);
+          *reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 8) = v[q];
+        }
+      } else {
+        for (int64_t e = threadIdx.x; e < left; e += kThreads) o[e] = to_bf16(from_bf16(g[e]) * scale);
+      }
+    }
+  }
+}
+
+// The next tensors that hold anything, from *at on, as one launch's table.
+void next_table(const GradTensor *ts, int64_t num, int64_t *at, Table *t) {
+  t->num = 0;
+  t->f32 = 0;
+  t->first[0] = 0;
+  for (; *at < num && t->num < kMaxTensors; ++*at) {
+    const GradTensor& x = ts[*at];
+    if (x.n <= 0) continue;
+    const int i = t->num++;
+    t->g[i] = x.g;
+    t->out[i] = x.out;
+    t->n[i] = x.n;
+    t->first[i + 1] = t->first[i] + (x.n + kChunk - 1) / kChunk;
+    if (x.f32) t->f32 |= uint64_t{1} << i;
+  }
+}
+
+}  // namespace
+
+hipError_t grad_sumsq_launch(const GradTensor *ts, int64_t num, double *parts, hipStream_t s) {
+  int64_t at = 0;
+  int add = 0;
+  do {   // at least once: the partials are written even where there is nothing to add
+    Table t;
+    next_table(ts, num, &at, &t);
+    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(kGradParts), dim3(kThreads), 0, s, t, parts, add);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    add = 1;
+  } while (at < num);
+  return hipSuccess;
+}
+
+hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *parts, int64_t ranks, double max_norm,
+                            double eps, float *norm_out, hipStream_t s) {
+  int64_t at = 0;
+  do {
+    Table t;
+    next_table(ts, num, &at, &t);
+    const int64_t chunks = t.first[t.num];
+    const int64_t grid = chunks < 1 ? 1 : chunks < 2048 ? chunks : 2048;
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, t, parts, ranks,
+                       max_norm, eps, norm_out);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    norm_out = nullptr;
+  } while (at < num);
+  return hipSuccess;
+}
+
+}  // namespace tpshard

@@ -1,0 +1,84 @@
+// Launch interface of the linear layer, the gated block, their backward passes
+// and the gradient norm (linear_api.cpp validates and schedules; the kernels
+// trust what reaches them).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace tpshard {
+
+// What a product's two weight operands mean.
+enum {
+  kModeOne = 0,   // c = epi(A W)
+  kModeDual = 1,  // gated: G = A W, U = A W2, c = act(G) * U; aux, aux2 keep G, U
+  kModeCat = 2,   // c = A W + A2 W2 (one accumulator over both)
+  kModePair = 3,  // c = A W and c2 = A2 W2, two products of one shape in one launch
+};
+
+// C[M,N] = epi(A[M,K] W[K,N]), strides in elements.  As in GemmArgs, a_t: A is
+// stored [K][lda]; w_t: W is stored [N][ldw].  The second operands share the
+// first ones' shape and stride.  Epilogue, on the fp32 accumulator (kModeOne):
+//   pre = acc + bias[n];  aux <- pre;  c <- act(pre) + res
+// aux, res in the operands' type; c in it too, or fp32 (c_f32).  acc_c: c is
+// added to (fp32 c).  Every optional pointer may be null.
+struct LinGemm {
+  const void *a = nullptr, *a2 = nullptr;
+  const void *w = nullptr, *w2 = nullptr;
+  void *c = nullptr, *c2 = nullptr;
+  int64_t M = 0, N = 0, K = 0;
+  int64_t lda = 0, ldw = 0, ldc = 0;
+  const float *bias = nullptr;
+  const void *res = nullptr;
+  int64_t ldres = 0;
+  void *aux = nullptr, *aux2 = nullptr;
+  int64_t ldaux = 0;
+  int32_t a_t = 0, w_t = 0;
+  int32_t mode = kModeOne;
+  int32_t f32 = 0;      // operands are fp32 (else bf16)
+  int32_t act = 0;      // TP_ACT_*
+  int32_t c_f32 = 0;    // c holds fp32 (always with f32)
+  int32_t acc_c = 0;
+  int32_t vec = 0;      // set by the launcher: four columns at a time are aligned
+};
+
+// Whether the grids of the kernels below reach every tile of [M, N].
+bool lin_grid_ok(int64_t M, int64_t N);
+
+// Enqueues the product.
+hipError_t lin_gemm_launch(LinGemm p, hipStream_t s);
+
+// The general kernel: any layout, alignment and size.
+hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s);
+
+// ---- gradients at the activation -----------------------------------------
+// kLinear: d_pre = d_out * act'(pre) (pre NULL: d_pre = d_out, not written) and,
+// with colsum, the column sums of the unrounded d_pre.
+// kGated : d_up = d_out * act(gate), d_gate = d_out * up * act'(gate).
+struct ActGrad {
+  const void *d_out = nullptr, *pre = nullptr, *up = nullptr;
+  void *d_pre = nullptr, *d_up = nullptr;   // contiguous [M, N]
+  int64_t M = 0, N = 0, ld_dout = 0, ld_pre = 0;
+  float *parts = nullptr;                   // [slabs][N], or null
+  float *colsum = nullptr;                  // [N]
+  int32_t f32 = 0, act = 0, gated = 0, accumulate = 0;
+};
+int64_t act_grad_slabs(int64_t M, int64_t N);   // rows of `parts`
+hipError_t act_grad_launch(const ActGrad& p, hipStream_t s);
+
+// ---- gradient norm and clipping --------------------------------------------
+constexpr int kGradParts = 1024;   // partial sums of squares of one call
+
+struct GradTensor {
+  const void *g;
+  void *out;
+  int64_t n;
+  int32_t f32;
+};
+hipError_t grad_sumsq_launch(const GradTensor *ts, int64_t num, double *parts, hipStream_t s);
+// parts: `ranks` blocks of kGradParts.
+hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *parts, int64_t ranks, double max_norm,
+                            double eps, float *norm_out, hipStream_t s);
+
+}  // namespace tpshard
