@@ -52,6 +52,10 @@ hipError_t lin_gemm_launch(LinGemm p, hipStream_t s);
 // The general kernel: any layout, alignment and size.
 hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s);
 
+// The kernel for few rows, where lin_rows_ok.
+bool lin_rows_ok(const LinGemm& p);
+hipError_t lin_rows_launch(const LinGemm& p, hipStream_t s);
+
 // ---- gradients at the activation -----------------------------------------
 // kLinear: d_pre = d_out * act'(pre) (pre NULL: d_pre = d_out, not written) and,
 // with colsum, the column sums of the unrounded d_pre.

@@ -313,6 +313,7 @@ hipError_t lin_gemm_launch(LinGemm p, hipStream_t s) {
   const int64_t es = p.f32 ? 4 : 2, ces = p.c_f32 ? 4 : 2;
   p.vec = vec4(p.c, p.ldc, ces) && vec4(p.c2, p.ldc, ces) && vec4(p.res, p.ldres, es) && vec4(p.aux, p.ldaux, es) &&
           vec4(p.aux2, p.ldaux, es) && vec4(p.bias, 4, 4);
+  if (lin_rows_ok(p)) return lin_rows_launch(p, s);
   return lin_staged_launch(p, s);
 }
 
