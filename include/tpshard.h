@@ -555,12 +555,21 @@ typedef struct {
   int64_t out_ld;
   void *pre_out;         /* optional [M, N]: X W + bias rounded to dtype, kept for the backward */
   int64_t pre_ld;
+  void *ws;              /* optional, tp_linear_ws bytes: lets few rows (a decode step) split K
+                            over the whole chip.  16-byte aligned, zero before its first use;
+                            every call leaves it fit for the next.  Calls that may overlap
+                            need one each.  NULL or smaller: one workgroup a tile */
+  int64_t ws_bytes;
 } tp_linear_args;
+
+/* Bytes of workspace that the call can use (0: none).  Reads dtype, weight_layout
+ * and the sizes.  Host only. */
+int tp_linear_ws(const tp_linear_args *args, int64_t *bytes);
 
 /*
  * out = act(X W + bias) + residual, in one launch; the value is rounded once, when
  * it is stored.  Rows are independent: a row's result does not depend on the
- * other rows' values.  Capturable into a HIP graph.
+ * other rows' values.  Deterministic.  Capturable into a HIP graph.
  * Errors: TP_ERR_ARG (NULL or overlapping buffers, unknown dtype / act / layout,
  *         bad sizes or strides), TP_ERR_UNSUPPORTED (sizes beyond the kernels'
  *         32-bit indexes or the grid), TP_ERR_HIP.
@@ -620,7 +629,11 @@ typedef struct {
   void *gate_out;        /* optional [M, F]: X W_gate and X W_up, rounded, kept for the */
   void *up_out;          /* backward (both or neither) */
   int64_t keep_ld;       /* of both */
+  void *ws;              /* optional, tp_gated_linear_ws bytes, as in tp_linear_args */
+  int64_t ws_bytes;
 } tp_gated_args;
+
+int tp_gated_linear_ws(const tp_gated_args *args, int64_t *bytes);
 
 /*
  * out = act(X W_gate) * (X W_up): both projections, the activation and the

@@ -42,8 +42,8 @@ TP_REDUCE_OP_MIN = 2
 # Every symbol include/tpshard.h declares.
 EXPORTS = ("tp_last_error", "tp_version", "tp_layout_plan", "tp_check_broadcast_binary", "tp_infer_matmul_dims_mapping", "tp_shard_materialize", "tp_shard_materialize_batch", "tp_shard_gather",
            "tp_partial_reduce", "tp_partial_reduce_ex", "tp_colrow_mlp", "tp_colrow_mlp_noalloc", "tp_colrow_mlp_stack", "tp_colrow_mlp_backward",
-           "tp_linear", "tp_linear_backward_ws", "tp_linear_backward", "tp_gated_linear", "tp_gated_linear_backward_ws",
-           "tp_gated_linear_backward", "tp_grad_sumsq", "tp_grad_clip", "tp_timing_enable", "tp_timing_read")
+           "tp_linear", "tp_linear_ws", "tp_linear_backward_ws", "tp_linear_backward", "tp_gated_linear", "tp_gated_linear_ws",
+           "tp_gated_linear_backward_ws", "tp_gated_linear_backward", "tp_grad_sumsq", "tp_grad_clip", "tp_timing_enable", "tp_timing_read")
 
 TP_KERNEL_NAMES = ("materialize", "gemm1", "gemm2", "reduce", "gemm_dgrad", "gemm_wgrad", "gather", "gemm2_reduce",
                    "gemm_dgrad_reduce", "reduce_tail")
@@ -129,7 +129,8 @@ class tp_linear_args(C.Structure):
                 ("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64),
                 ("X", C.c_void_p), ("X_ld", C.c_int64), ("W", C.c_void_p), ("W_ld", C.c_int64),
                 ("bias", C.c_void_p), ("residual", C.c_void_p), ("residual_ld", C.c_int64),
-                ("out", C.c_void_p), ("out_ld", C.c_int64), ("pre_out", C.c_void_p), ("pre_ld", C.c_int64)]
+                ("out", C.c_void_p), ("out_ld", C.c_int64), ("pre_out", C.c_void_p), ("pre_ld", C.c_int64),
+                ("ws", C.c_void_p), ("ws_bytes", C.c_int64)]
 
 
 class tp_linear_bwd_args(C.Structure):
@@ -147,7 +148,8 @@ class tp_gated_args(C.Structure):
                 ("M", C.c_int64), ("F", C.c_int64), ("K", C.c_int64),
                 ("X", C.c_void_p), ("X_ld", C.c_int64), ("W_gate", C.c_void_p), ("W_up", C.c_void_p),
                 ("W_ld", C.c_int64), ("out", C.c_void_p), ("out_ld", C.c_int64),
-                ("gate_out", C.c_void_p), ("up_out", C.c_void_p), ("keep_ld", C.c_int64)]
+                ("gate_out", C.c_void_p), ("up_out", C.c_void_p), ("keep_ld", C.c_int64),
+                ("ws", C.c_void_p), ("ws_bytes", C.c_int64)]
 
 
 class tp_gated_bwd_args(C.Structure):
@@ -222,7 +224,8 @@ def load(path: str = LIB_PATH) -> C.CDLL:
                          ("tp_gated_linear", tp_gated_args), ("tp_gated_linear_backward", tp_gated_bwd_args)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = C.c_int, [C.POINTER(struct), C.c_void_p]
-    for name, struct in (("tp_linear_backward_ws", tp_linear_bwd_args),
+    for name, struct in (("tp_linear_ws", tp_linear_args), ("tp_gated_linear_ws", tp_gated_args),
+                         ("tp_linear_backward_ws", tp_linear_bwd_args),
                          ("tp_gated_linear_backward_ws", tp_gated_bwd_args)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = C.c_int, [C.POINTER(struct), i64p]
@@ -778,11 +781,28 @@ def _ws(ws):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _new_ws(fn, args, device):
-    import torch
+def _ws_bytes(fn, args):
     n = C.c_int64()
     _check(fn(C.byref(args), C.byref(n)))
-    return torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
+    return n.value
+
+
+def _new_ws(fn, args, device):
+    import torch
+    return torch.empty(max(16, _ws_bytes(fn, args)), dtype=torch.uint8, device=device)
+
+
+def _forward_ws(fn, args, ws, device, stream, prepare):
+    """The zeroed workspace of a forward call: the caller's, or a prepared call's own."""
+    import torch
+    if ws is None and prepare and torch.device(device).type == "cuda":
+        n = _ws_bytes(fn, args)
+        if n:
+            ws = torch.zeros(n, dtype=torch.uint8, device=device)
+            if _stream_ptr(stream).value != _stream_ptr(None).value:
+                torch.cuda.current_stream().synchronize()   # zeroed before another stream uses it
+    args.ws, args.ws_bytes = _ws(ws)
+    return ws
 
 
 def _call(fn, args, stream, prepare, tensors):
@@ -793,15 +813,26 @@ def _call(fn, args, stream, prepare, tensors):
     _check(fn(C.byref(args), _stream_ptr(stream)))
 
 
+def tp_linear_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH):
+    """A zeroed workspace (uint8 tensor, maybe empty) for ``tp_linear`` of these shapes: with it
+    a few rows' product (M <= 64) is split over the whole chip.  It serves any number of calls
+    of the shapes, one after another."""
+    import torch
+    args = tp_linear_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
+                          N=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]))
+    return torch.zeros(_ws_bytes(load().tp_linear_ws, args), dtype=torch.uint8, device=X.device)
+
+
 def tp_linear(X, W, out, *, bias=None, residual=None, pre_out=None, act=TP_ACT_NONE, weight_layout=TP_WEIGHTS_MATH,
-              stream=None, prepare=False):
+              ws=None, stream=None, prepare=False):
     """out = act(X W + bias) + residual, in one launch; ``pre_out`` keeps X W + bias
     for the backward.
 
     X [M, K], W [K, N] (or [N, K], TP_WEIGHTS_LINEAR) and residual share a dtype (bf16
     or fp32); out is in it, or fp32, and may be the residual itself; bias is fp32
-    [N].  Rows may be strided (a weight may be a column slice of a full one).  With
-    ``prepare=True`` nothing runs; a ``Prepared`` call taking the stream is returned."""
+    [N].  Rows may be strided (a weight may be a column slice of a full one).  ``ws``: from
+    ``tp_linear_ws``, optional.  With ``prepare=True`` nothing runs; a ``Prepared`` call
+    taking the stream is returned (with a workspace of its own if none is given)."""
     lib = load()
     M, K = (int(v) for v in X.shape)
     N = _weight_dims(W, weight_layout)[1]
@@ -815,7 +846,8 @@ def tp_linear(X, W, out, *, bias=None, residual=None, pre_out=None, act=TP_ACT_N
     args.pre_out, args.pre_ld = _mat(pre_out, "pre_out", (M, N), dt)
     _check_bias(bias, N)
     args.bias = _ptr(bias)
-    return _call(lib.tp_linear, args, stream, prepare, (X, W, out, bias, residual, pre_out))
+    ws = _forward_ws(lib.tp_linear_ws, args, ws, X.device, stream, prepare)
+    return _call(lib.tp_linear, args, stream, prepare, (X, W, out, bias, residual, pre_out, ws))
 
 
 def tp_linear_backward_ws(X, W, dOut, *, act=TP_ACT_NONE, weight_layout=TP_WEIGHTS_MATH, dbias=None):
@@ -853,13 +885,22 @@ def tp_linear_backward(X, W, dOut, *, pre=None, dX=None, dW=None, dbias=None, ac
     return _call(lib.tp_linear_backward, args, stream, prepare, (X, W, dOut, pre, dX, dW, dbias, ws))
 
 
+def tp_gated_linear_ws(X, W_gate, *, weight_layout=TP_WEIGHTS_MATH):
+    """A zeroed workspace for ``tp_gated_linear``, as ``tp_linear_ws``."""
+    import torch
+    args = tp_gated_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
+                         F=_weight_dims(W_gate, weight_layout)[1], K=int(X.shape[1]))
+    return torch.zeros(_ws_bytes(load().tp_gated_linear_ws, args), dtype=torch.uint8, device=X.device)
+
+
 def tp_gated_linear(X, W_gate, W_up, out, *, gate_out=None, up_out=None, act=TP_ACT_SILU,
-                    weight_layout=TP_WEIGHTS_MATH, stream=None, prepare=False):
+                    weight_layout=TP_WEIGHTS_MATH, ws=None, stream=None, prepare=False):
     """out = act(X W_gate) * (X W_up), in one launch; ``gate_out`` and ``up_out`` keep the
     two products for the backward.
 
     X [M, K]; W_gate, W_up [K, F] (or [F, K], TP_WEIGHTS_LINEAR), of one row stride (two
-    tensors, or the halves of a merged weight); everything in one dtype."""
+    tensors, or the halves of a merged weight); everything in one dtype.  ``ws``: from
+    ``tp_gated_linear_ws``, optional."""
     lib = load()
     M, K = (int(v) for v in X.shape)
     F = _weight_dims(W_gate, weight_layout, "W_gate")[1]
@@ -874,7 +915,8 @@ def tp_gated_linear(X, W_gate, W_up, out, *, gate_out=None, up_out=None, act=TP_
     args.up_out, ld = _mat(up_out, "up_out", (M, F), dt)
     if gate_out is not None and up_out is not None:
         _same_ld(args.keep_ld, ld, (M, F), "gate_out and up_out")
-    return _call(lib.tp_gated_linear, args, stream, prepare, (X, W_gate, W_up, out, gate_out, up_out))
+    ws = _forward_ws(lib.tp_gated_linear_ws, args, ws, X.device, stream, prepare)
+    return _call(lib.tp_gated_linear, args, stream, prepare, (X, W_gate, W_up, out, gate_out, up_out, ws))
 
 
 def _same_ld(a, b, shape, names):

@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["plan.cpp", "checker.cpp", "api.cpp", "timing.cpp", "shard.hip", "reduce.hip", "gemm.hip", "noalloc.hip",
-           "linear_api.cpp", "linear_staged.hip", "linear_rows.hip", "act_grad.hip", "grad_clip.hip"]
+           "linear_api.cpp", "linear_launch.cpp", "linear_staged.hip", "linear_rows.hip", "linear_one.hip",
+           "linear_dual.hip", "linear_cat.hip", "linear_pair.hip", "act_grad.hip", "grad_clip.hip"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result",

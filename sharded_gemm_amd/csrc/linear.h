@@ -41,20 +41,35 @@ struct LinGemm {
   int32_t c_f32 = 0;    // c holds fp32 (always with f32)
   int32_t acc_c = 0;
   int32_t vec = 0;      // set by the launcher: four columns at a time are aligned
+  // Few rows, several workgroups a tile: their partials and arrival counts.
+  float *join = nullptr;
+  uint32_t *tickets = nullptr;
 };
 
 // Whether the grids of the kernels below reach every tile of [M, N].
 bool lin_grid_ok(int64_t M, int64_t N);
 
-// Enqueues the product.
-hipError_t lin_gemm_launch(LinGemm p, hipStream_t s);
+// Enqueues the product.  ws: lin_rows_ws bytes of zeros (or null); left zeroed
+// where it has to be.
+hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws = nullptr, int64_t ws_bytes = 0);
 
 // The general kernel: any layout, alignment and size.
 hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s);
 
-// The kernel for few rows, where lin_rows_ok.
+// The tiled bf16 kernels, where lin_tiles_ok: 16-byte aligned operands and rows,
+// K a multiple of 32, a row-contiguous operand of whole 8-column groups.
+bool lin_tiles_ok(const LinGemm& p);
+hipError_t lin_tiles_launch(const LinGemm& p, hipStream_t s);
+hipError_t lin_tiles_one(const LinGemm& p, hipStream_t s);
+hipError_t lin_tiles_dual(const LinGemm& p, hipStream_t s);
+hipError_t lin_tiles_cat(const LinGemm& p, hipStream_t s);
+hipError_t lin_tiles_pair(const LinGemm& p, hipStream_t s);
+
+// The kernel for few rows, where lin_rows_ok.  Given lin_rows_ws bytes of
+// workspace, several workgroups may split a tile's K.
 bool lin_rows_ok(const LinGemm& p);
-hipError_t lin_rows_launch(const LinGemm& p, hipStream_t s);
+int64_t lin_rows_ws(const LinGemm& p);
+hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s);
 
 // ---- gradients at the activation -----------------------------------------
 // kLinear: d_pre = d_out * act'(pre) (pre NULL: d_pre = d_out, not written) and,

@@ -92,9 +92,18 @@ int check_ws(const void *ws, int64_t have, int64_t need) {
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-int launch(const LinGemm& p, hipStream_t s, int kind, double flops, const char *what) {
+// An optional workspace: given at all, it has to be aligned and apart.
+int take_ws(Mat *m, void *ws, int64_t bytes) {
+  if (!ws || bytes <= 0) return TP_OK;
+  if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(TP_ERR_ARG, "ws is not 16-byte aligned");
+  *m = Mat{ws, 1, bytes, bytes, 1, "ws"};
+  return TP_OK;
+}
+
+int launch(const LinGemm& p, hipStream_t s, int kind, double flops, const char *what, void *ws = nullptr,
+           int64_t ws_bytes = 0) {
   hipEvent_t t0 = timing_begin(s);
-  const hipError_t e = lin_gemm_launch(p, s);
+  const hipError_t e = lin_gemm_launch(p, s, ws, ws_bytes);
   if (e != hipSuccess) return hip_fail(e, what);
   timing_end(t0, s, kind, flops);
   return TP_OK;
@@ -120,6 +129,37 @@ using namespace tpshard;
 
 extern "C" {
 
+int tp_linear_ws(const tp_linear_args *a, int64_t *bytes) {
+  clear_error();
+  if (!a || !bytes) return fail(TP_ERR_ARG, "args or bytes is NULL");
+  const int rc = check_common(a->dtype, a->act, a->weight_layout, a->M, a->N, a->K, "N");
+  if (rc != TP_OK) return rc;
+  LinGemm p;
+  p.M = a->M;
+  p.N = a->N;
+  p.K = a->K;
+  p.w_t = a->weight_layout == TP_WEIGHTS_LINEAR;
+  p.f32 = a->dtype == TP_F32;
+  *bytes = lin_rows_ws(p);
+  return TP_OK;
+}
+
+int tp_gated_linear_ws(const tp_gated_args *a, int64_t *bytes) {
+  clear_error();
+  if (!a || !bytes) return fail(TP_ERR_ARG, "args or bytes is NULL");
+  const int rc = check_common(a->dtype, a->act, a->weight_layout, a->M, a->F, a->K, "F");
+  if (rc != TP_OK) return rc;
+  LinGemm p;
+  p.mode = kModeDual;
+  p.M = a->M;
+  p.N = a->F;
+  p.K = a->K;
+  p.w_t = a->weight_layout == TP_WEIGHTS_LINEAR;
+  p.f32 = a->dtype == TP_F32;
+  *bytes = lin_rows_ws(p);
+  return TP_OK;
+}
+
 int tp_linear(const tp_linear_args *a, tp_stream_t stream) {
   clear_error();
   if (!a) return fail(TP_ERR_ARG, "args is NULL");
@@ -128,19 +168,20 @@ int tp_linear(const tp_linear_args *a, tp_stream_t stream) {
   if (rc != TP_OK) return rc;
   const int64_t M = a->M, N = a->N, K = a->K, es = dtype_size(a->dtype), oes = dtype_size(a->out_dtype);
   const bool linear = a->weight_layout == TP_WEIGHTS_LINEAR, any = M > 0;
-  Mat x, w, b, r, o, pre;
+  Mat x, w, b, r, o, pre, wsm;
   if ((rc = take(&x, "X", a->X, M, K, a->X_ld, es, any)) != TP_OK ||
       (rc = take(&w, "W", a->W, linear ? N : K, linear ? K : N, a->W_ld, es, any)) != TP_OK ||
       (rc = take(&b, "bias", a->bias, 1, N, 0, 4, false)) != TP_OK ||
       (rc = take(&r, "residual", a->residual, M, N, a->residual_ld, es, false)) != TP_OK ||
       (rc = take(&o, "out", a->out, M, N, a->out_ld, oes, any)) != TP_OK ||
-      (rc = take(&pre, "pre_out", a->pre_out, M, N, a->pre_ld, es, false)) != TP_OK)
+      (rc = take(&pre, "pre_out", a->pre_out, M, N, a->pre_ld, es, false)) != TP_OK ||
+      (rc = take_ws(&wsm, a->ws, a->ws_bytes)) != TP_OK)
     return rc;
   // Each output element is written by the lane that read the residual's.
   const bool in_place = r.p && r.p == o.p && r.ld == o.ld && es == oes;
   std::vector<Mat> ins = {x, w, b};
   if (!in_place) ins.push_back(r);
-  if ((rc = disjoint(ins, {o, pre})) != TP_OK) return rc;
+  if ((rc = disjoint(ins, {o, pre, wsm})) != TP_OK) return rc;
   if (in_place && (rc = disjoint({r}, {pre})) != TP_OK) return rc;
   if (!any) return TP_OK;
   LinGemm p;
@@ -162,7 +203,8 @@ int tp_linear(const tp_linear_args *a, tp_stream_t stream) {
   p.act = a->act;
   p.f32 = a->dtype == TP_F32;
   p.c_f32 = a->out_dtype == TP_F32;
-  return launch(p, static_cast<hipStream_t>(stream), TP_KERNEL_GEMM1, 2.0 * M * N * K, "linear launch");
+  return launch(p, static_cast<hipStream_t>(stream), TP_KERNEL_GEMM1, 2.0 * M * N * K, "linear launch", a->ws,
+                a->ws_bytes);
 }
 
 int tp_linear_backward_ws(const tp_linear_bwd_args *a, int64_t *bytes) {
@@ -272,16 +314,17 @@ int tp_gated_linear(const tp_gated_args *a, tp_stream_t stream) {
   const int64_t M = a->M, F = a->F, K = a->K, es = dtype_size(a->dtype);
   const bool linear = a->weight_layout == TP_WEIGHTS_LINEAR, any = M > 0;
   const int64_t wr = linear ? F : K, wc = linear ? K : F;
-  Mat x, wg, wu, o, g, u;
+  Mat x, wg, wu, o, g, u, wsm;
   if ((rc = take(&x, "X", a->X, M, K, a->X_ld, es, any)) != TP_OK ||
       (rc = take(&wg, "W_gate", a->W_gate, wr, wc, a->W_ld, es, any)) != TP_OK ||
       (rc = take(&wu, "W_up", a->W_up, wr, wc, a->W_ld, es, any)) != TP_OK ||
       (rc = take(&o, "out", a->out, M, F, a->out_ld, es, any)) != TP_OK ||
       (rc = take(&g, "gate_out", a->gate_out, M, F, a->keep_ld, es, false)) != TP_OK ||
-      (rc = take(&u, "up_out", a->up_out, M, F, a->keep_ld, es, false)) != TP_OK)
+      (rc = take(&u, "up_out", a->up_out, M, F, a->keep_ld, es, false)) != TP_OK ||
+      (rc = take_ws(&wsm, a->ws, a->ws_bytes)) != TP_OK)
     return rc;
   if (!g.p != !u.p) return fail(TP_ERR_ARG, "gate_out and up_out: both or neither");
-  if ((rc = disjoint({x, wg, wu}, {o, g, u})) != TP_OK) return rc;
+  if ((rc = disjoint({x, wg, wu}, {o, g, u, wsm})) != TP_OK) return rc;
   if (!any) return TP_OK;
   LinGemm p;
   p.mode = kModeDual;
@@ -301,7 +344,8 @@ int tp_gated_linear(const tp_gated_args *a, tp_stream_t stream) {
   p.ldaux = g.ld;
   p.act = a->act;
   p.f32 = p.c_f32 = a->dtype == TP_F32;
-  return launch(p, static_cast<hipStream_t>(stream), TP_KERNEL_GEMM1, 4.0 * M * F * K, "gated linear launch");
+  return launch(p, static_cast<hipStream_t>(stream), TP_KERNEL_GEMM1, 4.0 * M * F * K, "gated linear launch",
+                a->ws, a->ws_bytes);
 }
 
 int tp_gated_linear_backward_ws(const tp_gated_bwd_args *a, int64_t *bytes) {

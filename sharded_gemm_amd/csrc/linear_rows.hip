@@ -112,9 +112,11 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TC;
   const T *X = static_cast<const T *>(p.a);
 
-  // This wave's steps [s0, s1) of K's, and whether it ends with K's ragged one.
+  // This wave's steps [s0, s1) of K's (the workgroups of one tile split them
+  // first), and whether it ends with K's ragged one.
   const int64_t steps = (p.K + STEP - 1) / STEP;
-  const int64_t s0 = steps * wave / waves, s1 = steps * (wave + 1) / waves;
+  const int64_t part = static_cast<int64_t>(blockIdx.y) * waves + wave, parts = static_cast<int64_t>(gridDim.y) * waves;
+  const int64_t s0 = steps * part / parts, s1 = steps * (part + 1) / parts;
   const int64_t s1_full = (s1 == steps && p.K % STEP) ? s1 - 1 : s1;
 
   const T *xp[MT];
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) x[i][t] = load16<T>(xp[t] + k, rest);
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) x[i][t] = load16<T>(xp[t] + k, checked ? rest : PER);
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -247,6 +251,40 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
     }
   }
   __syncthreads();
+  // Sum of cell i over the waves.
+  auto joined = [&](int i) {
+    float v = red[i];
+    for (int w = 1; w < waves; ++w) v += red[w * MATS * M * TC + i];
+    return v;
+  };
+  const int cells = MATS * M * TC, splits = gridDim.y;
+  const float *from = nullptr;                  // the tile's partials, once all are there
+  if (splits > 1) {
+    // Every workgroup of the tile leaves its partial; the one that finds all
+    // the others' done adds them, in their order, so the sum does not depend
+    // on who that is.  Nobody waits for anybody, and the ticket ends at zero
+    // again.  The partials are device-scope accesses: such a store is past this
+    // XCD's own L2 once vmcnt has counted it, and such a load does not read a
+    // stale line there, so no cache is written back or invalidated (a device
+    // fence writes the whole L2 back: with one per wave the 4096 -> 14336 gated
+    // product took 531 us instead of 51).
+    float *mine = p.join + (static_cast<int64_t>(blockIdx.x) * splits + blockIdx.y) * cells;
+    for (int i = threadIdx.x; i < cells; i += blockDim.x)
+      __hip_atomic_store(mine + i, joined(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    __shared__ uint32_t before;
+    if (threadIdx.x == 0)
+      before = __hip_atomic_fetch_add(p.tickets + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before + 1 != static_cast<uint32_t>(splits)) return;
+    if (threadIdx.x == 0)
+      __hip_atomic_store(p.tickets + blockIdx.x, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    from = p.join + static_cast<int64_t>(blockIdx.x) * splits * cells;
+  }
+  auto partial = [&](int y, int cell) {
+    return __hip_atomic_load(from + static_cast<int64_t>(y) * cells + cell, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
   with_act(p.act, [&](auto A) {
     constexpr int ACT = decltype(A)::value;
     for (int i = threadIdx.x; i < M * TC; i += blockDim.x) {
@@ -256,8 +294,13 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
       float v[MATS];
 #pragma unroll
       for (int a = 0; a < MATS; ++a) {
-        v[a] = red[a * M * TC + i];
-        for (int w = 1; w < waves; ++w) v[a] += red[(w * MATS + a) * M * TC + i];
+        const int cell = a * M * TC + i;
+        if (from) {
+          v[a] = partial(0, cell);
+          for (int y = 1; y < splits; ++y) v[a] += partial(y, cell);
+        } else {
+          v[a] = joined(cell);
+        }
       }
       auto put = [&](void *base, int64_t at, float y, bool f32) {
         if (f32) static_cast<float *>(base)[at] = y;
@@ -279,30 +322,46 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
   });
 }
 
-// Waves of a workgroup: enough that each still has `least` steps, and that the
-// join fits 64 KiB of LDS.
-template <typename T, bool WKC, bool DUAL, int G, int MT>
-hipError_t launch(const LinGemm& p, hipStream_t s) {
-  constexpr int STEP = 64 / sizeof(T), TC = 16 * G, MATS = DUAL ? 2 : 1;
-  const int64_t steps = (p.K + STEP - 1) / STEP, per_wave = MATS * p.M * TC * 4;
-  int waves = kWaves<MT>;
-  while (waves > 1 && (waves * 2 > steps || waves * per_wave > 64 * 1024)) waves /= 2;
-  hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, MT>), dim3(static_cast<unsigned>((p.N + TC - 1) / TC)),
-                     dim3(64 * waves), static_cast<unsigned>(waves * per_wave), s, p);
+// The launch: columns of a tile (16 g), waves of a workgroup and workgroups of a
+// tile.
+struct Shape {
+  int g, waves, splits;
+  int64_t tiles, cells;    // cells: floats of a workgroup's partial
+};
+
+Shape shape_of(const LinGemm& p) {
+  const int es = p.f32 ? 4 : 2, mats = p.mode == kModeDual ? 2 : 1;
+  Shape s;
+  s.g = p.w_t ? 1 : 8 / es;
+  const int tc = 16 * s.g;
+  s.tiles = (p.N + tc - 1) / tc;
+  s.cells = mats * p.M * tc;
+  const int64_t steps = (p.K * es + 63) / 64;
+  s.waves = 8;
+  while (s.waves > 1 && (s.waves * 2 > steps || s.waves * s.cells * 4 > 64 * 1024)) s.waves /= 2;
+  const int target = 512, least = 4;
+  s.splits = 1;
+  while (s.splits < 16 && s.tiles * s.splits < target && s.splits * 2 * s.waves * least <= steps) s.splits *= 2;
+  return s;
+}
+
+// Tickets first, then the partials.
+int64_t ticket_bytes(const Shape& s) { return (s.tiles * 4 + 255) / 256 * 256; }
+
+template <typename T, bool WKC, bool DUAL, int G>
+hipError_t by_rows(const LinGemm& p, const Shape& h, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits)), block(64 * h.waves);
+  const unsigned lds = static_cast<unsigned>(h.waves * h.cells * 4);
+  if (p.M <= 16) hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 1>), grid, block, lds, s, p);
+  else if (p.M <= 32) hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 2>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 4>), grid, block, lds, s, p);
   return hipGetLastError();
 }
 
-template <typename T, bool WKC, bool DUAL, int G>
-hipError_t by_rows(const LinGemm& p, hipStream_t s) {
-  if (p.M <= 16) return launch<T, WKC, DUAL, G, 1>(p, s);
-  if (p.M <= 32) return launch<T, WKC, DUAL, G, 2>(p, s);
-  return launch<T, WKC, DUAL, G, 4>(p, s);
-}
-
 template <typename T, bool DUAL>
-hipError_t by_layout(const LinGemm& p, hipStream_t s) {
-  if (p.w_t) return by_rows<T, true, DUAL, 1>(p, s);
-  return p.N >= 8192 ? by_rows<T, false, DUAL, 4>(p, s) : by_rows<T, false, DUAL, 2>(p, s);
+hipError_t by_layout(const LinGemm& p, const Shape& h, hipStream_t s) {
+  if (p.w_t) return by_rows<T, true, DUAL, 1>(p, h, s);
+  return by_rows<T, false, DUAL, 8 / static_cast<int>(sizeof(T))>(p, h, s);
 }
 
 }  // namespace
@@ -311,11 +370,23 @@ bool lin_rows_ok(const LinGemm& p) {
   return p.M <= 64 && !p.a_t && p.K > 0 && (p.mode == kModeOne || p.mode == kModeDual) && !p.acc_c;
 }
 
-hipError_t lin_rows_launch(const LinGemm& p, hipStream_t s) {
+int64_t lin_rows_ws(const LinGemm& p) {
+  if (!lin_rows_ok(p) || p.M <= 0 || p.N <= 0) return 0;
+  const Shape h = shape_of(p);
+  return h.splits > 1 ? ticket_bytes(h) + h.tiles * h.splits * h.cells * 4 : 0;
+}
+
+hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  Shape h = shape_of(p);
+  if (!ws || ws_bytes < lin_rows_ws(p)) h.splits = 1;
+  if (h.splits > 1) {
+    p.tickets = static_cast<uint32_t *>(ws);
+    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + ticket_bytes(h));
+  }
   const bool dual = p.mode == kModeDual;
-  if (p.f32) return dual ? by_layout<uint32_t, true>(p, s) : by_layout<uint32_t, false>(p, s);
-  return dual ? by_layout<uint16_t, true>(p, s) : by_layout<uint16_t, false>(p, s);
+  if (p.f32) return dual ? by_layout<uint32_t, true>(p, h, s) : by_layout<uint32_t, false>(p, h, s);
+  return dual ? by_layout<uint16_t, true>(p, h, s) : by_layout<uint16_t, false>(p, h, s);
 }
 
 }  // namespace tpshard

@@ -301,22 +301,6 @@ hipError_t dispatch(const LinGemm& p, hipStream_t s) {
 // workgroups of 256 threads where two products share a launch).
 bool lin_grid_ok(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22); }
 
-namespace {
-
-bool vec4(const void *p, int64_t ld, int64_t es) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && ld % 4 == 0);
-}
-
-}  // namespace
-
-hipError_t lin_gemm_launch(LinGemm p, hipStream_t s) {
-  const int64_t es = p.f32 ? 4 : 2, ces = p.c_f32 ? 4 : 2;
-  p.vec = vec4(p.c, p.ldc, ces) && vec4(p.c2, p.ldc, ces) && vec4(p.res, p.ldres, es) && vec4(p.aux, p.ldaux, es) &&
-          vec4(p.aux2, p.ldaux, es) && vec4(p.bias, 4, 4);
-  if (lin_rows_ok(p)) return lin_rows_launch(p, s);
-  return lin_staged_launch(p, s);
-}
-
 hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
   return p.f32 ? dispatch<uint32_t>(p, s) : dispatch<uint16_t>(p, s);
