@@ -41,7 +41,7 @@ struct LinGemm {
   int32_t c_f32 = 0;    // c holds fp32 (always with f32)
   int32_t acc_c = 0;
   int32_t vec = 0;      // set by the launcher: four columns at a time are aligned
-  // Few rows, several workgroups a tile: their partials and arrival counts.
+  // Several workgroups to a tile: their partials and arrival counts.
   float *join = nullptr;
   uint32_t *tickets = nullptr;
 };
@@ -49,8 +49,10 @@ struct LinGemm {
 // Whether the grids of the kernels below reach every tile of [M, N].
 bool lin_grid_ok(int64_t M, int64_t N);
 
-// Enqueues the product.  ws: lin_rows_ws bytes of zeros (or null); left zeroed
-// where it has to be.
+// Bytes of workspace that the product can use: zeros, left zeroed where they have
+// to be.
+int64_t lin_gemm_ws(const LinGemm& p);
+// Enqueues the product; ws may be null.
 hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws = nullptr, int64_t ws_bytes = 0);
 
 // The general kernel: any layout, alignment and size.
@@ -59,11 +61,22 @@ hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s);
 // The tiled bf16 kernels, where lin_tiles_ok: 16-byte aligned operands and rows,
 // K a multiple of 32, a row-contiguous operand of whole 8-column groups.
 bool lin_tiles_ok(const LinGemm& p);
-hipError_t lin_tiles_launch(const LinGemm& p, hipStream_t s);
-hipError_t lin_tiles_one(const LinGemm& p, hipStream_t s);
-hipError_t lin_tiles_dual(const LinGemm& p, hipStream_t s);
-hipError_t lin_tiles_cat(const LinGemm& p, hipStream_t s);
-hipError_t lin_tiles_pair(const LinGemm& p, hipStream_t s);
+enum Tile { kTile256, kTile192, kTile128w, kTile128, kTile64, kTile64k32 };
+struct TilePick {
+  int tile;     // Tile
+  int splits;   // workgroups that split a tile's K
+};
+// A workspace holds a launch's tickets, then its partials.
+inline int64_t lin_ticket_bytes(int64_t tiles) { return (tiles * 4 + 255) / 256 * 256; }
+// Tiles of a launch of bm x bn: kModeDual counts both weights' columns, kModePair both products.
+inline int64_t lin_tiles_count(const LinGemm& p, int bm, int bn) {
+  const int bno = p.mode == kModeDual ? bn / 2 : bn;
+  return (p.M + bm - 1) / bm * ((p.N + bno - 1) / bno) * (p.mode == kModePair ? 2 : 1);
+}
+hipError_t lin_tiles_one(const LinGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_dual(const LinGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_cat(const LinGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_pair(const LinGemm& p, const TilePick& t, hipStream_t s);
 
 // The kernel for few rows, where lin_rows_ok.  Given lin_rows_ws bytes of
 // workspace, several workgroups may split a tile's K.

@@ -140,7 +140,7 @@ int tp_linear_ws(const tp_linear_args *a, int64_t *bytes) {
   p.K = a->K;
   p.w_t = a->weight_layout == TP_WEIGHTS_LINEAR;
   p.f32 = a->dtype == TP_F32;
-  *bytes = lin_rows_ws(p);
+  *bytes = lin_gemm_ws(p);
   return TP_OK;
 }
 
@@ -156,7 +156,7 @@ int tp_gated_linear_ws(const tp_gated_args *a, int64_t *bytes) {
   p.K = a->K;
   p.w_t = a->weight_layout == TP_WEIGHTS_LINEAR;
   p.f32 = a->dtype == TP_F32;
-  *bytes = lin_rows_ws(p);
+  *bytes = lin_gemm_ws(p);
   return TP_OK;
 }
 

@@ -118,6 +118,87 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
   }
 }
 
+// ---- several workgroups to a tile ---------------------------------------------
+// Every workgroup of a tile leaves its partial sums; the one that finds all the
+// others' done adds them, in their order, so that the result does not depend on
+// who that is.  Nobody waits for anybody, and the ticket ends at zero again.
+//
+// The partials are device-scope accesses: such a store is past this XCD's own L2
+// once vmcnt has counted it, and such a load does not read a stale line there,
+// so no cache is written back or invalidated.  (A device fence writes the whole
+// L2 back: one per wave made a 51 us product take 531.)
+__device__ __forceinline__ void put_partial(float *p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_partial(const float *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put_partial(f32x2 *p, f32x2 v) {
+  __hip_atomic_store(reinterpret_cast<uint64_t *>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 get_partial(const f32x2 *p) {
+  return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED,
+                                                     __HIP_MEMORY_SCOPE_AGENT));
+}
+
+// After this workgroup's put_partial calls: whether it is the tile's last.
+__device__ __forceinline__ bool last_of_tile(uint32_t *ticket, uint32_t splits) {
+  __shared__ uint32_t before;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) before = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (before + 1 != splits) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+
+// Sum over `splits` partials, `pitch` elements apart, in order; eight loads in
+// flight at a time.
+template <typename V>
+__device__ __forceinline__ V sum_partials(const V *p, int64_t pitch, int splits) {
+  V v[8], s{};
+  for (int y0 = 0; y0 < splits; y0 += 8) {
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      if (y0 + y < splits) v[y] = get_partial(p + (y0 + y) * pitch);
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      if (y0 + y < splits) s = s + v[y];
+  }
+  return s;
+}
+
+// The accumulators of workgroup (blockIdx.x, blockIdx.y): left as a partial; true
+// in the tile's last workgroup, whose acc then holds the sum over all.
+template <int THREADS, int TM, int TN>
+__device__ __forceinline__ bool join_splits(const LinGemm& p, f32x4 (&acc)[TM][TN]) {
+  constexpr int64_t PITCH = TM * TN * 2 * THREADS;   // f32x2 of one workgroup
+  const int splits = gridDim.y;
+  f32x2 *tile = reinterpret_cast<f32x2 *>(p.join) + static_cast<int64_t>(blockIdx.x) * splits * PITCH + threadIdx.x;
+  f32x2 *mine = tile + blockIdx.y * PITCH;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        put_partial(mine + ((i * TN + j) * 2 + h) * THREADS, f32x2{acc[i][j][2 * h], acc[i][j][2 * h + 1]});
+  if (!last_of_tile(p.tickets + blockIdx.x, splits)) return false;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x2 s = sum_partials(tile + ((i * TN + j) * 2 + h) * THREADS, PITCH, splits);
+        acc[i][j][2 * h] = s[0];
+        acc[i][j][2 * h + 1] = s[1];
+      }
+  return true;
+}
+
 // ---- four columns of an output row ---------------------------------------------
 // `full`: all four exist and the row is aligned for one vector access;
 // otherwise `left` of them exist.

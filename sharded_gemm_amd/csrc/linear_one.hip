@@ -3,8 +3,8 @@
 
 namespace tpshard {
 
-hipError_t lin_tiles_one(const LinGemm& p, hipStream_t s) {
-  return p.w_t ? dispatch_tiles<kModeOne, false, true>(p, s) : dispatch_tiles<kModeOne, false, false>(p, s);
+hipError_t lin_tiles_one(const LinGemm& p, const TilePick& t, hipStream_t s) {
+  return p.w_t ? dispatch_tiles<kModeOne, false, true>(p, t, s) : dispatch_tiles<kModeOne, false, false>(p, t, s);
 }
 
 }  // namespace tpshard

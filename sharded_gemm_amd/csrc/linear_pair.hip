@@ -3,8 +3,8 @@
 
 namespace tpshard {
 
-hipError_t lin_tiles_pair(const LinGemm& p, hipStream_t s) {
-  return dispatch_tiles<kModePair, true, false>(p, s);
+hipError_t lin_tiles_pair(const LinGemm& p, const TilePick& t, hipStream_t s) {
+  return dispatch_tiles<kModePair, true, false>(p, t, s);
 }
 
 }  // namespace tpshard

@@ -1,5 +1,5 @@
-// The product for few rows (a decode step): M <= 64 tokens against a weight
-// that is read once, so the weight's bytes bound it.
+// The product for few rows (a decode step): up to 16 tokens, or 64, against a
+// weight that is read once, so the weight's bytes bound it.
 //
 //   kModeOne  c = epi(X W)        kModeDual  c = act(X W) * (X W2)
 //
@@ -91,13 +91,11 @@ struct Cols {
   }
 };
 
-// Most waves of a workgroup: past 16 rows the accumulators need more than the
-// 128 registers that 16 waves leave each.
-template <int MT>
-constexpr int kWaves = MT == 1 ? 16 : 8;
+// Waves of a workgroup (measured against 4 and 16 with one token).
+constexpr int kWaves = 8;
 
 template <typename T, bool WKC, bool DUAL, int G, int MT>
-__global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
+__global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
   constexpr int PER = 16 / sizeof(T);          // k of a lane in a step
   constexpr int STEP = 4 * PER;                // k of a step
   constexpr int MATS = DUAL ? 2 : 1;
@@ -260,31 +258,11 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
   const int cells = MATS * M * TC, splits = gridDim.y;
   const float *from = nullptr;                  // the tile's partials, once all are there
   if (splits > 1) {
-    // Every workgroup of the tile leaves its partial; the one that finds all
-    // the others' done adds them, in their order, so the sum does not depend
-    // on who that is.  Nobody waits for anybody, and the ticket ends at zero
-    // again.  The partials are device-scope accesses: such a store is past this
-    // XCD's own L2 once vmcnt has counted it, and such a load does not read a
-    // stale line there, so no cache is written back or invalidated (a device
-    // fence writes the whole L2 back: with one per wave the 4096 -> 14336 gated
-    // product took 531 us instead of 51).
     float *mine = p.join + (static_cast<int64_t>(blockIdx.x) * splits + blockIdx.y) * cells;
-    for (int i = threadIdx.x; i < cells; i += blockDim.x)
-      __hip_atomic_store(mine + i, joined(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    __shared__ uint32_t before;
-    if (threadIdx.x == 0)
-      before = __hip_atomic_fetch_add(p.tickets + blockIdx.x, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (before + 1 != static_cast<uint32_t>(splits)) return;
-    if (threadIdx.x == 0)
-      __hip_atomic_store(p.tickets + blockIdx.x, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = threadIdx.x; i < cells; i += blockDim.x) put_partial(mine + i, joined(i));
+    if (!last_of_tile(p.tickets + blockIdx.x, splits)) return;
     from = p.join + static_cast<int64_t>(blockIdx.x) * splits * cells;
   }
-  auto partial = [&](int y, int cell) {
-    return __hip_atomic_load(from + static_cast<int64_t>(y) * cells + cell, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  };
   with_act(p.act, [&](auto A) {
     constexpr int ACT = decltype(A)::value;
     for (int i = threadIdx.x; i < M * TC; i += blockDim.x) {
@@ -295,12 +273,7 @@ __global__ void __launch_bounds__(64 * kWaves<MT>) lin_rows_kernel(LinGemm p) {
 #pragma unroll
       for (int a = 0; a < MATS; ++a) {
         const int cell = a * M * TC + i;
-        if (from) {
-          v[a] = partial(0, cell);
-          for (int y = 1; y < splits; ++y) v[a] += partial(y, cell);
-        } else {
-          v[a] = joined(cell);
-        }
+        v[a] = from ? sum_partials(from + cell, cells, splits) : joined(cell);
       }
       auto put = [&](void *base, int64_t at, float y, bool f32) {
         if (f32) static_cast<float *>(base)[at] = y;
@@ -337,22 +310,29 @@ Shape shape_of(const LinGemm& p) {
   s.tiles = (p.N + tc - 1) / tc;
   s.cells = mats * p.M * tc;
   const int64_t steps = (p.K * es + 63) / 64;
-  s.waves = 8;
+  s.waves = kWaves;
   while (s.waves > 1 && (s.waves * 2 > steps || s.waves * s.cells * 4 > 64 * 1024)) s.waves /= 2;
-  const int target = 512, least = 4;
+  // Workgroups of a tile: until every CU has one (a wave keeping two steps),
+  // then up to two each where a workgroup still reads 256 KiB, which pays for
+  // the join.  MI355X, one token: gated 12288 -> 6144 (k-contiguous) 65 us with
+  // 384 workgroups, 55 with 768; 6144 -> 12288 (n-contiguous) 36 with 384, 31
+  // with 768; but gated 4096 -> 2048 (131 KiB each at 256) 10.4 with 256, 11.7
+  // with 512.
   s.splits = 1;
-  while (s.splits < 16 && s.tiles * s.splits < target && s.splits * 2 * s.waves * least <= steps) s.splits *= 2;
+  while (s.splits < 16 && s.splits * 2 * s.waves * 2 <= steps) {
+    const int64_t wgs = s.tiles * s.splits, each = static_cast<int64_t>(mats) * tc * es * p.K / s.splits;
+    if (wgs >= 512 || (wgs >= 256 && each < 256 * 1024)) break;
+    s.splits *= 2;
+  }
   return s;
 }
-
-// Tickets first, then the partials.
-int64_t ticket_bytes(const Shape& s) { return (s.tiles * 4 + 255) / 256 * 256; }
 
 template <typename T, bool WKC, bool DUAL, int G>
 hipError_t by_rows(const LinGemm& p, const Shape& h, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits)), block(64 * h.waves);
   const unsigned lds = static_cast<unsigned>(h.waves * h.cells * 4);
   if (p.M <= 16) hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 1>), grid, block, lds, s, p);
+  else if constexpr (!WKC) return hipErrorInvalidValue;
   else if (p.M <= 32) hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 2>), grid, block, lds, s, p);
   else hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 4>), grid, block, lds, s, p);
   return hipGetLastError();
@@ -366,14 +346,17 @@ hipError_t by_layout(const LinGemm& p, const Shape& h, hipStream_t s) {
 
 }  // namespace
 
+// Up to 16 rows (one operand's worth); with a k-contiguous weight up to 64, since
+// there more rows cost accumulators only (an n-contiguous one keeps four columns
+// a lane, and their accumulators spill).
 bool lin_rows_ok(const LinGemm& p) {
-  return p.M <= 64 && !p.a_t && p.K > 0 && (p.mode == kModeOne || p.mode == kModeDual) && !p.acc_c;
+  return p.M <= (p.w_t ? 64 : 16) && !p.a_t && p.K > 0 && (p.mode == kModeOne || p.mode == kModeDual) && !p.acc_c;
 }
 
 int64_t lin_rows_ws(const LinGemm& p) {
   if (!lin_rows_ok(p) || p.M <= 0 || p.N <= 0) return 0;
   const Shape h = shape_of(p);
-  return h.splits > 1 ? ticket_bytes(h) + h.tiles * h.splits * h.cells * 4 : 0;
+  return h.splits > 1 ? lin_ticket_bytes(h.tiles) + h.tiles * h.splits * h.cells * 4 : 0;
 }
 
 hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
@@ -382,7 +365,7 @@ hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s)
   if (!ws || ws_bytes < lin_rows_ws(p)) h.splits = 1;
   if (h.splits > 1) {
     p.tickets = static_cast<uint32_t *>(ws);
-    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + ticket_bytes(h));
+    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + lin_ticket_bytes(h.tiles));
   }
   const bool dual = p.mode == kModeDual;
   if (p.f32) return dual ? by_layout<uint32_t, true>(p, h, s) : by_layout<uint32_t, false>(p, h, s);

@@ -2,8 +2,6 @@
 // building blocks (gemm_tiles.h).  One translation unit instantiates each mode.
 #pragma once
 
-#include <algorithm>
-
 #include "gemm_tiles.h"
 #include "linear_dev.h"
 
@@ -130,6 +128,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(Lin
   };
   const int pending = 0;
   if (pl.st1 > pl.st0) ring_loop<C, S, false>(pl.st1 - pl.st0, issue, wait_stages, read, mma, [] {}, pending);
+  if (gridDim.y > 1 && !lin::join_splits<C::THREADS>(p, acc)) return;
 
   auto rm = [&](int i) -> int64_t { return pl.m0 + wm * C::WM + i * 16 + (lane & 15); };
   auto cn = [&](int j) -> int64_t {
@@ -198,17 +197,17 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinGemm p) {
 
 // ---- launchers -----------------------------------------------------------------
 
-// Tiles of a launch: kModeDual counts both weights' columns, kModePair both products.
 template <int MODE>
 int64_t tiles_of(const LinGemm& p, int bm, int bn) {
-  const int bno = MODE == kModeDual ? bn / 2 : bn;
-  return (p.M + bm - 1) / bm * ((p.N + bno - 1) / bno) * (p.mode == kModePair ? 2 : 1);
+  static_assert(MODE >= kModeOne && MODE <= kModePair, "mode");
+  return lin_tiles_count(p, bm, bn);
 }
 
 template <int BM, int BN, int BK, int S, int MODE, bool AT, bool WT, int WAVES_M, int WAVES_N>
-hipError_t launch_ring(const LinGemm& p, hipStream_t s) {
+hipError_t launch_ring(const LinGemm& p, int splits, hipStream_t s) {
   hipLaunchKernelGGL((lin_ring_kernel<BM, BN, BK, S, MODE, AT, WT, WAVES_M, WAVES_N>),
-                     dim3(static_cast<unsigned>(tiles_of<MODE>(p, BM, BN))), dim3(64 * WAVES_M * WAVES_N), 0, s, p);
+                     dim3(static_cast<unsigned>(tiles_of<MODE>(p, BM, BN)), static_cast<unsigned>(splits)),
+                     dim3(64 * WAVES_M * WAVES_N), 0, s, p);
   return hipGetLastError();
 }
 
@@ -219,32 +218,23 @@ hipError_t launch_lin_pps(const LinGemm& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The tile: waves of workgroups over the CUs times the tile's work over its
-// relative throughput (as gemm.hip's choice, whose measurements these are).
 template <int MODE, bool AT, bool WT>
-hipError_t dispatch_tiles(const LinGemm& p, hipStream_t s) {
+hipError_t dispatch_tiles(const LinGemm& p, const TilePick& t, hipStream_t s) {
   constexpr bool dual = MODE == kModeDual;
-  const bool k64 = p.K % 64 == 0;
-  constexpr int SN = dual ? 128 : 64;   // the small tile's W columns (64 of each weight)
-  if (tiles_of<MODE>(p, 128, 128) < kCUs) {
-    if (k64) return launch_ring<64, SN, 64, 2, MODE, AT, WT, 2, 2>(p, s);
-    return launch_ring<64, SN, 32, 4, MODE, AT, WT, 2, 2>(p, s);
-  }
-  auto cost = [&](int bm, int bn, double eff) {
-    return static_cast<double>((tiles_of<MODE>(p, bm, bn) + kCUs - 1) / kCUs) * bm * bn / eff;
-  };
-  const int64_t a_span = (AT ? p.K : p.M) * p.lda * 2, w_span = (WT ? p.N : p.K) * p.ldw * 2;
-  const bool pps = k64 && a_span < (int64_t{1} << 31) && w_span < (int64_t{1} << 31);
-  const double c256 = !AT && pps ? cost(256, 256, 1.0) : 1e300, c192 = !dual && pps ? cost(256, 192, 0.95) : 1e300;
-  const double c128w = pps ? cost(256, 128, 0.85) : 1e300, c128 = cost(128, 128, 0.7);
-  const double best = std::min(std::min(c256, c192), std::min(c128w, c128));
   constexpr int WGM = AT ? 4 : 2;
-  if constexpr (!AT)
-    if (c256 == best) return launch_lin_pps<256, 256, MODE, AT, WT>(p, s);
-  if constexpr (!dual)
-    if (c192 == best) return launch_lin_pps<256, 192, MODE, AT, WT, WGM>(p, s);
-  if (c128w == best) return launch_lin_pps<256, 128, MODE, AT, WT, AT || WT ? 4 : 2>(p, s);
-  return launch_ring<128, 128, 32, 8, MODE, AT, WT, 2, 4>(p, s);
+  switch (t.tile) {
+    case kTile256:
+      if constexpr (!AT) return launch_lin_pps<256, 256, MODE, AT, WT>(p, s);
+      break;
+    case kTile192:
+      if constexpr (!dual) return launch_lin_pps<256, 192, MODE, AT, WT, WGM>(p, s);
+      break;
+    case kTile128w: return launch_lin_pps<256, 128, MODE, AT, WT, AT || WT ? 4 : 2>(p, s);
+    case kTile128: return launch_ring<128, 128, 32, 8, MODE, AT, WT, 2, 4>(p, t.splits, s);
+    case kTile64: return launch_ring<64, dual ? 128 : 64, 64, 3, MODE, AT, WT, 2, 2>(p, t.splits, s);
+    case kTile64k32: return launch_ring<64, dual ? 128 : 64, 32, 4, MODE, AT, WT, 2, 2>(p, t.splits, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
