@@ -555,10 +555,11 @@ typedef struct {
   int64_t out_ld;
   void *pre_out;         /* optional [M, N]: X W + bias rounded to dtype, kept for the backward */
   int64_t pre_ld;
-  void *ws;              /* optional, tp_linear_ws bytes: lets few rows (a decode step) split K
-                            over the whole chip.  16-byte aligned, zero before its first use;
-                            every call leaves it fit for the next.  Calls that may overlap
-                            need one each.  NULL or smaller: one workgroup a tile */
+  void *ws;              /* optional, tp_linear_ws bytes: lets few rows (a decode step)
+                            and small batches split K over the whole chip.  16-byte
+                            aligned, zero before its first use; any calls may follow one
+                            another on it (of tp_gated_linear too), but calls that may
+                            overlap need one each.  NULL or smaller: K is not split */
   int64_t ws_bytes;
 } tp_linear_args;
 

@@ -815,8 +815,9 @@ def _call(fn, args, stream, prepare, tensors):
 
 def tp_linear_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH):
     """A zeroed workspace (uint8 tensor, maybe empty) for ``tp_linear`` of these shapes: with it
-    a few rows' product (M <= 64) is split over the whole chip.  It serves any number of calls
-    of the shapes, one after another."""
+    few rows and small batches split K over the whole chip.  It serves any number of calls
+    one after another, also of other shapes and of ``tp_gated_linear`` (one that needs more
+    runs as without it)."""
     import torch
     args = tp_linear_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
                           N=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]))

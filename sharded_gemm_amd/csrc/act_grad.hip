@@ -4,12 +4,15 @@
 //   linear: dPre = dOut * act'(pre);         dbias[n] = sum over m of dPre[m, n]
 //   gated : dU = dOut * act(G);              dG = dOut * U * act'(G)
 //
-// One pass over the inputs, memory-bound: a workgroup takes 512 columns by a
-// slab of rows, each lane 8 columns (16 bytes of bf16) of every fourth row.
-// The column sums add the unrounded fp32 values (dPre itself is rounded once to
-// the operands' type, for the products that read it next); each slab leaves its
-// own partial row and a second kernel adds the slabs in order, so no atomics
-// decide the result.
+// One pass over the inputs, memory-bound.  The gated form without row strides is
+// one flat array, 8 elements a lane.  Otherwise a workgroup takes up to 512
+// columns by a slab of rows, each lane 8 columns (16 bytes of bf16).  The column
+// sums add the unrounded fp32 values (dPre itself is rounded once to the
+// operands' type, for the products that read it next); each slab leaves its own
+// partial row and a second kernel adds the slabs in order, so no atomics decide
+// the result.
+#include <algorithm>
+
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -18,13 +21,14 @@ using namespace lin;
 
 namespace {
 
-constexpr int kLanes = 64, kGroups = 4, kCols = 8;
-constexpr int kTileCols = kLanes * kCols;
+constexpr int kThreads = 256, kCols = 8;
 
-// Eight elements at p; `left` exist (the rest read as zero).
+// Eight elements at p; `left` exist.  `on`: there are at least eight elements of
+// the array from p on, so the missing ones are read from the next rows (and not
+// used); otherwise they read as zero.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int64_t left, float (&v)[8]) {
-  if (left >= 8) {
+__device__ __forceinline__ void load8(const T *p, int64_t left, bool on, float (&v)[8]) {
+  if (left >= 8 || on) {
     if constexpr (sizeof(T) == 4) {
       const u32x4 a = *reinterpret_cast<const u32x4_any *>(p), b = *reinterpret_cast<const u32x4_any *>(p + 4);
 #pragma unroll
@@ -71,11 +75,38 @@ __device__ __forceinline__ void store8(T *p, int64_t left, const float (&v)[8]) 
   }
 }
 
+template <typename T, int ACT>
+__device__ __forceinline__ void gated8(const float (&d)[8], const float (&z)[8], const float (&u)[8], float (&dg)[8],
+                                       float (&du)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const f32x2 a = act_both<ACT>(z[e]);
+    du[e] = d[e] * a[0];
+    dg[e] = d[e] * u[e] * a[1];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) gated_grad_flat(ActGrad p) {
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kCols, left = p.M * p.N - at;
+  if (left <= 0) return;
+  float d[8], z[8], u[8], dg[8], du[8];
+  load8(static_cast<const T *>(p.d_out) + at, left, false, d);
+  load8(static_cast<const T *>(p.pre) + at, left, false, z);
+  load8(static_cast<const T *>(p.up) + at, left, false, u);
+  with_act(p.act, [&](auto A) { gated8<T, decltype(A)::value>(d, z, u, dg, du); });
+  store8(static_cast<T *>(p.d_up) + at, left, du);
+  store8(static_cast<T *>(p.d_pre) + at, left, dg);
+}
+
+// lanes: of a row (a power of two); the workgroup's 256 / lanes groups take the
+// slab's rows in turn.
 template <typename T, bool GATED>
-__global__ void __launch_bounds__(kLanes * kGroups) act_grad_kernel(ActGrad p, int64_t rows_per_slab) {
-  __shared__ float sums[GATED ? 1 : kGroups][GATED ? 1 : kTileCols];
-  const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kTileCols + lane * kCols, left = p.N - n;
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGrad p, int64_t rows_per_slab, int lanes) {
+  __shared__ float sums[GATED ? 1 : kThreads * kCols];
+  const int lane = threadIdx.x & (lanes - 1), grp = threadIdx.x / lanes, groups = kThreads / lanes;
+  const int cols = lanes * kCols;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * cols + lane * kCols, left = p.N - n;
   const int64_t r0 = blockIdx.y * rows_per_slab, r1 = min(r0 + rows_per_slab, p.M);
   float col[8];
 #pragma unroll
@@ -84,19 +115,16 @@ __global__ void __launch_bounds__(kLanes * kGroups) act_grad_kernel(ActGrad p, i
     constexpr int ACT = decltype(A)::value;
     if (left > 0) {
 #pragma unroll 2
-      for (int64_t m = r0 + grp; m < r1; m += kGroups) {
+      for (int64_t m = r0 + grp; m < r1; m += groups) {
+        // Seven more rows hold seven more elements, whatever their stride.
+        const bool on = m + 7 < p.M;
         float d[8], z[8], o[8];
-        load8(static_cast<const T *>(p.d_out) + m * p.ld_dout + n, left, d);
-        if (p.pre) load8(static_cast<const T *>(p.pre) + m * p.ld_pre + n, left, z);
+        load8(static_cast<const T *>(p.d_out) + m * p.ld_dout + n, left, on, d);
+        if (p.pre) load8(static_cast<const T *>(p.pre) + m * p.ld_pre + n, left, on, z);
         if constexpr (GATED) {
           float u[8], du[8];
-          load8(static_cast<const T *>(p.up) + m * p.ld_pre + n, left, u);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const f32x2 a = act_both<ACT>(z[e]);
-            du[e] = d[e] * a[0];
-            o[e] = d[e] * u[e] * a[1];
-          }
+          load8(static_cast<const T *>(p.up) + m * p.ld_pre + n, left, on, u);
+          gated8<T, ACT>(d, z, u, o, du);
           store8(static_cast<T *>(p.d_up) + m * p.N + n, left, du);
           store8(static_cast<T *>(p.d_pre) + m * p.N + n, left, o);
         } else {
@@ -117,12 +145,14 @@ __global__ void __launch_bounds__(kLanes * kGroups) act_grad_kernel(ActGrad p, i
   if constexpr (!GATED) {
     if (!p.parts) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[grp][lane * kCols + e] = col[e];
+    for (int e = 0; e < 8; ++e) sums[grp * cols + lane * kCols + e] = col[e];
     __syncthreads();
-    for (int i = threadIdx.x; i < kTileCols; i += kLanes * kGroups) {
-      const int64_t c = static_cast<int64_t>(blockIdx.x) * kTileCols + i;
+    for (int i = threadIdx.x; i < cols; i += kThreads) {
+      const int64_t c = static_cast<int64_t>(blockIdx.x) * cols + i;
       if (c >= p.N) break;
-      p.parts[blockIdx.y * p.N + c] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+      float v = sums[i];
+      for (int g = 1; g < groups; ++g) v += sums[g * cols + i];
+      p.parts[blockIdx.y * p.N + c] = v;
     }
   }
 }
@@ -151,26 +181,43 @@ __global__ void __launch_bounds__(64 * kSumGroups) colsum_kernel(const float *pa
   }
 }
 
-// Rows of a slab: 64 (16 rows a lane), more where a slab each would be more
-// than 1024 of them (the grid's second dimension, and the partials' size).
-int64_t slab_rows(int64_t M) {
-  const int64_t r = (M + 1023) / 1024;
-  return r < 64 ? 64 : r;
+// The grid: lanes of a row, and rows of a slab.  64 rows, fewer where that leaves
+// under 1024 workgroups (1021 x 999, gated: 67 us in 32 workgroups), though not
+// so few that the partial rows weigh more than an eighth of the input, nor so
+// many slabs that they exceed the grid.
+struct Grid {
+  int lanes;
+  int64_t tiles, rows, slabs;
+};
+Grid grid_of(int64_t M, int64_t N) {
+  Grid g{64, 0, 64, 0};
+  while (g.lanes > 1 && (g.lanes / 2) * kCols >= N) g.lanes /= 2;
+  g.tiles = (N + g.lanes * kCols - 1) / (g.lanes * kCols);
+  const int64_t least = std::max<int64_t>(16, kThreads / g.lanes);
+  while (g.rows > least && g.tiles * ((M + g.rows - 1) / g.rows) < 1024) g.rows /= 2;
+  g.rows = std::max(std::max(g.rows, least), (M + 1023) / 1024);
+  g.slabs = (M + g.rows - 1) / g.rows;
+  return g;
 }
 
 template <typename T>
 hipError_t launch(const ActGrad& p, hipStream_t s) {
-  const int64_t rows = slab_rows(p.M), slabs = (p.M + rows - 1) / rows;
-  if (slabs > 0) {
-    const dim3 grid(static_cast<unsigned>((p.N + kTileCols - 1) / kTileCols), static_cast<unsigned>(slabs));
-    if (p.gated) hipLaunchKernelGGL((act_grad_kernel<T, true>), grid, dim3(kLanes * kGroups), 0, s, p, rows);
-    else hipLaunchKernelGGL((act_grad_kernel<T, false>), grid, dim3(kLanes * kGroups), 0, s, p, rows);
+  const Grid g = grid_of(p.M, p.N);
+  if (p.M > 0) {
+    const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(g.slabs));
+    const int64_t flat = (p.M * p.N + kThreads * kCols - 1) / (kThreads * kCols);
+    if (p.gated && p.ld_dout == p.N && p.ld_pre == p.N && flat < (int64_t{1} << 23))
+      hipLaunchKernelGGL((gated_grad_flat<T>), dim3(static_cast<unsigned>(flat)), dim3(kThreads), 0, s, p);
+    else if (p.gated)
+      hipLaunchKernelGGL((act_grad_kernel<T, true>), grid, dim3(kThreads), 0, s, p, g.rows, g.lanes);
+    else
+      hipLaunchKernelGGL((act_grad_kernel<T, false>), grid, dim3(kThreads), 0, s, p, g.rows, g.lanes);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (p.colsum) {
     hipLaunchKernelGGL(colsum_kernel, dim3(static_cast<unsigned>((p.N + 63) / 64)), dim3(64 * kSumGroups), 0, s, p.parts,
-                       slabs, p.N, p.colsum, p.accumulate);
+                       g.slabs, p.N, p.colsum, p.accumulate);
     return hipGetLastError();
   }
   return hipSuccess;
@@ -178,10 +225,7 @@ hipError_t launch(const ActGrad& p, hipStream_t s) {
 
 }  // namespace
 
-int64_t act_grad_slabs(int64_t M, int64_t) {
-  const int64_t rows = slab_rows(M);
-  return (M + rows - 1) / rows;
-}
+int64_t act_grad_slabs(int64_t M, int64_t N) { return grid_of(M, N).slabs; }
 
 hipError_t act_grad_launch(const ActGrad& p, hipStream_t s) {
   if (p.N <= 0) return hipSuccess;

@@ -56,7 +56,8 @@ int64_t lin_gemm_ws(const LinGemm& p);
 hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws = nullptr, int64_t ws_bytes = 0);
 
 // The general kernel: any layout, alignment and size.
-hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s);
+int64_t lin_staged_ws(const LinGemm& p);
+hipError_t lin_staged_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s);
 
 // The tiled bf16 kernels, where lin_tiles_ok: 16-byte aligned operands and rows,
 // K a multiple of 32, a row-contiguous operand of whole 8-column groups.
@@ -66,8 +67,10 @@ struct TilePick {
   int tile;     // Tile
   int splits;   // workgroups that split a tile's K
 };
-// A workspace holds a launch's tickets, then its partials.
-inline int64_t lin_ticket_bytes(int64_t tiles) { return (tiles * 4 + 255) / 256 * 256; }
+// A workspace holds tickets, then a launch's partials.  The tickets' place does
+// not depend on the launch, so calls of any shapes may follow one another on one
+// workspace.  (K is only split where a launch has fewer than 512 tiles.)
+constexpr int64_t kTicketBytes = 4096, kMaxTickets = kTicketBytes / 4;
 // Tiles of a launch of bm x bn: kModeDual counts both weights' columns, kModePair both products.
 inline int64_t lin_tiles_count(const LinGemm& p, int bm, int bn) {
   const int bno = p.mode == kModeDual ? bn / 2 : bn;

@@ -62,7 +62,7 @@ TilePick pick(const LinGemm& p) {
 int64_t ws_of(const LinGemm& p, const TilePick& t) {
   if (t.splits < 2) return 0;
   const int64_t tiles = small_tiles(p);
-  return lin_ticket_bytes(tiles) + tiles * t.splits * 64 * (p.mode == kModeDual ? 128 : 64) * 4;
+  return kTicketBytes + tiles * t.splits * 64 * (p.mode == kModeDual ? 128 : 64) * 4;
 }
 
 // Whether few rows run on their own kernel: always where the tiled ones cannot,
@@ -81,7 +81,7 @@ hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   if (!ws || ws_bytes < ws_of(p, t)) t.splits = 1;
   if (t.splits > 1) {
     p.tickets = static_cast<uint32_t *>(ws);
-    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + lin_ticket_bytes(small_tiles(p)));
+    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
   }
   if (p.a_t) return lin_tiles_pair(p, t, s);
   switch (p.mode) {
@@ -94,11 +94,11 @@ hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
 
 }  // namespace
 
-// (Asked before any pointer is known: that of a call whose operands are aligned.)
+// (Asked before the strides are known: enough for either kernel.)
 int64_t lin_gemm_ws(const LinGemm& p) {
   if (p.M <= 0 || p.N <= 0) return 0;
   if (takes_rows(p)) return lin_rows_ws(p);
-  return lin_tiles_ok(p) ? ws_of(p, pick(p)) : 0;
+  return std::max(lin_tiles_ok(p) ? ws_of(p, pick(p)) : 0, lin_staged_ws(p));
 }
 
 hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws, int64_t ws_bytes) {
@@ -107,7 +107,7 @@ hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws, int64_t ws_bytes)
           aligned(p.aux, p.ldaux, es, 4) && aligned(p.aux2, p.ldaux, es, 4) && aligned(p.bias, 4, 4, 4);
   if (takes_rows(p)) return lin_rows_launch(p, ws, ws_bytes, s);
   if (lin_tiles_ok(p)) return launch_tiles(p, ws, ws_bytes, s);
-  return lin_staged_launch(p, s);
+  return lin_staged_launch(p, ws, ws_bytes, s);
 }
 
 }  // namespace tpshard

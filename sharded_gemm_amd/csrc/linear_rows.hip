@@ -319,6 +319,7 @@ Shape shape_of(const LinGemm& p) {
   // with 768; but gated 4096 -> 2048 (131 KiB each at 256) 10.4 with 256, 11.7
   // with 512.
   s.splits = 1;
+  static_assert(kMaxTickets >= 512, "a ticket for every tile that is split");
   while (s.splits < 16 && s.splits * 2 * s.waves * 2 <= steps) {
     const int64_t wgs = s.tiles * s.splits, each = static_cast<int64_t>(mats) * tc * es * p.K / s.splits;
     if (wgs >= 512 || (wgs >= 256 && each < 256 * 1024)) break;
@@ -356,7 +357,7 @@ bool lin_rows_ok(const LinGemm& p) {
 int64_t lin_rows_ws(const LinGemm& p) {
   if (!lin_rows_ok(p) || p.M <= 0 || p.N <= 0) return 0;
   const Shape h = shape_of(p);
-  return h.splits > 1 ? lin_ticket_bytes(h.tiles) + h.tiles * h.splits * h.cells * 4 : 0;
+  return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * h.cells * 4 : 0;
 }
 
 hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
@@ -365,7 +366,7 @@ hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s)
   if (!ws || ws_bytes < lin_rows_ws(p)) h.splits = 1;
   if (h.splits > 1) {
     p.tickets = static_cast<uint32_t *>(ws);
-    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + lin_ticket_bytes(h.tiles));
+    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
   }
   const bool dual = p.mode == kModeDual;
   if (p.f32) return dual ? by_layout<uint32_t, true>(p, h, s) : by_layout<uint32_t, false>(p, h, s);

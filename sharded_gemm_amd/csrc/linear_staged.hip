@@ -53,6 +53,13 @@ __device__ __forceinline__ u32x4 load16(const T *p, int64_t left) {
 
 // One operand's tile: ROWS output rows (or columns) by one stage of K.
 // KC: k is contiguous in memory.  T: uint32_t (fp32) or uint16_t (bf16).
+//
+// Rows past the edge are clamped onto an existing one, and a row-contiguous
+// group that reaches past it reads on into the next rows: both only feed
+// outputs that are never stored.  So a stage is fetched without a check per
+// element wherever it and the V rows after it lie inside K (there, reading V
+// elements from any existing one stays within the operand whatever its stride);
+// only the last stages of K are checked, and their missing elements are zero.
 template <typename T, int ROWS, bool KC>
 struct Tile {
   static constexpr int V = 16 / sizeof(T);          // elements of a 16-byte chunk
@@ -62,28 +69,49 @@ struct Tile {
   static_assert(KB == 2 || KB == 4, "tile rows");
   static_assert(KC || NBLK * (BK / KB) == kThreads, "one block of KB k rows per thread");
 
-  // at(r): element offset of tile row r at k = 0 (KC; < 0: no such row), or
-  // group(b, &left): offset of the V rows of group b and how many exist.
-  template <typename At>
-  __device__ __forceinline__ static void load(const T *base, int64_t ld, int64_t k0, int64_t K, At&& at,
-                                              u32x4 (&g)[KB]) {
+  const T *at[KC ? KB : 1];    // sources at k = 0
+  int64_t ld;
+  int left;                    // elements of the group that exist (row-contiguous)
+
+  // where(r, &base, &index): the matrix and the row of tile row r; n: rows that exist.
+  template <typename Where>
+  __device__ __forceinline__ void init(int64_t ld_, int64_t n, Where&& where) {
     const int t = threadIdx.x;
+    ld = ld_;
+    left = V;
+    const T *base;
+    int64_t row;
     if constexpr (KC) {
 #pragma unroll
       for (int q = 0; q < KB; ++q) {
-        const int idx = t + kThreads * q, r = idx >> 3, c = idx & 7;
-        const int64_t k = k0 + c * V;
-        int64_t left = K - k, row;
-        if (!at(r, &row)) left = 0;
-        g[q] = load16<T>(base + row * ld + k, left);
+        const int idx = t + kThreads * q;
+        where(idx >> 3, &base, &row);
+        at[q] = base + (row < n ? row : n - 1) * ld + (idx & 7) * V;
       }
     } else {
-      const int b = t % NBLK, kb = t / NBLK;
-      int64_t col, left = at(b * V, &col);
+      where(t % NBLK * V, &base, &row);
+      const int64_t rest = n - row;
+      if (rest <= 0) row = n - 1;
+      else if (rest < V) left = static_cast<int>(rest);
+      at[0] = base + row + static_cast<int64_t>(t / NBLK * KB) * ld;
+    }
+  }
+
+  // `shift`: from the first matrix to the one read (elements).
+  __device__ __forceinline__ void load(int64_t k0, int64_t K, int64_t shift, u32x4 (&g)[KB]) const {
+    const int t = threadIdx.x;
+    if (k0 + BK + V <= K) {
+#pragma unroll
+      for (int q = 0; q < KB; ++q)
+        g[q] = *reinterpret_cast<const u32x4_any *>(KC ? at[KC ? q : 0] + shift + k0 : at[0] + shift + (k0 + q) * ld);
+    } else {
 #pragma unroll
       for (int q = 0; q < KB; ++q) {
-        const int64_t k = k0 + kb * KB + q;
-        g[q] = load16<T>(base + k * ld + col, k < K ? left : 0);
+        if constexpr (KC) {
+          g[q] = load16<T>(at[q] + shift + k0, K - k0 - ((t + kThreads * q) & 7) * V);
+        } else {
+          g[q] = load16<T>(at[0] + shift + (k0 + q) * ld, k0 + t / NBLK * KB + q < K ? left : 0);
+        }
       }
     }
   }
@@ -108,10 +136,8 @@ struct Tile {
         } else {
           uint32_t d[KB / 2];
 #pragma unroll
-          for (int e = 0; e < KB / 2; ++e) {
-            const uint32_t lo = g[2 * e][j >> 1], hi = g[2 * e + 1][j >> 1];
-            d[e] = (j & 1) ? ((lo >> 16) | (hi & 0xffff0000u)) : ((lo & 0xffffu) | (hi << 16));
-          }
+          for (int e = 0; e < KB / 2; ++e)
+            d[e] = __builtin_amdgcn_perm(g[2 * e + 1][j >> 1], g[2 * e][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
           if constexpr (KB == 4) *reinterpret_cast<u32x2 *>(dst) = u32x2{d[0], d[1]};
           else *reinterpret_cast<uint32_t *>(dst) = d[0];
         }
@@ -124,7 +150,7 @@ template <typename T, int BM, int BN, bool AKC, bool WKC, int MODE>
 __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
   using TA = Tile<T, BM, AKC>;
   using TW = Tile<T, BN, WKC>;
-  constexpr int BK = TA::BK, V = TA::V;
+  constexpr int BK = TA::BK;
   constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 16, TN = WN / 16;
   constexpr int BNO = MODE == kModeDual ? BN / 2 : BN;   // output columns of a tile
   constexpr int LDS_A = BM * kRow, STAGE = (BM + BN) * kRow;
@@ -137,51 +163,24 @@ __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
   // Neighbouring workgroups share a W panel (tiles walk down the rows first).
   const int64_t m0 = tile % tiles_m * BM, n0 = tile / tiles_m * BNO;
   const T *A = static_cast<const T *>(second ? p.a2 : p.a), *W = static_cast<const T *>(second ? p.w2 : p.w);
+  const T *W2 = static_cast<const T *>(p.w2);
   void *c = second ? p.c2 : p.c;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
 
-  // A row r (KC) or the group of rows from r on: the first row's index, and
-  // how many exist.
-  auto a_at = [&](int r, int64_t *row) -> int64_t {
-    const int64_t m = m0 + r;
-    *row = m < p.M ? m : 0;
-    return m < p.M ? p.M - m : 0;
-  };
-  // W tile row r: with kModeDual each wave's first half are the gate's columns
-  // and its second half the up projection's.
-  auto w_col = [&](int r) -> int64_t {
-    if constexpr (MODE == kModeDual) return n0 + r / WN * (WN / 2) + r % (WN / 2);
-    else return n0 + r;
-  };
-  auto w_at = [&](int r, int64_t *row) -> int64_t {
-    const int64_t n = w_col(r);
-    *row = n < p.N ? n : 0;
-    return n < p.N ? p.N - n : 0;
-  };
-
-  u32x4 ga[TA::KB], gw[TW::KB];
-  auto load = [&](int64_t k0, const T *Ab, const T *Wb) {
-    TA::load(Ab, p.lda, k0, p.K, a_at, ga);
-    if constexpr (MODE == kModeDual) {
-      // Per thread: the matrix of the tile row (or group) it fetches.
-      const T *W2 = static_cast<const T *>(p.w2);
-      if constexpr (WKC) {
-#pragma unroll
-        for (int q = 0; q < TW::KB; ++q) {
-          const int idx = threadIdx.x + kThreads * q, r = idx >> 3, ch = idx & 7;
-          const int64_t k = k0 + ch * V;
-          int64_t row, left = w_at(r, &row) ? p.K - k : 0;
-          gw[q] = load16<T>((r % WN < WN / 2 ? Wb : W2) + row * p.ldw + k, left);
-        }
-      } else {
-        const int b = threadIdx.x % TW::NBLK;
-        TW::load(b * V % WN < WN / 2 ? Wb : W2, p.ldw, k0, p.K, w_at, gw);
-      }
-    } else {
-      TW::load(Wb, p.ldw, k0, p.K, w_at, gw);
-    }
-  };
+  TA ta;
+  TW tw;
+  ta.init(p.lda, p.M, [&](int r, const T **base, int64_t *row) {
+    *base = A;
+    *row = m0 + r;
+  });
+  tw.init(p.ldw, p.N, [&](int r, const T **base, int64_t *row) {
+    // kModeDual: each wave's first half of the tile are the gate's columns, its
+    // second half the up projection's.
+    const bool up = MODE == kModeDual && r % WN >= WN / 2;
+    *base = up ? W2 : W;
+    *row = n0 + (MODE == kModeDual ? r / WN * (WN / 2) + r % (WN / 2) : r);
+  });
 
   f32x4 acc[TM][TN];
 #pragma unroll
@@ -189,15 +188,23 @@ __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int64_t per = (p.K + BK - 1) / BK, nst = MODE == kModeCat ? 2 * per : per;
-  auto fetch = [&](int64_t st) {
-    if constexpr (MODE == kModeCat) {
-      if (st >= per) {
-        load((st - per) * BK, static_cast<const T *>(p.a2), static_cast<const T *>(p.w2));
-        return;
-      }
-    }
-    load(st * BK, A, W);
+  const int64_t per = (p.K + BK - 1) / BK, all = MODE == kModeCat ? 2 * per : per;
+  const int64_t st0 = all * blockIdx.y / gridDim.y, nst = all * (blockIdx.y + 1) / gridDim.y - st0;
+  const int64_t a_far = MODE == kModeCat ? static_cast<const T *>(p.a2) - A : 0, w_far = MODE == kModeCat ? W2 - W : 0;
+  struct Regs {
+    u32x4 a[TA::KB], w[TW::KB];
+  };
+  auto fetch = [&](int64_t st, Regs& g) {
+    st += st0;
+    const bool far = MODE == kModeCat && st >= per;
+    const int64_t k0 = (far ? st - per : st) * BK;
+    ta.load(k0, p.K, far ? a_far : 0, g.a);
+    tw.load(k0, p.K, far ? w_far : 0, g.w);
+  };
+  auto put = [&](int64_t st, const Regs& g) {
+    char *slot = smem + (st & 1) * STAGE;
+    TA::store(slot, g.a);
+    TW::store(slot + LDS_A, g.w);
   };
   auto compute = [&](const char *stage) {
     const char *As = stage, *Ws = stage + LDS_A;
@@ -231,23 +238,25 @@ __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
     }
   };
 
-  if (nst > 0) {
-    fetch(0);
-    TA::store(smem, ga);
-    TW::store(smem + LDS_A, gw);
-  }
-  __syncthreads();
-  for (int64_t st = 0; st < nst; ++st) {
-    char *cur = smem + (st & 1) * STAGE, *nxt = smem + ((st + 1) & 1) * STAGE;
-    const bool more = st + 1 < nst;
-    if (more) fetch(st + 1);
-    compute(cur);
-    if (more) {
-      TA::store(nxt, ga);
-      TW::store(nxt + LDS_A, gw);
-    }
+  // Stage st + 2 leaves for the registers that stage st has left, stage st + 1
+  // moves from its own to LDS after stage st's products: a load has two stages'
+  // time to arrive.
+  Regs g0, g1;
+  auto step = [&](int64_t st, Regs& mine, const Regs& next) {
+    if (st + 2 < nst) fetch(st + 2, mine);
+    compute(smem + (st & 1) * STAGE);
+    if (st + 1 < nst) put(st + 1, next);
     __syncthreads();
+  };
+  if (nst > 0) fetch(0, g0);
+  if (nst > 1) fetch(1, g1);
+  if (nst > 0) put(0, g0);
+  __syncthreads();
+  for (int64_t st = 0; st < nst; st += 2) {
+    step(st, g0, g1);
+    if (st + 1 < nst) step(st + 1, g1, g0);
   }
+  if (gridDim.y > 1 && !join_splits<kThreads>(p, acc)) return;
 
   auto rm = [&](int i) -> int64_t { return m0 + wm * WM + i * 16 + (lane & 15); };
   auto cn = [&](int j) -> int64_t {
@@ -260,38 +269,48 @@ __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
 
 constexpr int64_t kCUs = 256;
 
+// The tile's edge (128 where every CU gets such a tile, else 64) and the
+// workgroups that split its K.
+struct Shape {
+  int edge, splits;
+  int64_t tiles;
+};
+Shape shape_of(const LinGemm& p) {
+  Shape h{128, 1, lin_tiles_count(p, 128, 128)};
+  if (h.tiles >= kCUs) return h;
+  h.edge = 64;
+  h.tiles = lin_tiles_count(p, 64, 64);
+  const int64_t stages = (p.K * (p.f32 ? 4 : 2) + kRow - 1) / kRow * (p.mode == kModeCat ? 2 : 1);
+  while (h.splits < 16 && h.tiles * h.splits < 2 * kCUs && stages >= 2 * h.splits * 8) h.splits *= 2;
+  return h;
+}
+
 template <typename T, bool AKC, bool WKC, int MODE>
-hipError_t launch(const LinGemm& p, hipStream_t s) {
-  const int64_t products = MODE == kModePair ? 2 : 1, cols = MODE == kModeDual ? 2 * p.N : p.N;
-  const int64_t big = (p.M + 127) / 128 * ((cols + 127) / 128) * products;
-  const int64_t small = (p.M + 63) / 64 * ((cols + 63) / 64) * products;
-  if (big >= kCUs)
-    hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), dim3(static_cast<unsigned>(big)),
-                       dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), dim3(static_cast<unsigned>(small)),
-                       dim3(kThreads), 0, s, p);
+hipError_t launch(const LinGemm& p, const Shape& h, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits));
+  if (h.edge == 128) hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), grid, dim3(kThreads), 0, s, p);
+  else hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), grid, dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t dispatch(const LinGemm& p, hipStream_t s) {
+hipError_t dispatch(const LinGemm& p, const Shape& h, hipStream_t s) {
   const bool akc = !p.a_t, wkc = p.w_t != 0;
   switch (p.mode) {
     case kModeOne:
-      if (akc) return wkc ? launch<T, true, true, kModeOne>(p, s) : launch<T, true, false, kModeOne>(p, s);
+      if (akc) return wkc ? launch<T, true, true, kModeOne>(p, h, s) : launch<T, true, false, kModeOne>(p, h, s);
       break;
     case kModeDual:
-      if (akc) return wkc ? launch<T, true, true, kModeDual>(p, s) : launch<T, true, false, kModeDual>(p, s);
+      if (akc) return wkc ? launch<T, true, true, kModeDual>(p, h, s) : launch<T, true, false, kModeDual>(p, h, s);
       break;
     case kModeCat:
-      if (akc) return wkc ? launch<T, true, true, kModeCat>(p, s) : launch<T, true, false, kModeCat>(p, s);
+      if (akc) return wkc ? launch<T, true, true, kModeCat>(p, h, s) : launch<T, true, false, kModeCat>(p, h, s);
       break;
     case kModePair:
-      if (!akc && !wkc) return launch<T, false, false, kModePair>(p, s);
+      if (!akc && !wkc) return launch<T, false, false, kModePair>(p, h, s);
       break;
   }
-  if (p.mode == kModeOne && !akc && !wkc) return launch<T, false, false, kModeOne>(p, s);
+  if (p.mode == kModeOne && !akc && !wkc) return launch<T, false, false, kModeOne>(p, h, s);
   return hipErrorInvalidValue;
 }
 
@@ -301,9 +320,20 @@ hipError_t dispatch(const LinGemm& p, hipStream_t s) {
 // workgroups of 256 threads where two products share a launch).
 bool lin_grid_ok(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22); }
 
-hipError_t lin_staged_launch(const LinGemm& p, hipStream_t s) {
+int64_t lin_staged_ws(const LinGemm& p) {
+  const Shape h = shape_of(p);
+  return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * 64 * 64 * 4 : 0;
+}
+
+hipError_t lin_staged_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  return p.f32 ? dispatch<uint32_t>(p, s) : dispatch<uint16_t>(p, s);
+  Shape h = shape_of(p);
+  if (!ws || ws_bytes < lin_staged_ws(p)) h.splits = 1;
+  if (h.splits > 1) {
+    p.tickets = static_cast<uint32_t *>(ws);
+    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
+  }
+  return p.f32 ? dispatch<uint32_t>(p, h, s) : dispatch<uint16_t>(p, h, s);
 }
 
 }  // namespace tpshard
