@@ -91,8 +91,12 @@ struct Tile {
     } else {
       where(t % NBLK * V, &base, &row);
       const int64_t rest = n - row;
-      if (rest <= 0) row = n - 1;
-      else if (rest < V) left = static_cast<int>(rest);
+      if (rest <= 0) {
+        row = n - 1;
+        left = 1;      // the clamped element itself: nothing lies behind the last row's
+      } else if (rest < V) {
+        left = static_cast<int>(rest);
+      }
       at[0] = base + row + static_cast<int64_t>(t / NBLK * KB) * ld;
     }
   }

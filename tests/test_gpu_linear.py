@@ -432,6 +432,26 @@ def test_prepared_calls():
         call()
 
 
+@pytest.mark.parametrize("dtype,K,N", [(F32, 2047, 2049), (BF16, 4095, 4097)])
+@pytest.mark.parametrize("layout", [MATH, LINEAR])
+def test_nothing_behind_the_last_element(dtype, K, N, layout):
+    """A weight that ends within 8 bytes of its allocation, with columns past the edge in the last tile."""
+    announce(f"last element {dtype} {K} x {N} layout {layout}")
+    M = 40
+    W = (torch.randn((K, N) if layout == MATH else (N, K), device="cuda") * 0.02).to(dtype)
+    X = rnd((M, K), 1, dtype).cuda()
+    out = torch.empty((M, N), dtype=dtype, device="cuda")
+    tp.tp_linear(X, W, out, weight_layout=layout)
+    dX, dW, d = torch.empty_like(X), torch.empty_like(W), rnd((M, N), 2, dtype).cuda()
+    tp.tp_linear_backward(X, W, d, dX=dX, dW=dW, weight_layout=layout)
+    torch.cuda.synchronize()
+    w = W.double() if layout == MATH else W.double().t()
+    for got, a, b in ((out, X.double(), w), (dX, d.double(), w.t())):
+        ref = a @ b
+        e = (a.shape[1] + 4) * U32 * (a.abs() @ b.abs())
+        assert bool(((got.double() - ref).abs() <= e + u(dtype) * (ref.abs() + e)).all())
+
+
 def test_far_offsets():
     """Operands whose last element lies past 2^32 bytes from their base."""
     if torch.cuda.mem_get_info()[0] < 40 << 30:
