@@ -602,8 +602,11 @@ typedef struct {
   int64_t ws_bytes;
 } tp_linear_bwd_args;
 
-/* Bytes of workspace the call needs (0: none).  Reads dtype, act, M, N and which
- * of dX, dW, dbias are asked for (non-NULL).  Host only. */
+/* Bytes of workspace the call uses (0: none).  Reads dtype, act, weight_layout,
+ * the sizes and which of dX, dW, dbias are asked for (non-NULL).  Host only.  The
+ * call refuses less than what it cannot do without (dPre where there is an
+ * activation, and partial sums for dbias); the rest lets its products split K.
+ * A backward's workspace need not be cleared. */
 int tp_linear_backward_ws(const tp_linear_bwd_args *args, int64_t *bytes);
 
 /*
@@ -671,7 +674,8 @@ typedef struct {
   int64_t ws_bytes;
 } tp_gated_bwd_args;
 
-/* Bytes of workspace the call needs (reads dtype, M and F).  Host only. */
+/* Bytes of workspace the call uses (reads dtype and the sizes); it refuses less
+ * than dGate and dUp take, the rest lets its products split K.  Host only. */
 int tp_gated_linear_backward_ws(const tp_gated_bwd_args *args, int64_t *bytes);
 
 /*

@@ -86,8 +86,17 @@ __device__ __forceinline__ void gated8(const float (&d)[8], const float (&z)[8],
   }
 }
 
+// The first workgroup clears the tickets of the products that follow.
+__device__ __forceinline__ void zero_tickets(uint32_t *tickets) {
+  if (tickets && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int64_t i = threadIdx.x; i < kMaxTickets; i += blockDim.x) tickets[i] = 0;
+}
+
+__global__ void __launch_bounds__(kThreads) zero_tickets_kernel(uint32_t *tickets) { zero_tickets(tickets); }
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gated_grad_flat(ActGrad p) {
+  zero_tickets(p.tickets);
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * kCols, left = p.M * p.N - at;
   if (left <= 0) return;
   float d[8], z[8], u[8], dg[8], du[8];
@@ -104,6 +113,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_flat(ActGrad p) {
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGrad p, int64_t rows_per_slab, int lanes) {
   __shared__ float sums[GATED ? 1 : kThreads * kCols];
+  zero_tickets(p.tickets);
   const int lane = threadIdx.x & (lanes - 1), grp = threadIdx.x / lanes, groups = kThreads / lanes;
   const int cols = lanes * kCols;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * cols + lane * kCols, left = p.N - n;
@@ -226,6 +236,11 @@ hipError_t launch(const ActGrad& p, hipStream_t s) {
 }  // namespace
 
 int64_t act_grad_slabs(int64_t M, int64_t N) { return grid_of(M, N).slabs; }
+
+hipError_t zero_tickets_launch(uint32_t *tickets, hipStream_t s) {
+  hipLaunchKernelGGL(zero_tickets_kernel, dim3(1), dim3(kThreads), 0, s, tickets);
+  return hipGetLastError();
+}
 
 hipError_t act_grad_launch(const ActGrad& p, hipStream_t s) {
   if (p.N <= 0) return hipSuccess;

@@ -17,6 +17,12 @@ enum {
   kModePair = 3,  // c = A W and c2 = A2 W2, two products of one shape in one launch
 };
 
+// A workspace's first bytes are tickets (zero before and after every launch), its
+// rest a launch's partials.  The tickets' place does not depend on the launch, so
+// calls of any shapes may follow one another on one workspace.  (K is only split
+// where a launch has a ticket for every tile.)
+constexpr int64_t kTicketBytes = 4096, kMaxTickets = kTicketBytes / 4;
+
 // C[M,N] = epi(A[M,K] W[K,N]), strides in elements.  As in GemmArgs, a_t: A is
 // stored [K][lda]; w_t: W is stored [N][ldw].  The second operands share the
 // first ones' shape and stride.  Epilogue, on the fp32 accumulator (kModeOne):
@@ -67,10 +73,6 @@ struct TilePick {
   int tile;     // Tile
   int splits;   // workgroups that split a tile's K
 };
-// A workspace holds tickets, then a launch's partials.  The tickets' place does
-// not depend on the launch, so calls of any shapes may follow one another on one
-// workspace.  (K is only split where a launch has fewer than 512 tiles.)
-constexpr int64_t kTicketBytes = 4096, kMaxTickets = kTicketBytes / 4;
 // Tiles of a launch of bm x bn: kModeDual counts both weights' columns, kModePair both products.
 inline int64_t lin_tiles_count(const LinGemm& p, int bm, int bn) {
   const int bno = p.mode == kModeDual ? bn / 2 : bn;
@@ -98,9 +100,11 @@ struct ActGrad {
   float *parts = nullptr;                   // [slabs][N], or null
   float *colsum = nullptr;                  // [N]
   int32_t f32 = 0, act = 0, gated = 0, accumulate = 0;
+  uint32_t *tickets = nullptr;              // kMaxTickets to set to zero, or null
 };
 int64_t act_grad_slabs(int64_t M, int64_t N);   // rows of `parts`
 hipError_t act_grad_launch(const ActGrad& p, hipStream_t s);
+hipError_t zero_tickets_launch(uint32_t *tickets, hipStream_t s);
 
 // ---- gradient norm and clipping --------------------------------------------
 constexpr int kGradParts = 1024;   // partial sums of squares of one call

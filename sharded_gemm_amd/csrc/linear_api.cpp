@@ -109,16 +109,63 @@ int launch(const LinGemm& p, hipStream_t s, int kind, double flops, const char *
   return TP_OK;
 }
 
-// Workspace of the linear backward: dPre in the operands' type (an activation,
-// and a product that reads it), then the bias gradient's partial rows.
-struct LinearWs {
-  int64_t d_pre = 0, parts = 0, total = 0;
+// The backward's products (pointers to the gradients at the activation apart).
+// dX [M, K] = dPre [M, N] W^T; with two weights both, in one accumulator.
+LinGemm dx_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool linear, bool gated) {
+  LinGemm p;
+  p.mode = gated ? kModeCat : kModeOne;
+  p.w_t = !linear;
+  p.M = M;
+  p.N = K;
+  p.K = N;
+  p.f32 = dtype == TP_F32;
+  return p;
+}
+// dW: math [K, N] = X^T dPre; linear [N, K] = dPre^T X.
+LinGemm dw_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool linear, bool gated) {
+  LinGemm p;
+  p.mode = gated ? kModePair : kModeOne;
+  p.a_t = 1;
+  p.M = linear ? N : K;
+  p.N = linear ? K : N;
+  p.K = M;
+  p.f32 = dtype == TP_F32;
+  return p;
+}
+
+// Workspace of a backward: the gradients at the activation in the operands' type
+// (where a product reads them) and the bias gradient's partial rows, which a call
+// cannot do without, then what the products need to split K, used where it is
+// there (and, without the rest, aligned).
+struct BwdWs {
+  int64_t d_pre = 0, d_up = 0, parts = 0, join = 0, total = 0;   // offsets; total: bytes
+  bool keeps = false;                                            // d_pre is written
+  int64_t used(const void *ws, int64_t bytes) const {
+    return ws && bytes >= total && (reinterpret_cast<uintptr_t>(ws) & 15) == 0 ? total : join;
+  }
 };
-LinearWs linear_ws(const tp_linear_bwd_args *a) {
-  LinearWs w;
-  if (a->act != TP_ACT_NONE && (a->dX || a->dW)) w.d_pre = a->M * a->N * dtype_size(a->dtype);
-  w.parts = round_up(w.d_pre, kWsAlign);
-  w.total = a->dbias ? w.parts + act_grad_slabs(a->M, a->N) * a->N * 4 : w.d_pre;
+BwdWs linear_ws(const tp_linear_bwd_args *a) {
+  const bool linear = a->weight_layout == TP_WEIGHTS_LINEAR;
+  BwdWs w;
+  w.keeps = a->act != TP_ACT_NONE && (a->dX || a->dW) && a->M > 0;
+  w.parts = w.keeps ? round_up(a->M * a->N * dtype_size(a->dtype), kWsAlign) : 0;
+  w.join = w.parts + (a->dbias ? round_up(act_grad_slabs(a->M, a->N) * a->N * 4, kWsAlign) : 0);
+  const int64_t x = a->dX ? lin_gemm_ws(dx_product(a->M, a->N, a->K, a->dtype, linear, false)) : 0;
+  const int64_t y = a->dW ? lin_gemm_ws(dw_product(a->M, a->N, a->K, a->dtype, linear, false)) : 0;
+  w.total = w.join + std::max(x, y);
+  return w;
+}
+// (Enough for either weight layout and any of the gradients.)
+BwdWs gated_ws(int64_t M, int64_t F, int64_t K, int32_t dtype) {
+  BwdWs w;
+  w.keeps = M > 0;
+  w.d_up = round_up(M * F * dtype_size(dtype), kWsAlign);
+  w.join = 2 * w.d_up;
+  int64_t most = 0;
+  for (const bool linear : {false, true})
+    most = std::max(most, std::max(lin_gemm_ws(dx_product(M, F, K, dtype, linear, true)),
+                                   lin_gemm_ws(dw_product(M, F, K, dtype, linear, true))));
+  w.total = w.join + most;
   return w;
 }
 
@@ -237,71 +284,68 @@ int tp_linear_backward(const tp_linear_bwd_args *a, tp_stream_t stream) {
       (rc = take(&dw, "dW", a->dW, wr, wc, a->dW_ld, dtype_size(a->dw_dtype), false)) != TP_OK ||
       (rc = take(&db, "dbias", a->dbias, 1, N, 0, 4, false)) != TP_OK)
     return rc;
-  const LinearWs ws = linear_ws(a);
-  if ((rc = check_ws(a->ws, a->ws_bytes, ws.total)) != TP_OK) return rc;
-  const Mat wsm{ws.total ? a->ws : nullptr, 1, ws.total, ws.total, 1, "ws"};
+  const BwdWs ws = linear_ws(a);
+  if ((rc = check_ws(a->ws, a->ws_bytes, ws.join)) != TP_OK) return rc;
+  const int64_t used = ws.used(a->ws, a->ws_bytes);
+  const Mat wsm{used ? a->ws : nullptr, 1, used, used, 1, "ws"};
   if ((rc = disjoint({x, w, d, pre}, {dx, dw, db, wsm})) != TP_OK) return rc;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
+  char *base = static_cast<char *>(a->ws);
+  uint32_t *tickets = used > ws.join ? reinterpret_cast<uint32_t *>(base + ws.join) : nullptr;
   const void *d_pre = d.p;
   int64_t ld_pre = d.ld;
-  if (ws.total || a->dbias) {
+  if (ws.keeps || a->dbias) {
     ActGrad g;
     g.d_out = d.p;
     g.ld_dout = d.ld;
     g.pre = acts ? pre.p : nullptr;
     g.ld_pre = pre.ld;
-    g.d_pre = ws.d_pre ? a->ws : nullptr;
+    g.d_pre = ws.keeps ? base : nullptr;
     g.M = M;
     g.N = N;
-    g.parts = a->dbias ? reinterpret_cast<float *>(static_cast<char *>(a->ws) + ws.parts) : nullptr;
+    g.parts = a->dbias && any ? reinterpret_cast<float *>(base + ws.parts) : nullptr;
     g.colsum = a->dbias;
     g.f32 = a->dtype == TP_F32;
     g.act = a->act;
     g.accumulate = a->accumulate;
+    g.tickets = tickets;
     hipEvent_t t0 = timing_begin(s);
     const hipError_t e = act_grad_launch(g, s);
     if (e != hipSuccess) return hip_fail(e, "activation gradient launch");
     timing_end(t0, s, TP_KERNEL_REDUCE,
-               static_cast<double>(es) * M * N * (1 + acts + (ws.d_pre ? 1 : 0)) + (a->dbias ? 4.0 * N : 0.0));
-    if (ws.d_pre) {
-      d_pre = a->ws;
+               static_cast<double>(es) * M * N * (1 + acts + ws.keeps) + (a->dbias ? 4.0 * N : 0.0));
+    if (ws.keeps) {
+      d_pre = base;
       ld_pre = N;
     }
+  } else if (tickets) {
+    const hipError_t e = zero_tickets_launch(tickets, s);
+    if (e != hipSuccess) return hip_fail(e, "ticket launch");
   }
   const double flops = 2.0 * M * N * K;
   if (a->dX && any) {
-    LinGemm p;   // [M, K] = dPre [M, N] times W^T [N, K]
+    LinGemm p = dx_product(M, N, K, a->dtype, linear, false);
     p.a = d_pre;
     p.lda = ld_pre;
     p.w = w.p;
     p.ldw = w.ld;
-    p.w_t = !linear;
     p.c = a->dX;
     p.ldc = dx.ld;
-    p.M = M;
-    p.N = K;
-    p.K = N;
-    p.f32 = a->dtype == TP_F32;
     p.c_f32 = a->dx_dtype == TP_F32;
-    if ((rc = launch(p, s, TP_KERNEL_GEMM_DGRAD, flops, "dX launch")) != TP_OK) return rc;
+    if ((rc = launch(p, s, TP_KERNEL_GEMM_DGRAD, flops, "dX launch", tickets, used - ws.join)) != TP_OK) return rc;
   }
   if (a->dW) {
-    LinGemm p;   // math: [K, N] = X^T dPre; linear: [N, K] = dPre^T X
+    LinGemm p = dw_product(M, N, K, a->dtype, linear, false);
     p.a = linear ? d_pre : x.p;
     p.lda = linear ? ld_pre : x.ld;
     p.w = linear ? x.p : d_pre;
     p.ldw = linear ? x.ld : ld_pre;
-    p.a_t = 1;
     p.c = a->dW;
     p.ldc = dw.ld;
-    p.M = wr;
-    p.N = wc;
-    p.K = M;
-    p.f32 = a->dtype == TP_F32;
     p.c_f32 = a->dw_dtype == TP_F32;
     p.acc_c = a->accumulate;
-    if ((rc = launch(p, s, TP_KERNEL_GEMM_WGRAD, flops, "dW launch")) != TP_OK) return rc;
+    if ((rc = launch(p, s, TP_KERNEL_GEMM_WGRAD, flops, "dW launch", tickets, used - ws.join)) != TP_OK) return rc;
   }
   return TP_OK;
 }
@@ -353,7 +397,7 @@ int tp_gated_linear_backward_ws(const tp_gated_bwd_args *a, int64_t *bytes) {
   if (!a || !bytes) return fail(TP_ERR_ARG, "args or bytes is NULL");
   const int rc = check_common(a->dtype, a->act, a->weight_layout, a->M, a->F, a->K, "F");
   if (rc != TP_OK) return rc;
-  *bytes = 2 * round_up(a->M * a->F * dtype_size(a->dtype), kWsAlign);
+  *bytes = gated_ws(a->M, a->F, a->K, a->dtype).total;
   return TP_OK;
 }
 
@@ -381,13 +425,15 @@ int tp_gated_linear_backward(const tp_gated_bwd_args *a, tp_stream_t stream) {
       (rc = take(&dwg, "dW_gate", a->dW_gate, wr, wc, a->dW_ld, dwes, false)) != TP_OK ||
       (rc = take(&dwu, "dW_up", a->dW_up, wr, wc, a->dW_ld, dwes, false)) != TP_OK)
     return rc;
-  const int64_t half = round_up(M * F * es, kWsAlign), need = 2 * half;
-  if ((rc = check_ws(a->ws, a->ws_bytes, need)) != TP_OK) return rc;
-  const Mat wsm{need ? a->ws : nullptr, 1, need, need, 1, "ws"};
+  const BwdWs ws = gated_ws(M, F, K, a->dtype);
+  if ((rc = check_ws(a->ws, a->ws_bytes, ws.join)) != TP_OK) return rc;
+  const int64_t used = ws.used(a->ws, a->ws_bytes);
+  const Mat wsm{used ? a->ws : nullptr, 1, used, used, 1, "ws"};
   if ((rc = disjoint({x, wg, wu, g, u, d}, {dx, dwg, dwu, wsm})) != TP_OK) return rc;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
-  char *d_gate = static_cast<char *>(a->ws), *d_up = d_gate + half;
+  char *d_gate = static_cast<char *>(a->ws), *d_up = d_gate + ws.d_up;
+  uint32_t *tickets = used > ws.join ? reinterpret_cast<uint32_t *>(d_gate + ws.join) : nullptr;
   if (any) {
     ActGrad q;
     q.d_out = d.p;
@@ -402,51 +448,43 @@ int tp_gated_linear_backward(const tp_gated_bwd_args *a, tp_stream_t stream) {
     q.f32 = a->dtype == TP_F32;
     q.act = a->act;
     q.gated = 1;
+    q.tickets = tickets;
     hipEvent_t t0 = timing_begin(s);
     const hipError_t e = act_grad_launch(q, s);
     if (e != hipSuccess) return hip_fail(e, "activation gradient launch");
     timing_end(t0, s, TP_KERNEL_REDUCE, 5.0 * es * M * F);
+  } else if (tickets) {
+    const hipError_t e = zero_tickets_launch(tickets, s);
+    if (e != hipSuccess) return hip_fail(e, "ticket launch");
   }
   const double flops = 4.0 * M * F * K;
   if (a->dX && any) {
-    LinGemm p;   // [M, K] = dGate W_gate^T + dUp W_up^T
-    p.mode = kModeCat;
+    LinGemm p = dx_product(M, F, K, a->dtype, linear, true);
     p.a = d_gate;
     p.a2 = d_up;
     p.lda = F;
     p.w = wg.p;
     p.w2 = wu.p;
     p.ldw = wg.ld;
-    p.w_t = !linear;
     p.c = a->dX;
     p.ldc = dx.ld;
-    p.M = M;
-    p.N = K;
-    p.K = F;
-    p.f32 = a->dtype == TP_F32;
     p.c_f32 = a->dx_dtype == TP_F32;
-    if ((rc = launch(p, s, TP_KERNEL_GEMM_DGRAD, flops, "dX launch")) != TP_OK) return rc;
+    if ((rc = launch(p, s, TP_KERNEL_GEMM_DGRAD, flops, "dX launch", tickets, used - ws.join)) != TP_OK) return rc;
   }
   if (a->dW_gate) {
-    LinGemm p;
-    p.mode = kModePair;
+    LinGemm p = dw_product(M, F, K, a->dtype, linear, true);
     p.a = linear ? d_gate : x.p;
     p.a2 = linear ? d_up : x.p;
     p.lda = linear ? F : x.ld;
     p.w = linear ? x.p : d_gate;
     p.w2 = linear ? x.p : d_up;
     p.ldw = linear ? x.ld : F;
-    p.a_t = 1;
     p.c = a->dW_gate;
     p.c2 = a->dW_up;
     p.ldc = dwg.ld;
-    p.M = wr;
-    p.N = wc;
-    p.K = M;
-    p.f32 = a->dtype == TP_F32;
     p.c_f32 = a->dw_dtype == TP_F32;
     p.acc_c = a->accumulate;
-    if ((rc = launch(p, s, TP_KERNEL_GEMM_WGRAD, flops, "dW launch")) != TP_OK) return rc;
+    if ((rc = launch(p, s, TP_KERNEL_GEMM_WGRAD, flops, "dW launch", tickets, used - ws.join)) != TP_OK) return rc;
   }
   return TP_OK;
 }

@@ -154,20 +154,27 @@ __device__ __forceinline__ bool last_of_tile(uint32_t *ticket, uint32_t splits) 
   return true;
 }
 
-// Sum over `splits` partials, `pitch` elements apart, in order; eight loads in
-// flight at a time.
-template <typename V>
-__device__ __forceinline__ V sum_partials(const V *p, int64_t pitch, int splits) {
-  V v[8], s{};
-  for (int y0 = 0; y0 < splits; y0 += 8) {
+// out[i] = sum over y < splits, in order, of p[y * pitch + i * step], with at
+// least eight loads in flight at a time (a round trip to the memory side each batch).
+template <int N, typename V>
+__device__ __forceinline__ void sum_partials(const V *p, int64_t pitch, int64_t step, int splits, V (&out)[N]) {
+  constexpr int Y = N >= 8 ? 1 : 8 / N;   // splits of a batch
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      if (y0 + y < splits) v[y] = get_partial(p + (y0 + y) * pitch);
+  for (int i = 0; i < N; ++i) out[i] = V{};
+  for (int y0 = 0; y0 < splits; y0 += Y) {
+    V v[Y][N];
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      if (y0 + y < splits) s = s + v[y];
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (y0 + y < splits) v[y][i] = get_partial(p + (y0 + y) * pitch + i * step);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (y0 + y < splits) out[i] = out[i] + v[y][i];
   }
-  return s;
 }
 
 // The accumulators of workgroup (blockIdx.x, blockIdx.y): left as a partial; true
@@ -186,16 +193,14 @@ __device__ __forceinline__ bool join_splits(const LinGemm& p, f32x4 (&acc)[TM][T
       for (int h = 0; h < 2; ++h)
         put_partial(mine + ((i * TN + j) * 2 + h) * THREADS, f32x2{acc[i][j][2 * h], acc[i][j][2 * h + 1]});
   if (!last_of_tile(p.tickets + blockIdx.x, splits)) return false;
+  f32x2 sum[TM * TN * 2];
+  sum_partials(tile, PITCH, THREADS, splits, sum);
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x2 s = sum_partials(tile + ((i * TN + j) * 2 + h) * THREADS, PITCH, splits);
-        acc[i][j][2 * h] = s[0];
-        acc[i][j][2 * h + 1] = s[1];
-      }
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = sum[(i * TN + j) * 2 + e / 2][e % 2];
   return true;
 }
 

@@ -270,10 +270,11 @@ __global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
       const int64_t n = n0 + i % TC;
       if (n >= p.N) continue;
       float v[MATS];
+      if (from) {
+        sum_partials(from + i, cells, M * TC, splits, v);
+      } else {
 #pragma unroll
-      for (int a = 0; a < MATS; ++a) {
-        const int cell = a * M * TC + i;
-        v[a] = from ? sum_partials(from + cell, cells, splits) : joined(cell);
+        for (int a = 0; a < MATS; ++a) v[a] = joined(a * M * TC + i);
       }
       auto put = [&](void *base, int64_t at, float y, bool f32) {
         if (f32) static_cast<float *>(base)[at] = y;

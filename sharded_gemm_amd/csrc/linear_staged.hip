@@ -18,6 +18,8 @@
 // bf16: v_mfma_f32_16x16x32_bf16.  fp32: v_mfma_f32_16x16x4_f32, four per
 // 16-byte chunk; a lane group's chunk holds four consecutive k, which the four
 // MFMAs take in turn (the order of a sum over k is free, and A and W agree).
+#include <algorithm>
+
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -101,21 +103,23 @@ struct Tile {
     }
   }
 
-  // `shift`: from the first matrix to the one read (elements).
-  __device__ __forceinline__ void load(int64_t k0, int64_t K, int64_t shift, u32x4 (&g)[KB]) const {
+  // Stages that lie inside K as above.
+  __device__ __forceinline__ static int64_t inside(int64_t K) { return K >= V ? (K - V) / BK : 0; }
+
+  // The stage from k0 on; `shift`: from the first matrix to the one read (elements).
+  __device__ __forceinline__ void load(int64_t k0, int64_t shift, u32x4 (&g)[KB]) const {
+#pragma unroll
+    for (int q = 0; q < KB; ++q)
+      g[q] = *reinterpret_cast<const u32x4_any *>(KC ? at[KC ? q : 0] + shift + k0 : at[0] + shift + (k0 + q) * ld);
+  }
+  __device__ __forceinline__ void load_checked(int64_t k0, int64_t K, int64_t shift, u32x4 (&g)[KB]) const {
     const int t = threadIdx.x;
-    if (k0 + BK + V <= K) {
 #pragma unroll
-      for (int q = 0; q < KB; ++q)
-        g[q] = *reinterpret_cast<const u32x4_any *>(KC ? at[KC ? q : 0] + shift + k0 : at[0] + shift + (k0 + q) * ld);
-    } else {
-#pragma unroll
-      for (int q = 0; q < KB; ++q) {
-        if constexpr (KC) {
-          g[q] = load16<T>(at[q] + shift + k0, K - k0 - ((t + kThreads * q) & 7) * V);
-        } else {
-          g[q] = load16<T>(at[0] + shift + (k0 + q) * ld, k0 + t / NBLK * KB + q < K ? left : 0);
-        }
+    for (int q = 0; q < KB; ++q) {
+      if constexpr (KC) {
+        g[q] = load16<T>(at[q] + shift + k0, K - k0 - ((t + kThreads * q) & 7) * V);
+      } else {
+        g[q] = load16<T>(at[0] + shift + (k0 + q) * ld, k0 + t / NBLK * KB + q < K ? left : 0);
       }
     }
   }
@@ -151,7 +155,7 @@ struct Tile {
 };
 
 template <typename T, int BM, int BN, bool AKC, bool WKC, int MODE>
-__global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
+__global__ void __launch_bounds__(kThreads, 2) lin_staged_kernel(LinGemm p) {
   using TA = Tile<T, BM, AKC>;
   using TW = Tile<T, BN, WKC>;
   constexpr int BK = TA::BK;
@@ -192,74 +196,133 @@ __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int64_t per = (p.K + BK - 1) / BK, all = MODE == kModeCat ? 2 * per : per;
-  const int64_t st0 = all * blockIdx.y / gridDim.y, nst = all * (blockIdx.y + 1) / gridDim.y - st0;
-  const int64_t a_far = MODE == kModeCat ? static_cast<const T *>(p.a2) - A : 0, w_far = MODE == kModeCat ? W2 - W : 0;
   struct Regs {
     u32x4 a[TA::KB], w[TW::KB];
-  };
-  auto fetch = [&](int64_t st, Regs& g) {
-    st += st0;
-    const bool far = MODE == kModeCat && st >= per;
-    const int64_t k0 = (far ? st - per : st) * BK;
-    ta.load(k0, p.K, far ? a_far : 0, g.a);
-    tw.load(k0, p.K, far ? w_far : 0, g.w);
   };
   auto put = [&](int64_t st, const Regs& g) {
     char *slot = smem + (st & 1) * STAGE;
     TA::store(slot, g.a);
     TW::store(slot + LDS_A, g.w);
   };
+  // All of a stage's fragments are read before its products where they fit
+  // the registers (64 x 64).
+  constexpr int AHEAD = BM == 64 ? 2 : 1;
   auto compute = [&](const char *stage) {
     const char *As = stage, *Ws = stage + LDS_A;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int ch = kk * 4 + (lane >> 4);
-      u32x4 fa[TM], fw[TN];
+    for (int k0 = 0; k0 < 2; k0 += AHEAD) {
+      u32x4 fa[AHEAD][TM], fw[AHEAD][TN];
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-        fa[i] = *reinterpret_cast<const u32x4 *>(As + lds_at(wm * WM + i * 16 + (lane & 15), ch));
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fw[j] = *reinterpret_cast<const u32x4 *>(Ws + lds_at(wn * WN + j * 16 + (lane & 15), ch));
-      if constexpr (sizeof(T) == 2) {
+      for (int kk = 0; kk < AHEAD; ++kk) {
+        const int ch = (k0 + kk) * 4 + (lane >> 4);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
+          fa[kk][i] = *reinterpret_cast<const u32x4 *>(As + lds_at(wm * WM + i * 16 + (lane & 15), ch));
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fw[j]),
-                                                                __builtin_bit_cast(bf16x8, fa[i]), acc[i][j], 0, 0, 0);
-      } else {
+        for (int j = 0; j < TN; ++j)
+          fw[kk][j] = *reinterpret_cast<const u32x4 *>(Ws + lds_at(wn * WN + j * 16 + (lane & 15), ch));
+      }
+      if constexpr (AHEAD == 2) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+      for (int kk = 0; kk < AHEAD; ++kk) {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
           for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fw[j][e]), __uint_as_float(fa[i][e]),
-                                                               acc[i][j], 0, 0, 0);
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fw[kk][j]),
+                                                                  __builtin_bit_cast(bf16x8, fa[kk][i]), acc[i][j], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+              for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fw[kk][j][e]), __uint_as_float(fa[kk][i][e]),
+                                                                 acc[i][j], 0, 0, 0);
+        }
       }
     }
   };
 
-  // Stage st + 2 leaves for the registers that stage st has left, stage st + 1
-  // moves from its own to LDS after stage st's products: a load has two stages'
-  // time to arrive.
-  Regs g0, g1;
-  auto step = [&](int64_t st, Regs& mine, const Regs& next) {
-    if (st + 2 < nst) fetch(st + 2, mine);
-    compute(smem + (st & 1) * STAGE);
-    if (st + 1 < nst) put(st + 1, next);
-    __syncthreads();
+  // Stages [first, last) of one pair of matrices.  64 x 64: stage st + 2 leaves
+  // for the registers that stage st has left, stage st + 1 moves from its own to
+  // LDS after stage st's products, so a load has two stages' time to arrive.
+  // 128 x 128 has registers for one stage of it (two spilled: 4097^3 bf16 350 us).
+  // The unchecked stages have a loop of their own: where both kinds of fetch
+  // meet, the compiler waits for the newest load too.
+  auto run = [&](int64_t first, int64_t last, int64_t a_shift, int64_t w_shift) {
+    const int64_t nst = last - first;
+    if (nst <= 0) return;
+    Regs g0, g1;
+    auto fetch = [&](int64_t st, Regs& g) {
+      ta.load((first + st) * BK, a_shift, g.a);
+      tw.load((first + st) * BK, w_shift, g.w);
+    };
+    auto fetch_checked = [&](int64_t st, Regs& g) {
+      ta.load_checked((first + st) * BK, p.K, a_shift, g.a);
+      tw.load_checked((first + st) * BK, p.K, w_shift, g.w);
+    };
+    const int64_t free = min(TA::inside(p.K), last) - first;   // leading stages without checks
+    if constexpr (BM == 128) {
+      if (free > 0) fetch(0, g0); else fetch_checked(0, g0);
+      put(0, g0);
+      __syncthreads();
+      int64_t st = 0;
+      for (; st + 1 < free; ++st) {
+        fetch(st + 1, g0);
+        compute(smem + (st & 1) * STAGE);
+        put(st + 1, g0);
+        __syncthreads();
+      }
+      for (; st < nst; ++st) {
+        if (st + 1 < nst) fetch_checked(st + 1, g0);
+        compute(smem + (st & 1) * STAGE);
+        if (st + 1 < nst) put(st + 1, g0);
+        __syncthreads();
+      }
+      return;
+    }
+    auto step = [&](int64_t st, Regs& mine, const Regs& next) {
+      if (st + 2 < nst) fetch_checked(st + 2, mine);
+      compute(smem + (st & 1) * STAGE);
+      if (st + 1 < nst) put(st + 1, next);
+      __syncthreads();
+    };
+    int64_t st = 0;
+    if (free >= 2) {
+      fetch(0, g0);
+      fetch(1, g1);
+      put(0, g0);
+      __syncthreads();
+      for (; st + 3 < free; st += 2) {
+        fetch(st + 2, g0);
+        compute(smem);
+        put(1, g1);
+        __syncthreads();
+        fetch(st + 3, g1);
+        compute(smem + STAGE);
+        put(0, g0);
+        __syncthreads();
+      }
+    } else {
+      fetch_checked(0, g0);
+      if (nst > 1) fetch_checked(1, g1);
+      put(0, g0);
+      __syncthreads();
+    }
+    for (; st < nst; st += 2) {
+      step(st, g0, g1);
+      if (st + 1 < nst) step(st + 1, g1, g0);
+    }
   };
-  if (nst > 0) fetch(0, g0);
-  if (nst > 1) fetch(1, g1);
-  if (nst > 0) put(0, g0);
-  __syncthreads();
-  for (int64_t st = 0; st < nst; st += 2) {
-    step(st, g0, g1);
-    if (st + 1 < nst) step(st + 1, g1, g0);
-  }
+  // This workgroup's share of the stages, over both pairs of matrices in kModeCat.
+  const int64_t per = (p.K + BK - 1) / BK, all = MODE == kModeCat ? 2 * per : per;
+  const int64_t st0 = all * blockIdx.y / gridDim.y, st1 = all * (blockIdx.y + 1) / gridDim.y;
+  run(st0, min(st1, per), 0, 0);
+  if constexpr (MODE == kModeCat)
+    run(max(st0 - per, int64_t{0}), st1 - per, static_cast<const T *>(p.a2) - A, W2 - W);
   if (gridDim.y > 1 && !join_splits<kThreads>(p, acc)) return;
 
   auto rm = [&](int i) -> int64_t { return m0 + wm * WM + i * 16 + (lane & 15); };
@@ -273,20 +336,37 @@ __global__ void __launch_bounds__(kThreads) lin_staged_kernel(LinGemm p) {
 
 constexpr int64_t kCUs = 256;
 
-// The tile's edge (128 where every CU gets such a tile, else 64) and the
-// workgroups that split its K.
+// The tile's edge and the workgroups that split its K, by estimated time.  With
+// k workgroups to the busiest CU a stage takes max(alone, k * shared) us, and
+// joining S > 1 splits 2 us and 7 ns a workgroup (their partials' trip to memory
+// and back).  The constants are fitted to MI355X times, e.g. (bf16 / fp32)
+// 2049 x 2047 x 2049: edge 128 62 / 282 us, edge 64 71 / 194; 100 x 4097 x 2049: 29 / 88
+// unsplit, 16 / 36 with three splits; 515 x 1021 x 1531: 13 / 28 unsplit, 20 / 32
+// with four.
 struct Shape {
   int edge, splits;
   int64_t tiles;
 };
-Shape shape_of(const LinGemm& p) {
-  Shape h{128, 1, lin_tiles_count(p, 128, 128)};
-  if (h.tiles >= kCUs) return h;
-  h.edge = 64;
-  h.tiles = lin_tiles_count(p, 64, 64);
+Shape shape_of(const LinGemm& p, bool may_split) {
   const int64_t stages = (p.K * (p.f32 ? 4 : 2) + kRow - 1) / kRow * (p.mode == kModeCat ? 2 : 1);
-  while (h.splits < 16 && h.tiles * h.splits < 2 * kCUs && stages >= 2 * h.splits * 8) h.splits *= 2;
-  return h;
+  Shape best{64, 1, 0};
+  double least = 0.0;
+  for (int edge = 128; edge >= 64; edge -= 64) {
+    const double shared = p.f32 ? (edge == 128 ? 2.1 : 0.58) : (edge == 128 ? 0.92 : 0.38);
+    const double alone = p.f32 ? (edge == 128 ? 2.6 : 0.72) : (edge == 128 ? 1.8 : 0.55);
+    const int64_t tiles = lin_tiles_count(p, edge, edge);
+    // Only 64 x 64 tiles are split, few enough for a ticket each, down to 4 stages.
+    for (int s = 1; s <= 16 && (s == 1 || (may_split && edge == 64 && tiles <= kMaxTickets && 4 * s <= stages)); ++s) {
+      const int64_t k = (tiles * s + kCUs - 1) / kCUs;
+      const double t = static_cast<double>((stages + s - 1) / s) * std::max(alone, shared * static_cast<double>(k)) +
+                       (s > 1 ? 2.0 + 0.007 * static_cast<double>(tiles * s) : 0.0);
+      if (!best.tiles || t < least) {
+        best = {edge, s, tiles};
+        least = t;
+      }
+    }
+  }
+  return best;
 }
 
 template <typename T, bool AKC, bool WKC, int MODE>
@@ -325,14 +405,13 @@ hipError_t dispatch(const LinGemm& p, const Shape& h, hipStream_t s) {
 bool lin_grid_ok(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22); }
 
 int64_t lin_staged_ws(const LinGemm& p) {
-  const Shape h = shape_of(p);
+  const Shape h = shape_of(p, true);
   return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * 64 * 64 * 4 : 0;
 }
 
 hipError_t lin_staged_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  Shape h = shape_of(p);
-  if (!ws || ws_bytes < lin_staged_ws(p)) h.splits = 1;
+  const Shape h = shape_of(p, ws && ws_bytes >= lin_staged_ws(p));
   if (h.splits > 1) {
     p.tickets = static_cast<uint32_t *>(ws);
     p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);

@@ -417,6 +417,56 @@ def test_graph_replays_and_streams(shape):
         step(torch.cuda.current_stream())
 
 
+# Few rows and few tiles with a long K: the products split K and join through the workspace.
+SPLIT = [(1, 4096, 256, BF16, MATH), (3, 2056, 130, BF16, MATH), (16, 4100, 65, BF16, LINEAR), (1, 3000, 96, F32, MATH),
+         (9, 1030, 50, F32, LINEAR), (40, 4096, 256, BF16, LINEAR), (64, 4096, 192, BF16, MATH), (100, 2080, 120, BF16, MATH),
+         (100, 4097, 129, BF16, MATH), (70, 2051, 100, F32, LINEAR), (130, 1111, 77, F32, MATH)]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=[str(c[:3]) for c in SPLIT])
+def test_split_k(case):
+    """With a workspace the result is within the same bounds, the same every time, and the workspace stays fit for the
+    next call, also of another shape."""
+    M, K, N, dtype, layout = case
+    announce(f"split {case}")
+    X, W, W2 = rnd((M, K), 1, dtype), rnd((K, N), 2, dtype, (2.0 / K) ** 0.5), rnd((K, N), 3, dtype, (2.0 / K) ** 0.5)
+    Xd, Wd, W2d = X.cuda(), lay(W, layout).cuda(), lay(W2, layout).cuda()
+    ws1, ws2 = tp.tp_linear_ws(Xd, Wd, weight_layout=layout), tp.tp_gated_linear_ws(Xd, Wd, weight_layout=layout)
+    assert ws1.numel() > 0 and ws2.numel() > 0
+    ws = torch.zeros(max(ws1.numel(), ws2.numel()), dtype=torch.uint8, device="cuda")
+    out, both = Guarded((M, N), dtype), Guarded((M, N), dtype)
+    ref, pre = O.linear(f64(X), f64(W), kind=tp.TP_ACT_SILU)
+    e = SLOPE * product_err(f64(X), f64(W), K) + ACT_ERR * (1 + np.abs(pre)) + 2 * U32 * np.abs(ref)
+    gref, rg, ru = O.gated(f64(X), f64(W), f64(W2), tp.TP_ACT_SILU)
+    eu = product_err(f64(X), f64(W2), K)
+    eg = e * (np.abs(ru) + eu) + np.abs(ref) * eu + 2 * U32 * np.abs(gref)
+    first = None
+    for _ in range(4):
+        out.fill_sentinel()
+        both.fill_sentinel()
+        tp.tp_linear(Xd, Wd, out.t, act=tp.TP_ACT_SILU, weight_layout=layout, ws=ws)
+        tp.tp_gated_linear(Xd, Wd, W2d, both.t, weight_layout=layout, ws=ws)
+        torch.cuda.synchronize()
+        assert out.guards_intact() and both.guards_intact()
+        got = (bits(out.t), bits(both.t))
+        first = first or got
+        assert all(np.array_equal(a, b) for a, b in zip(first, got))
+    check(out.t, ref, e + u(dtype) * (np.abs(ref) + e), "out")
+    check(both.t, gref, eg + u(dtype) * (np.abs(gref) + eg), "gated out")
+
+
+@pytest.mark.parametrize("shape", [(8, 128, 96), (2048, 64, 96), (4100, 40, 72), (3000, 33, 65), (16, 512, 2048)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", [MATH, LINEAR])
+def test_split_k_backward(shape, dtype, layout):
+    """Many tokens against a small weight (and few against a wide one): the backward's products split K."""
+    announce(f"split backward {shape} {dtype} layout {layout}")
+    run_linear_bwd(*shape, dtype, layout, tp.TP_ACT_SILU, seed=120)
+    run_linear_bwd(*shape, dtype, layout, tp.TP_ACT_NONE, seed=121, dbias=False)
+    run_linear_bwd(*shape, dtype, layout, tp.TP_ACT_NONE, seed=122, dw_f32=True, accumulate=True)
+    run_gated_bwd(*shape, dtype, layout, tp.TP_ACT_GELU_ERF, seed=123)
+
+
 def test_prepared_calls():
     M, K, N = 33, 64, 48
     X, W = rnd((M, K), 1, BF16).cuda(), rnd((K, N), 2, BF16).cuda()
