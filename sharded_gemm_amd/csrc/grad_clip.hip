@@ -13,6 +13,8 @@
 //
 // The tensors' pointers travel in the kernel's arguments, kMaxTensors a launch:
 // no table in device memory, nothing to copy, and a captured graph keeps them.
+#include <vector>
+
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -108,9 +110,83 @@ __global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(Table t, double *p
   if (threadIdx.x == 0) parts[blockIdx.x] = add ? parts[blockIdx.x] + s : s;
 }
 
+// One chunk of one tensor: loaded, then scaled and stored.
+struct Chunk {
+  u32x4 v[kPer / 4];
+  const void *g;
+  void *out;
+  int64_t at, left;
+  bool f32;
+};
+
+__device__ __forceinline__ void chunk_load(const Table& t, int64_t u, int i, Chunk& c) {
+  c.g = t.g[i];
+  c.out = t.out[i];
+  c.at = (u - t.first[i]) * kChunk;
+  c.left = t.n[i] - c.at;
+  c.f32 = t.f32 >> i & 1;
+  if (c.left < kChunk) return;
+  if (c.f32) {
+    const uint32_t *g = static_cast<const uint32_t *>(c.g) + c.at;
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) c.v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 4);
+  } else {
+    const uint16_t *g = static_cast<const uint16_t *>(c.g) + c.at;
+#pragma unroll
+    for (int q = 0; q < kPer / 8; ++q) c.v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 8);
+  }
+}
+
+__device__ __forceinline__ void chunk_store(Chunk& c, float scale) {
+  // Nothing below its limit changes where it lies.
+  if (scale == 1.0f && c.out == c.g) return;
+  if (c.f32) {
+    const uint32_t *g = static_cast<const uint32_t *>(c.g) + c.at;
+    uint32_t *o = static_cast<uint32_t *>(c.out) + c.at;
+    if (c.left >= kChunk) {
+#pragma unroll
+      for (int q = 0; q < kPer / 4; ++q) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c.v[q][e] = __float_as_uint(__uint_as_float(c.v[q][e]) * scale);
+        __builtin_nontemporal_store(c.v[q], reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 4));
+      }
+    } else {
+      for (int64_t e = threadIdx.x; e < c.left; e += kThreads) o[e] = __float_as_uint(__uint_as_float(g[e]) * scale);
+    }
+  } else {
+    const uint16_t *g = static_cast<const uint16_t *>(c.g) + c.at;
+    uint16_t *o = static_cast<uint16_t *>(c.out) + c.at;
+    if (c.left >= kChunk) {
+#pragma unroll
+      for (int q = 0; q < kPer / 8; ++q) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          c.v[q][e] = pack2(from_bf16(c.v[q][e] & 0xffffu) * scale, from_bf16(c.v[q][e] >> 16) * scale);
+        __builtin_nontemporal_store(c.v[q], reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 8));
+      }
+    } else {
+      for (int64_t e = threadIdx.x; e < c.left; e += kThreads) o[e] = to_bf16(from_bf16(g[e]) * scale);
+    }
+  }
+}
+
+// Chunks are taken from the last to the first: the pass before went from first
+// to last, and what it read last is still in the 256 MB cache on the memory side.
+// The first chunk is on its way while the norm is added up.
 __global__ void __launch_bounds__(kThreads) grad_clip_kernel(Table t, const double *parts, int64_t ranks,
                                                              double max_norm, double eps, float *norm_out) {
   __shared__ double lds[kThreads / 64];
+  const int64_t chunks = t.first[t.num];
+  int64_t u = chunks - 1 - blockIdx.x;
+  int i = t.num - 1;
+  auto find = [&]() {
+    while (u < t.first[i]) --i;
+  };
+  Chunk c;
+  if (u >= 0) {
+    find();
+    chunk_load(t, u, i, c);
+  }
   double s = 0.0;
   for (int64_t q = threadIdx.x; q < ranks * kGradParts; q += kThreads) s += parts[q];
   const double norm = sqrt(block_sum(s, lds));
@@ -118,48 +194,12 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(Table t, const doub
   // A NaN norm makes a NaN scale; an infinite one a scale of zero.
   const double want = max_norm / (norm + eps);
   const float scale = want >= 1.0 ? 1.0f : static_cast<float>(want);
-  int i = 0;
-  for (int64_t u = blockIdx.x; u < t.first[t.num]; u += gridDim.x) {
-    i = tensor_of(t, u, i);
-    // Nothing below its limit changes where it lies.
-    if (scale == 1.0f && t.out[i] == t.g[i]) continue;
-    const int64_t at = (u - t.first[i]) * kChunk, left = t.n[i] - at;
-    if (t.f32 >> i & 1) {
-      const uint32_t *g = static_cast<const uint32_t *>(t.g[i]) + at;
-      uint32_t *o = static_cast<uint32_t *>(t.out[i]) + at;
-      if (left >= kChunk) {
-        u32x4 v[kPer / 4];
-#pragma unroll
-        for (int q = 0; q < kPer / 4; ++q)
-          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 4);
-#pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[q][e] = __float_as_uint(__uint_as_float(v[q][e]) * scale);
-          *reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 4) = v[q];
-        }
-      } else {
-        for (int64_t e = threadIdx.x; e < left; e += kThreads) o[e] = __float_as_uint(__uint_as_float(g[e]) * scale);
-      }
-    } else {
-      const uint16_t *g = static_cast<const uint16_t *>(t.g[i]) + at;
-      uint16_t *o = static_cast<uint16_t *>(t.out[i]) + at;
-      if (left >= kChunk) {
-        u32x4 v[kPer / 8];
-#pragma unroll
-        for (int q = 0; q < kPer / 8; ++q)
-          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 8);
-#pragma unroll
-        for (int q = 0; q < kPer / 8; ++q) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[q][e] = pack2(from_bf16(v[q][e] & 0xffffu) * scale, from_bf16(v[q][e] >> 16) * scale);
-          *reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 8) = v[q];
-        }
-      } else {
-        for (int64_t e = threadIdx.x; e < left; e += kThreads) o[e] = to_bf16(from_bf16(g[e]) * scale);
-      }
-    }
+  while (u >= 0) {
+    chunk_store(c, scale);
+    u -= gridDim.x;
+    if (u < 0) break;
+    find();
+    chunk_load(t, u, i, c);
   }
 }
 
@@ -198,9 +238,18 @@ hipError_t grad_sumsq_launch(const GradTensor *ts, int64_t num, double *parts, h
 
 hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *parts, int64_t ranks, double max_norm,
                             double eps, float *norm_out, hipStream_t s) {
-  int64_t at = 0;
+  // The tables of the pass before, from the last to the first.
+  int64_t begin = 0, at = 0;
+  std::vector<int64_t> starts;
   do {
     Table t;
+    begin = at;
+    next_table(ts, num, &at, &t);
+    starts.push_back(begin);
+  } while (at < num);
+  for (size_t k = starts.size(); k-- > 0;) {
+    Table t;
+    at = starts[k];
     next_table(ts, num, &at, &t);
     const int64_t chunks = t.first[t.num];
     const int64_t grid = chunks < 1 ? 1 : chunks < 2048 ? chunks : 2048;
@@ -209,7 +258,7 @@ hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *par
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     norm_out = nullptr;
-  } while (at < num);
+  }
   return hipSuccess;
 }
 

@@ -68,12 +68,13 @@ hipError_t lin_staged_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t 
 // The tiled bf16 kernels, where lin_tiles_ok: 16-byte aligned operands and rows,
 // K a multiple of 32, a row-contiguous operand of whole 8-column groups.
 bool lin_tiles_ok(const LinGemm& p);
-enum Tile { kTile256, kTile192, kTile128w, kTile128, kTile64, kTile64k32 };
+enum Tile { kTile256, kTile192, kTile128w, kTile128, kTile64, kTile64short, kTile64k32 };
 struct TilePick {
   int tile;     // Tile
   int splits;   // workgroups that split a tile's K
 };
 // Tiles of a launch of bm x bn: kModeDual counts both weights' columns, kModePair both products.
+
 inline int64_t lin_tiles_count(const LinGemm& p, int bm, int bn) {
   const int bno = p.mode == kModeDual ? bn / 2 : bn;
   return (p.M + bm - 1) / bm * ((p.N + bno - 1) / bno) * (p.mode == kModePair ? 2 : 1);

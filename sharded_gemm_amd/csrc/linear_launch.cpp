@@ -32,12 +32,13 @@ int64_t small_tiles(const LinGemm& p) { return lin_tiles_count(p, 64, p.mode == 
 
 // The tile: waves of workgroups over the CUs times the tile's work over its
 // relative throughput (measured in gemm.hip).  Problems too small to give every
-// CU a 128 x 128 tile take small ones, several of which share a CU (three stages
-// in flight: 768 -> 768 at 256 rows 7.3 us against 8.9 with two and 7.4 with
-// four, gated 12288 -> 6144 at 256 rows 160 us against 173 and 199), and split
-// K: until there is one for every CU, and on to two where each still has 24
-// stages to pay for the join (gated 4096 -> 2048 at 64 rows: 40 -> 23 us; at 8
-// stages each the second split cost 25 -> 31 us at 128 rows).
+// CU a 128 x 128 tile take small ones, several of which share a CU: with three
+// stages in flight (2048 -> 4096 at 256 rows 12.7 us against 17.4 with two; gated
+// 12288 -> 6144 160 against 173, and 199 with four), or two where a workgroup has
+// at most 16 (1024^3 9.0 us against 10.3).  They split K until there is one for
+// every CU, and on to two where each still has 24 stages to pay for the join
+// (gated 4096 -> 2048 at 64 rows: 40 -> 17 us; at 8 stages each the second split
+// cost 25 -> 31 us at 128 rows).
 TilePick pick(const LinGemm& p) {
   const bool dual = p.mode == kModeDual, k64 = p.K % 64 == 0;
   if (lin_tiles_count(p, 128, 128) < kCUs) {
@@ -46,6 +47,7 @@ TilePick pick(const LinGemm& p) {
     while (t.splits < 16 && stages >= 2 * t.splits * 8 &&
            (tiles * t.splits < kCUs || (tiles * t.splits < 2 * kCUs && stages >= 2 * t.splits * 24)))
       t.splits *= 2;
+    if (k64 && stages <= 16 * t.splits) t.tile = kTile64short;
     return t;
   }
   auto cost = [&](int bm, int bn, double eff) {
