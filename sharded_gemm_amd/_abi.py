@@ -377,7 +377,8 @@ class Prepared:
     the same argument structures again, so a loop pays one C call per launch
     sequence.  It holds references to the tensors it points into, and a replay
     after any of them has moved (resized or re-pointed) raises instead of
-    touching stale memory."""
+    touching stale memory.  Replays follow one another: one that may overlap
+    another (on a second stream) needs a prepared call of its own."""
 
     def __init__(self, fn, args, keep, streams, tensors=()):
         self._fn, self._args, self._keep, self._streams = fn, args, keep, streams

@@ -147,11 +147,11 @@ __device__ __forceinline__ bool last_of_tile(uint32_t *ticket, uint32_t splits) 
   __shared__ uint32_t before;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0) before = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // Counts 0 .. splits - 1 and wraps to 0: even overlapping replays of one call,
+  // which would spoil each other's result, leave the ticket at zero.
+  if (threadIdx.x == 0) before = atomicInc(ticket, splits - 1);
   __syncthreads();
-  if (before + 1 != splits) return false;
-  if (threadIdx.x == 0) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return true;
+  return before + 1 == splits;
 }
 
 // out[i] = sum over y < splits, in order, of p[y * pitch + i * step], with at
