@@ -154,10 +154,10 @@ __device__ __forceinline__ bool last_of_tile(uint32_t *ticket, uint32_t splits) 
   return before + 1 == splits;
 }
 
-// out[i] = sum over y < splits, in order, of p[y * pitch + i * step], with at
-// least eight loads in flight at a time (a round trip to the memory side each batch).
-template <int N, typename V>
-__device__ __forceinline__ void sum_partials(const V *p, int64_t pitch, int64_t step, int splits, V (&out)[N]) {
+// out[i] = sum over y < splits, in order, of p[y * pitch + at(i)], with at least
+// eight loads in flight at a time (a round trip to the memory side each batch).
+template <int N, typename V, typename At>
+__device__ __forceinline__ void sum_partials(const V *p, int64_t pitch, At&& at, int splits, V (&out)[N]) {
   constexpr int Y = N >= 8 ? 1 : 8 / N;   // splits of a batch
 #pragma unroll
   for (int i = 0; i < N; ++i) out[i] = V{};
@@ -167,7 +167,7 @@ __device__ __forceinline__ void sum_partials(const V *p, int64_t pitch, int64_t 
     for (int y = 0; y < Y; ++y)
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (y0 + y < splits) v[y][i] = get_partial(p + (y0 + y) * pitch + i * step);
+        if (y0 + y < splits) v[y][i] = get_partial(p + (y0 + y) * pitch + at(i));
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int y = 0; y < Y; ++y)
@@ -194,7 +194,7 @@ __device__ __forceinline__ bool join_splits(const LinGemm& p, f32x4 (&acc)[TM][T
         put_partial(mine + ((i * TN + j) * 2 + h) * THREADS, f32x2{acc[i][j][2 * h], acc[i][j][2 * h + 1]});
   if (!last_of_tile(p.tickets + blockIdx.x, splits)) return false;
   f32x2 sum[TM * TN * 2];
-  sum_partials(tile, PITCH, THREADS, splits, sum);
+  sum_partials(tile, PITCH, [](int i) { return i * THREADS; }, splits, sum);
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll

@@ -18,6 +18,14 @@
 // fp32 does the same with v_mfma_f32_16x16x4_f32, 4 k a lane.
 // Rows past M repeat row M - 1, columns past N the last one (their results are
 // dropped); k past the end reads as zero on both sides.
+//
+// Bound by HBM where the weight is large: on an MI355X (copy 5.2 TB/s) one token
+// takes 30 us from 6144 to 12288 (151 MB, 5.0 TB/s) and 55 us through the gated
+// block from 12288 to 6144 (302 MB, 5.5 TB/s); by latency where it is small: 768 x
+// 768 4 us, gated 4096 -> 2048 (33.5 MB) 10 us, of which launch, first load and
+// join take about 6.  16 columns a tile for a k-contiguous weight, 128 bytes of
+// columns for an n-contiguous one: with 64 bytes two workgroups on different XCDs
+// fetch every line twice (gated 12288 -> 6144 93 us against 59).
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -101,7 +109,8 @@ __global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
   constexpr int MATS = DUAL ? 2 : 1;
   constexpr int TC = 16 * G;
   // Steps whose loads are in flight together.
-  constexpr int U = WKC ? (G * MATS * 4 + MT * 4 <= 12 ? 8 : G * MATS * 4 + MT * 4 <= 24 ? 4 : 2) : (G * MATS <= 4 ? 2 : 1);
+  constexpr int REGS = (WKC ? 4 * G * MATS : PER * MATS * G * static_cast<int>(sizeof(T)) / 4) + 4 * MT;
+  constexpr int U = REGS <= 12 ? 8 : REGS <= 24 ? 4 : REGS <= 32 ? 2 : 1;
   extern __shared__ float red[];               // [waves][MATS][M][TC]
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -265,33 +274,40 @@ __global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
   }
   with_act(p.act, [&](auto A) {
     constexpr int ACT = decltype(A)::value;
-    for (int i = threadIdx.x; i < M * TC; i += blockDim.x) {
-      const int m = i / TC;
-      const int64_t n = n0 + i % TC;
-      if (n >= p.N) continue;
-      float v[MATS];
+    // Two cells a lane at a time, so that their partials' loads travel together.
+    const int all = M * TC, stride = blockDim.x;
+    for (int i0 = threadIdx.x; i0 < all; i0 += 2 * stride) {
+      const int cell[2] = {i0, i0 + stride < all ? i0 + stride : i0};
+      float v[2 * MATS];
       if (from) {
-        sum_partials(from + i, cells, M * TC, splits, v);
+        sum_partials(from, cells, [&](int k) { return (k % MATS) * all + cell[k / MATS]; }, splits, v);
       } else {
 #pragma unroll
-        for (int a = 0; a < MATS; ++a) v[a] = joined(a * M * TC + i);
+        for (int k = 0; k < 2 * MATS; ++k) v[k] = joined((k % MATS) * all + cell[k / MATS]);
       }
       auto put = [&](void *base, int64_t at, float y, bool f32) {
         if (f32) static_cast<float *>(base)[at] = y;
         else static_cast<uint16_t *>(base)[at] = to_bf16(y);
       };
-      float y;
-      if constexpr (DUAL) {
-        if (p.aux) put(p.aux, m * p.ldaux + n, v[0], sizeof(T) == 4);
-        if (p.aux2) put(p.aux2, m * p.ldaux + n, v[1], sizeof(T) == 4);
-        y = act_fwd<ACT>(v[0]) * v[1];
-      } else {
-        const float pre = p.bias ? v[0] + p.bias[n] : v[0];
-        if (p.aux) put(p.aux, m * p.ldaux + n, pre, sizeof(T) == 4);
-        y = act_fwd<ACT>(pre);
-        if (p.res) y += load1(static_cast<const T *>(p.res) + m * p.ldres + n);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int m = cell[h] / TC;
+        const int64_t n = n0 + cell[h] % TC;
+        if (n >= p.N || (h && cell[1] == i0)) continue;
+        float y;
+        if constexpr (DUAL) {
+          const float gate = v[h * MATS], up = v[h * MATS + 1];
+          if (p.aux) put(p.aux, m * p.ldaux + n, gate, sizeof(T) == 4);
+          if (p.aux2) put(p.aux2, m * p.ldaux + n, up, sizeof(T) == 4);
+          y = act_fwd<ACT>(gate) * up;
+        } else {
+          const float pre = p.bias ? v[h] + p.bias[n] : v[h];
+          if (p.aux) put(p.aux, m * p.ldaux + n, pre, sizeof(T) == 4);
+          y = act_fwd<ACT>(pre);
+          if (p.res) y += load1(static_cast<const T *>(p.res) + m * p.ldres + n);
+        }
+        put(p.c, m * p.ldc + n, y, p.c_f32);
       }
-      put(p.c, m * p.ldc + n, y, p.c_f32);
     }
   });
 }
