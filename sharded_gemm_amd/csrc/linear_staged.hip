@@ -4,7 +4,7 @@
 //   kModeOne  c = epi(A W)              kModeDual  c = act(A W) * (A W2)
 //   kModeCat  c = A W + A2 W2           kModePair  c = A W, c2 = A2 W2
 //
-// A workgroup of 4 waves owns a BM x BN tile of the output (kModeDual: BM x
+// A workgroup of 4 or 8 waves owns a BM x BN tile of the output (kModeDual: BM x
 // BN/2, with the gate's and the up projection's columns side by side in the W
 // tile, so that each lane ends with both of an output's factors).  K is staged
 // 128 bytes at a time (64 bf16, 32 fp32) through two LDS slots: the next
@@ -28,7 +28,6 @@ using namespace lin;
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRow = 128;                 // LDS bytes of a tile row per stage
 
 __device__ __forceinline__ uint32_t lds_at(int r, int c) {
@@ -62,14 +61,14 @@ __device__ __forceinline__ u32x4 load16(const T *p, int64_t left) {
 // element wherever it and the V rows after it lie inside K (there, reading V
 // elements from any existing one stays within the operand whatever its stride);
 // only the last stages of K are checked, and their missing elements are zero.
-template <typename T, int ROWS, bool KC>
+template <typename T, int ROWS, bool KC, int THREADS>
 struct Tile {
   static constexpr int V = 16 / sizeof(T);          // elements of a 16-byte chunk
-  static constexpr int KB = ROWS / 32;              // chunks (KC) or k rows (else) per thread
+  static constexpr int KB = ROWS * 8 / THREADS;     // chunks (KC) or k rows (else) per thread
   static constexpr int NBLK = ROWS / V;             // groups of V rows
   static constexpr int BK = kRow / sizeof(T);
-  static_assert(KB == 2 || KB == 4, "tile rows");
-  static_assert(KC || NBLK * (BK / KB) == kThreads, "one block of KB k rows per thread");
+  static_assert(KB == 2, "tile rows");
+  static_assert(KC || NBLK * (BK / KB) == THREADS, "one block of KB k rows per thread");
 
   const T *at[KC ? KB : 1];    // sources at k = 0
   int64_t ld;
@@ -86,7 +85,7 @@ struct Tile {
     if constexpr (KC) {
 #pragma unroll
       for (int q = 0; q < KB; ++q) {
-        const int idx = t + kThreads * q;
+        const int idx = t + THREADS * q;
         where(idx >> 3, &base, &row);
         at[q] = base + (row < n ? row : n - 1) * ld + (idx & 7) * V;
       }
@@ -117,7 +116,7 @@ struct Tile {
 #pragma unroll
     for (int q = 0; q < KB; ++q) {
       if constexpr (KC) {
-        g[q] = load16<T>(at[q] + shift + k0, K - k0 - ((t + kThreads * q) & 7) * V);
+        g[q] = load16<T>(at[q] + shift + k0, K - k0 - ((t + THREADS * q) & 7) * V);
       } else {
         g[q] = load16<T>(at[0] + shift + (k0 + q) * ld, k0 + t / NBLK * KB + q < K ? left : 0);
       }
@@ -129,7 +128,7 @@ struct Tile {
     if constexpr (KC) {
 #pragma unroll
       for (int q = 0; q < KB; ++q) {
-        const int idx = t + kThreads * q;
+        const int idx = t + THREADS * q;
         *reinterpret_cast<u32x4 *>(lds + lds_at(idx >> 3, idx & 7)) = g[q];
       }
     } else {
@@ -139,27 +138,31 @@ struct Tile {
       for (int j = 0; j < V; ++j) {
         char *dst = lds + lds_at(b * V + j, byte >> 4) + (byte & 15);
         if constexpr (sizeof(T) == 4) {
-          if constexpr (KB == 4) *reinterpret_cast<u32x4 *>(dst) = u32x4{g[0][j], g[1][j], g[2][j], g[3][j]};
-          else *reinterpret_cast<u32x2 *>(dst) = u32x2{g[0][j], g[1][j]};
+          *reinterpret_cast<u32x2 *>(dst) = u32x2{g[0][j], g[1][j]};
         } else {
-          uint32_t d[KB / 2];
-#pragma unroll
-          for (int e = 0; e < KB / 2; ++e)
-            d[e] = __builtin_amdgcn_perm(g[2 * e + 1][j >> 1], g[2 * e][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
-          if constexpr (KB == 4) *reinterpret_cast<u32x2 *>(dst) = u32x2{d[0], d[1]};
-          else *reinterpret_cast<uint32_t *>(dst) = d[0];
+          *reinterpret_cast<uint32_t *>(dst) =
+              __builtin_amdgcn_perm(g[1][j >> 1], g[0][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
         }
       }
     }
   }
 };
 
+// 4 waves on 64 x 64, 8 on 128 x 128: two 16-byte chunks of each operand's stage a
+// thread on both.  The 8 waves stay within 128 registers, so that two such
+// workgroups share a CU (4 waves with 230 registers: 8191 x 333 x 2333 bf16 74 us
+// against 61, 2049 x 2047 x 2049 63 against 58).
+constexpr int threads_of(int edge) { return edge == 128 ? 512 : 256; }
+constexpr int waves_simd(int edge) { return edge == 128 ? 4 : 2; }
+
 template <typename T, int BM, int BN, bool AKC, bool WKC, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) lin_staged_kernel(LinGemm p) {
-  using TA = Tile<T, BM, AKC>;
-  using TW = Tile<T, BN, WKC>;
+__global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_kernel(LinGemm p) {
+  constexpr int THREADS = threads_of(BM);
+  using TA = Tile<T, BM, AKC, THREADS>;
+  using TW = Tile<T, BN, WKC, THREADS>;
   constexpr int BK = TA::BK;
-  constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 16, TN = WN / 16;
+  constexpr int WAVES_N = THREADS / 128;                 // by two rows of waves
+  constexpr int WM = BM / 2, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
   constexpr int BNO = MODE == kModeDual ? BN / 2 : BN;   // output columns of a tile
   constexpr int LDS_A = BM * kRow, STAGE = (BM + BN) * kRow;
   __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2) lin_staged_kernel(LinGemm p) {
   const T *W2 = static_cast<const T *>(p.w2);
   void *c = second ? p.c2 : p.c;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave >> 1, wn = wave & 1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WAVES_N, wn = wave % WAVES_N;
 
   TA ta;
   TW tw;
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 2) lin_staged_kernel(LinGemm p) {
 
   // Stages [first, last) of one pair of matrices.  64 x 64: stage st + 2 leaves
   // for the registers that stage st has left, stage st + 1 moves from its own to
-  // LDS after stage st's products, so a load has two stages' time to arrive.
-  // 128 x 128 has registers for one stage of it (two spilled: 4097^3 bf16 350 us).
+  // LDS after stage st's products, so a load has two stages' time to arrive
+  // (four gained nothing).  128 x 128: one stage ahead (two spill).
   // The unchecked stages have a loop of their own: where both kinds of fetch
   // meet, the compiler waits for the newest load too.
   auto run = [&](int64_t first, int64_t last, int64_t a_shift, int64_t w_shift) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) lin_staged_kernel(LinGemm p) {
   run(st0, min(st1, per), 0, 0);
   if constexpr (MODE == kModeCat)
     run(max(st0 - per, int64_t{0}), st1 - per, static_cast<const T *>(p.a2) - A, W2 - W);
-  if (gridDim.y > 1 && !join_splits<kThreads>(p, acc)) return;
+  if (gridDim.y > 1 && !join_splits<THREADS>(p, acc)) return;
 
   auto rm = [&](int i) -> int64_t { return m0 + wm * WM + i * 16 + (lane & 15); };
   auto cn = [&](int j) -> int64_t {
@@ -340,7 +343,7 @@ constexpr int64_t kCUs = 256;
 // k workgroups to the busiest CU a stage takes max(alone, k * shared) us, and
 // joining S > 1 splits 2 us and 7 ns a workgroup (their partials' trip to memory
 // and back).  The constants are fitted to MI355X times, e.g. (bf16 / fp32)
-// 2049 x 2047 x 2049: edge 128 62 / 282 us, edge 64 71 / 194; 100 x 4097 x 2049: 29 / 88
+// 2049 x 2047 x 2049: edge 128 60 / 281 us, edge 64 71 / 194; 100 x 4097 x 2049: 29 / 88
 // unsplit, 16 / 36 with three splits; 515 x 1021 x 1531: 13 / 28 unsplit, 20 / 32
 // with four.
 struct Shape {
@@ -352,8 +355,8 @@ Shape shape_of(const LinGemm& p, bool may_split) {
   Shape best{64, 1, 0};
   double least = 0.0;
   for (int edge = 128; edge >= 64; edge -= 64) {
-    const double shared = p.f32 ? (edge == 128 ? 2.1 : 0.58) : (edge == 128 ? 0.92 : 0.38);
-    const double alone = p.f32 ? (edge == 128 ? 2.6 : 0.72) : (edge == 128 ? 1.8 : 0.55);
+    const double shared = p.f32 ? (edge == 128 ? 2.08 : 0.58) : (edge == 128 ? 0.87 : 0.38);
+    const double alone = p.f32 ? (edge == 128 ? 2.35 : 0.72) : (edge == 128 ? 1.1 : 0.55);
     const int64_t tiles = lin_tiles_count(p, edge, edge);
     // Only 64 x 64 tiles are split, few enough for a ticket each, down to 4 stages.
     for (int s = 1; s <= 16 && (s == 1 || (may_split && edge == 64 && tiles <= kMaxTickets && 4 * s <= stages)); ++s) {
@@ -372,8 +375,8 @@ Shape shape_of(const LinGemm& p, bool may_split) {
 template <typename T, bool AKC, bool WKC, int MODE>
 hipError_t launch(const LinGemm& p, const Shape& h, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits));
-  if (h.edge == 128) hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), grid, dim3(kThreads), 0, s, p);
-  else hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), grid, dim3(kThreads), 0, s, p);
+  if (h.edge == 128) hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), grid, dim3(threads_of(128)), 0, s, p);
+  else hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), grid, dim3(threads_of(64)), 0, s, p);
   return hipGetLastError();
 }
 
