@@ -47,6 +47,9 @@
 // register-staged, bounds-checked loads, for shapes the DMA path cannot take
 // (K not a multiple of 32, N not a multiple of 8, misaligned pointers).
 //
+// The operand tiles, the DMA and both main loops are in gemm_tiles.h, which the
+// linear layer's kernels share.
+//
 // All paths accumulate every output element over k in the same order (32-wide
 // k steps, ascending), so results are bit-identical whichever path or tile
 // shape runs, do not depend on how the caller chunks M and N, and continuing

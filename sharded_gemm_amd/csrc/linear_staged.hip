@@ -18,6 +18,11 @@
 // bf16: v_mfma_f32_16x16x32_bf16.  fp32: v_mfma_f32_16x16x4_f32, four per
 // 16-byte chunk; a lane group's chunk holds four consecutive k, which the four
 // MFMAs take in turn (the order of a sum over k is free, and A and W agree).
+//
+// Measured on an MI355X: fp32 4096^3 1.03 ms (133 TFLOP/s, the library 150), 515 x
+// 1021 x 1531 28 us (58); bf16 4097 x 4095 x 4097 290 us (475), the gated
+// backward 1021 x 1337 -> 999 33 + 27 us.  Odd strides cost: a 16-byte load off a
+// 4-byte boundary goes through the address unit a lane at a time.
 #include <algorithm>
 
 #include "linear_dev.h"

@@ -1,5 +1,12 @@
 // The tiled bf16 kernels of the linear layer and the gated block, on gemm.hip's
 // building blocks (gemm_tiles.h).  One translation unit instantiates each mode.
+//
+// Bound by MFMA on large problems.  On an MI355X: the gated forward 4096 x 12288 ->
+// 6144 with both pre-activations kept 846 us (1.46 PFLOP/s; a bf16 8192^3 library
+// product reaches 1.39), the gated backward 8192 x 4096 -> 2048's input gradient
+// over both weights 205 us (1.34) and its two weight gradients 253 us (1.09: both
+// operands come through the transposing LDS read).  Two products for the gate and
+// the up projection would read X twice and pass both results through memory.
 #pragma once
 
 #include "gemm_tiles.h"
