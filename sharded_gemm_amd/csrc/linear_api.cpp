@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kMaxDim = int64_t{1} << 31;
 constexpr int64_t kMaxRanks = 64;
 constexpr int64_t kWsAlign = 256;
+static_assert(kGradParts == TP_GRAD_PARTS, "the header's count");
 
 int hip_fail(hipError_t e, const char *what) {
   return fail(TP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));

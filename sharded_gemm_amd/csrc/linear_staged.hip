@@ -408,9 +408,12 @@ hipError_t dispatch(const LinGemm& p, const Shape& h, hipStream_t s) {
 
 }  // namespace
 
-// Launches are capped at 2^32 threads: 2^23 tiles of 64 x 64 (twice that many
-// workgroups of 256 threads where two products share a launch).
-bool lin_grid_ok(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22); }
+// A launch holds fewer than 2^32 threads. Tiles: up to 2^22 of 64 x 64, 256
+// threads each, twice where two products share a launch (2^31). Few rows: 16
+// columns to a workgroup of up to 512 threads, so N below 2^26 (2^31).
+bool lin_grid_ok(int64_t M, int64_t N) {
+  return N < (int64_t{1} << 26) && ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22);
+}
 
 int64_t lin_staged_ws(const LinGemm& p) {
   const Shape h = shape_of(p, true);

@@ -417,6 +417,44 @@ def test_graph_replays_and_streams(shape):
         step(torch.cuda.current_stream())
 
 
+@pytest.mark.parametrize("layout", [MATH, LINEAR])
+@pytest.mark.parametrize("M,K,N", [(4096, 64, 4096), (2048, 64, 6144), (2048, 96, 2048), (64, 2048, 6144), (96, 2048, 2048)])
+def test_every_tile(M, K, N, layout):
+    """Enough output for each of the bf16 tiles (256 x 256, 256 x 192, 256 x 128, 128 x 128), forward and backward, against
+    64-bit products on the GPU."""
+    announce(f"tiles {M} {K} {N} layout {layout}")
+    X, d = rnd((M, K), 1, BF16).cuda(), rnd((M, N), 2, BF16).cuda()
+    W, W2 = rnd((K, N), 3, BF16, 0.2).cuda(), rnd((K, N), 4, BF16, 0.2).cuda()
+    Wl, W2l = lay(W, layout), lay(W2, layout)
+    x, w, w2, dd = X.double(), W.double(), W2.double(), d.double()
+
+    def acc(a, b):
+        return (a.shape[1] + 4) * U32 * (a.abs() @ b.abs())
+
+    def near(got, ref, e, name):
+        assert bool(((got.double() - ref).abs() <= e + u(BF16) * (ref.abs() + e)).all()), name
+    out = torch.empty((M, N), dtype=BF16, device="cuda")
+    tp.tp_linear(X, Wl, out, weight_layout=layout)
+    near(out, x @ w, acc(x, w), "linear")
+    tp.tp_gated_linear(X, Wl, W2l, out, act=tp.TP_ACT_NONE, weight_layout=layout)
+    g, up = x @ w, x @ w2
+    eg, eu = acc(x, w), acc(x, w2)
+    near(out, g * up, eg * (up.abs() + eu) + g.abs() * eu + 2 * U32 * (g * up).abs(), "gated")
+    dX, dW, dW2 = torch.empty_like(X), torch.empty_like(Wl), torch.empty_like(Wl)
+    tp.tp_linear_backward(X, Wl, d, dX=dX, dW=dW, weight_layout=layout)
+    near(dX, dd @ w.t(), acc(dd, w.t()), "dX")
+    near(dW if layout == MATH else dW.t(), x.t() @ dd, acc(x.t(), dd), "dW")
+    gb, ub = g.to(BF16), up.to(BF16)
+    tp.tp_gated_linear_backward(X, Wl, W2l, gb, ub, d, dX=dX, dW_gate=dW, dW_up=dW2, act=tp.TP_ACT_NONE, weight_layout=layout,
+                                ws=tp.tp_gated_linear_backward_ws(X, d))
+    torch.cuda.synchronize()
+    dg, du = (dd * ub.double()), (dd * gb.double())
+    rg, ru = u(BF16) * 1.01 * dg.abs(), u(BF16) * 1.01 * du.abs()      # each is stored once in bf16
+    near(dX, dg @ w.t() + du @ w2.t(), rg @ w.t().abs() + ru @ w2.t().abs() + 2 * (acc(dg, w.t()) + acc(du, w2.t())), "gated dX")
+    for got, h, r, name in ((dW, dg, rg, "dW_gate"), (dW2, du, ru, "dW_up")):
+        near(got if layout == MATH else got.t(), x.t() @ h, x.t().abs() @ r + acc(x.t(), h), name)
+
+
 # Few rows and few tiles with a long K: the products split K and join through the workspace.
 SPLIT = [(1, 4096, 256, BF16, MATH), (3, 2056, 130, BF16, MATH), (16, 4100, 65, BF16, LINEAR), (1, 3000, 96, F32, MATH),
          (9, 1030, 50, F32, LINEAR), (40, 4096, 256, BF16, LINEAR), (64, 4096, 192, BF16, MATH), (100, 2080, 120, BF16, MATH),

@@ -47,7 +47,7 @@ def _gated_bwd(**kw):
 
 ARG, UNS = _abi.TP_ERR_ARG, _abi.TP_ERR_UNSUPPORTED
 COMMON = [(dict(dtype=7), ARG), (dict(act=5), ARG), (dict(act=-1), ARG), (dict(weight_layout=2), ARG), (dict(M=-1), ARG),
-          (dict(K=0), ARG), (dict(K=1 << 31), UNS), (dict(M=1 << 31), UNS), (dict(M=1 << 30, K=1 << 16), UNS),
+          (dict(K=0), ARG), (dict(K=1 << 31), UNS), (dict(M=1 << 31), UNS), (dict(M=1 << 30, K=1 << 16), UNS), (dict(K=1 << 26), UNS),
           (dict(X=None), ARG), (dict(X=P(0) + 1), ARG), (dict(X_ld=31), ARG), (dict(X_ld=1 << 31), UNS)]
 
 
