@@ -46,7 +46,6 @@ struct LinGemm {
   int32_t act = 0;      // TP_ACT_*
   int32_t c_f32 = 0;    // c holds fp32 (always with f32)
   int32_t acc_c = 0;
-  int32_t vec = 0;      // set by the launcher: four columns at a time are aligned
   // Several workgroups to a tile: their partials and arrival counts.
   float *join = nullptr;
   uint32_t *tickets = nullptr;

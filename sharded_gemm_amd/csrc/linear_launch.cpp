@@ -104,9 +104,6 @@ int64_t lin_gemm_ws(const LinGemm& p) {
 }
 
 hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws, int64_t ws_bytes) {
-  const int64_t es = p.f32 ? 4 : 2, ces = p.c_f32 ? 4 : 2;
-  p.vec = aligned(p.c, p.ldc, ces, 4) && aligned(p.c2, p.ldc, ces, 4) && aligned(p.res, p.ldres, es, 4) &&
-          aligned(p.aux, p.ldaux, es, 4) && aligned(p.aux2, p.ldaux, es, 4) && aligned(p.bias, 4, 4, 4);
   if (takes_rows(p)) return lin_rows_launch(p, ws, ws_bytes, s);
   if (lin_tiles_ok(p)) return launch_tiles(p, ws, ws_bytes, s);
   return lin_staged_launch(p, ws, ws_bytes, s);
