@@ -20,8 +20,8 @@
 // MFMAs take in turn (the order of a sum over k is free, and A and W agree).
 //
 // Measured on an MI355X: fp32 4096^3 1.03 ms (133 TFLOP/s, the library 150), 515 x
-// 1021 x 1531 28 us (58); bf16 4097 x 4095 x 4097 290 us (475), the gated
-// backward 1021 x 1337 -> 999 33 + 27 us.  Odd strides cost: a 16-byte load off a
+// 1021 x 1531 28 us (58); bf16 4097 x 4095 x 4097 270 us (509), the gated
+// backward 1021 x 1337 -> 999 32 + 25 us.  Odd strides cost: a 16-byte load off a
 // 4-byte boundary goes through the address unit a lane at a time.
 #include <algorithm>
 
@@ -155,8 +155,8 @@ struct Tile {
 
 // 4 waves on 64 x 64, 8 on 128 x 128: two 16-byte chunks of each operand's stage a
 // thread on both.  The 8 waves stay within 128 registers, so that two such
-// workgroups share a CU (4 waves with 230 registers: 8191 x 333 x 2333 bf16 74 us
-// against 61, 2049 x 2047 x 2049 63 against 58).
+// workgroups share a CU (4 waves with 230 registers, both still storing element
+// by element: 8191 x 333 x 2333 bf16 74 us against 61, 2049 x 2047 x 2049 63 against 58).
 constexpr int threads_of(int edge) { return edge == 128 ? 512 : 256; }
 constexpr int waves_simd(int edge) { return edge == 128 ? 4 : 2; }
 
