@@ -326,6 +326,23 @@ def _stream_ptr(stream):
     return C.c_void_p(int(stream))
 
 
+def _torch_stream(ptr, device):
+    """The torch stream of a HIP stream (None: the default one)."""
+    import torch
+    return torch.cuda.ExternalStream(ptr, device=device) if ptr else torch.cuda.default_stream(device)
+
+
+def _capturing(stream, device):
+    """Whether the current stream, or `stream`, is being captured into a graph."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if stream is None:
+        return False
+    with torch.cuda.stream(_torch_stream(_stream_ptr(stream).value, device)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -378,11 +395,18 @@ class Prepared:
     sequence.  It holds references to the tensors it points into, and a replay
     after any of them has moved (resized or re-pointed) raises instead of
     touching stale memory.  Replays follow one another: one that may overlap
-    another (on a second stream) needs a prepared call of its own."""
+    another (on a second stream) needs a prepared call of its own.
 
-    def __init__(self, fn, args, keep, streams, tensors=()):
+    ``own``: a workspace that only this call holds.  It goes back to its stream's
+    memory pool with the call, so every other stream that a replay runs on is
+    recorded with the allocator, which then waits for that stream's work.  (A
+    graph that captured a replay needs the call to be kept, as it needs its
+    tensors.)"""
+
+    def __init__(self, fn, args, keep, streams, tensors=(), own=None):
         self._fn, self._args, self._keep, self._streams = fn, args, keep, streams
         self._tensors = [(t, t.data_ptr()) for t in tensors]
+        self._own, self._recorded = own, {_stream_ptr(None).value} if own is not None else None
 
     def __call__(self, *streams):
         for t, p in self._tensors:
@@ -391,6 +415,9 @@ class Prepared:
         ptrs = [_stream_ptr(s) for s in streams] if streams else self._streams
         if len(ptrs) < len(self._streams):
             ptrs = list(ptrs) + [ptrs[-1]] * (len(self._streams) - len(ptrs))
+        if self._own is not None and ptrs[0].value not in self._recorded:
+            self._own.record_stream(_torch_stream(ptrs[0].value, self._own.device))
+            self._recorded.add(ptrs[0].value)
         _check(self._fn(*self._args, *ptrs))
 
 
@@ -794,23 +821,26 @@ def _new_ws(fn, args, device):
 
 
 def _forward_ws(fn, args, ws, device, stream, prepare):
-    """The zeroed workspace of a forward call: the caller's, or a prepared call's own."""
+    """(workspace, whether it is the prepared call's own) of a forward call.  A prepared call
+    that is given none gets one, zeroed by the time this returns: its caller cannot order a
+    replay on another stream after the zeroing.  While a stream is captured that cannot be
+    waited for, and the call goes without."""
     import torch
-    if ws is None and prepare and torch.device(device).type == "cuda":
+    device, own = torch.device(device), False
+    if ws is None and prepare and device.type == "cuda" and not _capturing(stream, device):
         n = _ws_bytes(fn, args)
         if n:
-            ws = torch.zeros(n, dtype=torch.uint8, device=device)
-            if _stream_ptr(stream).value != _stream_ptr(None).value:
-                torch.cuda.current_stream().synchronize()   # zeroed before another stream uses it
+            ws, own = torch.zeros(n, dtype=torch.uint8, device=device), True
+            torch.cuda.current_stream().synchronize()
     args.ws, args.ws_bytes = _ws(ws)
-    return ws
+    return ws, own
 
 
-def _call(fn, args, stream, prepare, tensors):
-    """Run an entry point that takes one argument structure, or prepare it."""
+def _call(fn, args, stream, prepare, tensors, own=None):
+    """Run an entry point that takes one argument structure, or prepare it (``own``: as in ``Prepared``)."""
     _on_gpu(*tensors)
     if prepare:
-        return Prepared(fn, (C.byref(args),), [args], [_stream_ptr(stream)], _tensors(*tensors))
+        return Prepared(fn, (C.byref(args),), [args], [_stream_ptr(stream)], _tensors(*tensors), own)
     _check(fn(C.byref(args), _stream_ptr(stream)))
 
 
@@ -818,7 +848,8 @@ def tp_linear_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH):
     """A zeroed workspace (uint8 tensor, maybe empty) for ``tp_linear`` of these shapes: with it
     few rows and small batches split K over the whole chip.  It serves any number of calls
     one after another, also of other shapes and of ``tp_gated_linear`` (one that needs more
-    runs as without it)."""
+    runs as without it).  It is zeroed on the current stream, which calls on another one wait
+    for, as for any input."""
     import torch
     args = tp_linear_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
                           N=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]))
@@ -834,7 +865,8 @@ def tp_linear(X, W, out, *, bias=None, residual=None, pre_out=None, act=TP_ACT_N
     or fp32); out is in it, or fp32, and may be the residual itself; bias is fp32
     [N].  Rows may be strided (a weight may be a column slice of a full one).  ``ws``: from
     ``tp_linear_ws``, optional.  With ``prepare=True`` nothing runs; a ``Prepared`` call
-    taking the stream is returned (with a workspace of its own if none is given)."""
+    taking the stream is returned (with a workspace of its own if none is given and no graph
+    is being captured: prepare before a capture)."""
     lib = load()
     M, K = (int(v) for v in X.shape)
     N = _weight_dims(W, weight_layout)[1]
@@ -848,8 +880,9 @@ def tp_linear(X, W, out, *, bias=None, residual=None, pre_out=None, act=TP_ACT_N
     args.pre_out, args.pre_ld = _mat(pre_out, "pre_out", (M, N), dt)
     _check_bias(bias, N)
     args.bias = _ptr(bias)
-    ws = _forward_ws(lib.tp_linear_ws, args, ws, X.device, stream, prepare)
-    return _call(lib.tp_linear, args, stream, prepare, (X, W, out, bias, residual, pre_out, ws))
+    ws, own = _forward_ws(lib.tp_linear_ws, args, ws, X.device, stream, prepare)
+    return _call(lib.tp_linear, args, stream, prepare, (X, W, out, bias, residual, pre_out, ws),
+                 ws if own else None)
 
 
 def tp_linear_backward_ws(X, W, dOut, *, act=TP_ACT_NONE, weight_layout=TP_WEIGHTS_MATH, dbias=None):
@@ -917,8 +950,9 @@ def tp_gated_linear(X, W_gate, W_up, out, *, gate_out=None, up_out=None, act=TP_
     args.up_out, ld = _mat(up_out, "up_out", (M, F), dt)
     if gate_out is not None and up_out is not None:
         _same_ld(args.keep_ld, ld, (M, F), "gate_out and up_out")
-    ws = _forward_ws(lib.tp_gated_linear_ws, args, ws, X.device, stream, prepare)
-    return _call(lib.tp_gated_linear, args, stream, prepare, (X, W_gate, W_up, out, gate_out, up_out, ws))
+    ws, own = _forward_ws(lib.tp_gated_linear_ws, args, ws, X.device, stream, prepare)
+    return _call(lib.tp_gated_linear, args, stream, prepare, (X, W_gate, W_up, out, gate_out, up_out, ws),
+                 ws if own else None)
 
 
 def _same_ld(a, b, shape, names):
