@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
   // Steps whose loads are in flight together.
   constexpr int REGS = (WKC ? 4 * G * MATS : PER * MATS * G * static_cast<int>(sizeof(T)) / 4) + 4 * MT;
   constexpr int U = REGS <= 12 ? 8 : REGS <= 24 ? 4 : REGS <= 32 ? 2 : 1;
-  extern __shared__ float red[];               // [waves][MATS][M][TC]
+  // [waves][MATS][M][TC]; four floats at a time go in and out.
+  extern __shared__ __attribute__((aligned(16))) float red[];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
