@@ -12,8 +12,6 @@
 // partial row and a second kernel adds the slabs in order, so no atomics decide
 // the result.  Measured on an MI355X (copy 5.2 TB/s): gated 8192 x 2048 bf16 30 us
 // (5.6 TB/s), linear 8192 x 4096 with its bias gradient 42 + 4 us (4.8 TB/s).
-#include <algorithm>
-
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -22,7 +20,7 @@ using namespace lin;
 
 namespace {
 
-constexpr int kThreads = 256, kCols = 8;
+constexpr int kThreads = kActThreads, kCols = kActCols;
 
 // Eight elements at p; `left` exist.  `on`: there are at least eight elements of
 // the array from p on, so the missing ones are read from the next rows (and not
@@ -192,28 +190,9 @@ __global__ void __launch_bounds__(64 * kSumGroups) colsum_kernel(const float *pa
   }
 }
 
-// The grid: lanes of a row, and rows of a slab.  64 rows, fewer where that leaves
-// under 1024 workgroups (1021 x 999, gated: 67 us in 32 workgroups), though not
-// so few that the partial rows weigh more than an eighth of the input, nor so
-// many slabs that they exceed the grid.
-struct Grid {
-  int lanes;
-  int64_t tiles, rows, slabs;
-};
-Grid grid_of(int64_t M, int64_t N) {
-  Grid g{64, 0, 64, 0};
-  while (g.lanes > 1 && (g.lanes / 2) * kCols >= N) g.lanes /= 2;
-  g.tiles = (N + g.lanes * kCols - 1) / (g.lanes * kCols);
-  const int64_t least = std::max<int64_t>(16, kThreads / g.lanes);
-  while (g.rows > least && g.tiles * ((M + g.rows - 1) / g.rows) < 1024) g.rows /= 2;
-  g.rows = std::max(std::max(g.rows, least), (M + 1023) / 1024);
-  g.slabs = (M + g.rows - 1) / g.rows;
-  return g;
-}
-
 template <typename T>
 hipError_t launch(const ActGrad& p, hipStream_t s) {
-  const Grid g = grid_of(p.M, p.N);
+  const ActGrid g = act_grad_grid(p.M, p.N);
   if (p.M > 0) {
     const dim3 grid(static_cast<unsigned>(g.tiles), static_cast<unsigned>(g.slabs));
     const int64_t flat = (p.M * p.N + kThreads * kCols - 1) / (kThreads * kCols);
@@ -235,8 +214,6 @@ hipError_t launch(const ActGrad& p, hipStream_t s) {
 }
 
 }  // namespace
-
-int64_t act_grad_slabs(int64_t M, int64_t N) { return grid_of(M, N).slabs; }
 
 hipError_t zero_tickets_launch(uint32_t *tickets, hipStream_t s) {
   hipLaunchKernelGGL(zero_tickets_kernel, dim3(1), dim3(kThreads), 0, s, tickets);

@@ -18,6 +18,7 @@
 // no table in device memory, nothing to copy, and a captured graph keeps them.
 #include <vector>
 
+#include "grad_table.h"
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -25,22 +26,6 @@ namespace tpshard {
 using namespace lin;
 
 namespace {
-
-constexpr int kMaxTensors = 64;
-constexpr int kThreads = 256;
-// Elements of a chunk: 16 per lane.
-constexpr int kPer = 16;
-constexpr int kChunk = kThreads * kPer;
-
-struct Table {
-  const void *g[kMaxTensors];
-  void *out[kMaxTensors];
-  int64_t first[kMaxTensors + 1];   // chunks before tensor i
-  int64_t n[kMaxTensors];
-  uint64_t f32;                     // bit i: tensor i holds fp32
-  int32_t num;
-};
-static_assert(sizeof(Table) < 3500, "kernel arguments");
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -55,57 +40,57 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
   __syncthreads();
   double t = lds[0];
 #pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) t += lds[w];
+  for (int w = 1; w < kGradThreads / 64; ++w) t += lds[w];
   __syncthreads();
   return t;
 }
 
 // The tensor that chunk `u` belongs to, from `i` on (chunks come in order).
-__device__ __forceinline__ int tensor_of(const Table& t, int64_t u, int i) {
+__device__ __forceinline__ int tensor_of(const GradTable& t, int64_t u, int i) {
   while (u >= t.first[i + 1]) ++i;
   return i;
 }
 
 __device__ __forceinline__ double sq(float v) { return static_cast<double>(v) * static_cast<double>(v); }
 
-__global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(Table t, double *parts, int add) {
-  __shared__ double lds[kThreads / 64];
+__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(GradTable t, double *parts, int add) {
+  __shared__ double lds[kGradThreads / 64];
   double s0 = 0.0, s1 = 0.0;
   int i = 0;
   for (int64_t u = blockIdx.x; u < t.first[t.num]; u += kGradParts) {
     i = tensor_of(t, u, i);
-    const int64_t at = (u - t.first[i]) * kChunk, left = t.n[i] - at;
+    const int64_t at = (u - t.first[i]) * kGradChunk, left = t.n[i] - at;
     if (t.f32 >> i & 1) {
       const uint32_t *g = static_cast<const uint32_t *>(t.g[i]) + at;
-      if (left >= kChunk) {
-        u32x4 v[kPer / 4];
+      if (left >= kGradChunk) {
+        u32x4 v[kGradPer / 4];
 #pragma unroll
-        for (int q = 0; q < kPer / 4; ++q)
-          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 4);
+        for (int q = 0; q < kGradPer / 4; ++q)
+          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kGradThreads + threadIdx.x) * 4);
 #pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) {
+        for (int q = 0; q < kGradPer / 4; ++q) {
           s0 += sq(__uint_as_float(v[q][0])) + sq(__uint_as_float(v[q][1]));
           s1 += sq(__uint_as_float(v[q][2])) + sq(__uint_as_float(v[q][3]));
         }
       } else {
-        for (int64_t e = threadIdx.x; e < left; e += kThreads) s0 += sq(__uint_as_float(g[e]));
+        for (int64_t e = threadIdx.x; e < left; e += kGradThreads) s0 += sq(__uint_as_float(g[e]));
       }
     } else {
       const uint16_t *g = static_cast<const uint16_t *>(t.g[i]) + at;
-      if (left >= kChunk) {
-        u32x4 v[kPer / 8];
+      if (left >= kGradChunk) {
+        u32x4 v[kGradPer / 8];
 #pragma unroll
-        for (int q = 0; q < kPer / 8; ++q)
-          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 8);
+        for (int q = 0; q < kGradPer / 8; ++q)
+          v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kGradThreads + threadIdx.x) * 8);
 #pragma unroll
-        for (int q = 0; q < kPer / 8; ++q)
+        for (int q = 0; q < kGradPer / 8; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s0 += sq(from_bf16(v[q][e] & 0xffffu));
             s1 += sq(from_bf16(v[q][e] >> 16));
           }
       } else {
-        for (int64_t e = threadIdx.x; e < left; e += kThreads) s0 += sq(from_bf16(g[e]));
+        for (int64_t e = threadIdx.x; e < left; e += kGradThreads) s0 += sq(from_bf16(g[e]));
       }
     }
   }
@@ -115,28 +100,28 @@ __global__ void __launch_bounds__(kThreads) grad_sumsq_kernel(Table t, double *p
 
 // One chunk of one tensor: loaded, then scaled and stored.
 struct Chunk {
-  u32x4 v[kPer / 4];
+  u32x4 v[kGradPer / 4];
   const void *g;
   void *out;
   int64_t at, left;
   bool f32;
 };
 
-__device__ __forceinline__ void chunk_load(const Table& t, int64_t u, int i, Chunk& c) {
+__device__ __forceinline__ void chunk_load(const GradTable& t, int64_t u, int i, Chunk& c) {
   c.g = t.g[i];
   c.out = t.out[i];
-  c.at = (u - t.first[i]) * kChunk;
+  c.at = (u - t.first[i]) * kGradChunk;
   c.left = t.n[i] - c.at;
   c.f32 = t.f32 >> i & 1;
-  if (c.left < kChunk) return;
+  if (c.left < kGradChunk) return;
   if (c.f32) {
     const uint32_t *g = static_cast<const uint32_t *>(c.g) + c.at;
 #pragma unroll
-    for (int q = 0; q < kPer / 4; ++q) c.v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 4);
+    for (int q = 0; q < kGradPer / 4; ++q) c.v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kGradThreads + threadIdx.x) * 4);
   } else {
     const uint16_t *g = static_cast<const uint16_t *>(c.g) + c.at;
 #pragma unroll
-    for (int q = 0; q < kPer / 8; ++q) c.v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kThreads + threadIdx.x) * 8);
+    for (int q = 0; q < kGradPer / 8; ++q) c.v[q] = *reinterpret_cast<const u32x4_any *>(g + (q * kGradThreads + threadIdx.x) * 8);
   }
 }
 
@@ -146,29 +131,29 @@ __device__ __forceinline__ void chunk_store(Chunk& c, float scale) {
   if (c.f32) {
     const uint32_t *g = static_cast<const uint32_t *>(c.g) + c.at;
     uint32_t *o = static_cast<uint32_t *>(c.out) + c.at;
-    if (c.left >= kChunk) {
+    if (c.left >= kGradChunk) {
 #pragma unroll
-      for (int q = 0; q < kPer / 4; ++q) {
+      for (int q = 0; q < kGradPer / 4; ++q) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c.v[q][e] = __float_as_uint(__uint_as_float(c.v[q][e]) * scale);
-        __builtin_nontemporal_store(c.v[q], reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 4));
+        __builtin_nontemporal_store(c.v[q], reinterpret_cast<u32x4_any *>(o + (q * kGradThreads + threadIdx.x) * 4));
       }
     } else {
-      for (int64_t e = threadIdx.x; e < c.left; e += kThreads) o[e] = __float_as_uint(__uint_as_float(g[e]) * scale);
+      for (int64_t e = threadIdx.x; e < c.left; e += kGradThreads) o[e] = __float_as_uint(__uint_as_float(g[e]) * scale);
     }
   } else {
     const uint16_t *g = static_cast<const uint16_t *>(c.g) + c.at;
     uint16_t *o = static_cast<uint16_t *>(c.out) + c.at;
-    if (c.left >= kChunk) {
+    if (c.left >= kGradChunk) {
 #pragma unroll
-      for (int q = 0; q < kPer / 8; ++q) {
+      for (int q = 0; q < kGradPer / 8; ++q) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           c.v[q][e] = pack2(from_bf16(c.v[q][e] & 0xffffu) * scale, from_bf16(c.v[q][e] >> 16) * scale);
-        __builtin_nontemporal_store(c.v[q], reinterpret_cast<u32x4_any *>(o + (q * kThreads + threadIdx.x) * 8));
+        __builtin_nontemporal_store(c.v[q], reinterpret_cast<u32x4_any *>(o + (q * kGradThreads + threadIdx.x) * 8));
       }
     } else {
-      for (int64_t e = threadIdx.x; e < c.left; e += kThreads) o[e] = to_bf16(from_bf16(g[e]) * scale);
+      for (int64_t e = threadIdx.x; e < c.left; e += kGradThreads) o[e] = to_bf16(from_bf16(g[e]) * scale);
     }
   }
 }
@@ -176,9 +161,9 @@ __device__ __forceinline__ void chunk_store(Chunk& c, float scale) {
 // Chunks are taken from the last to the first: the pass before went from first
 // to last, and what it read last is still in the 256 MB cache on the memory side.
 // The first chunk is on its way while the norm is added up.
-__global__ void __launch_bounds__(kThreads) grad_clip_kernel(Table t, const double *parts, int64_t ranks,
+__global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(GradTable t, const double *parts, int64_t ranks,
                                                              double max_norm, double eps, float *norm_out) {
-  __shared__ double lds[kThreads / 64];
+  __shared__ double lds[kGradThreads / 64];
   const int64_t chunks = t.first[t.num];
   int64_t u = chunks - 1 - blockIdx.x;
   int i = t.num - 1;
@@ -191,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(Table t, const doub
     chunk_load(t, u, i, c);
   }
   double s = 0.0;
-  for (int64_t q = threadIdx.x; q < ranks * kGradParts; q += kThreads) s += parts[q];
+  for (int64_t q = threadIdx.x; q < ranks * kGradParts; q += kGradThreads) s += parts[q];
   const double norm = sqrt(block_sum(s, lds));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
   // A NaN norm makes a NaN scale; an infinite one a scale of zero.
@@ -206,32 +191,15 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(Table t, const doub
   }
 }
 
-// The next tensors that hold anything, from *at on, as one launch's table.
-void next_table(const GradTensor *ts, int64_t num, int64_t *at, Table *t) {
-  t->num = 0;
-  t->f32 = 0;
-  t->first[0] = 0;
-  for (; *at < num && t->num < kMaxTensors; ++*at) {
-    const GradTensor& x = ts[*at];
-    if (x.n <= 0) continue;
-    const int i = t->num++;
-    t->g[i] = x.g;
-    t->out[i] = x.out;
-    t->n[i] = x.n;
-    t->first[i + 1] = t->first[i] + (x.n + kChunk - 1) / kChunk;
-    if (x.f32) t->f32 |= uint64_t{1} << i;
-  }
-}
-
 }  // namespace
 
 hipError_t grad_sumsq_launch(const GradTensor *ts, int64_t num, double *parts, hipStream_t s) {
   int64_t at = 0;
   int add = 0;
   do {   // at least once: the partials are written even where there is nothing to add
-    Table t;
+    GradTable t;
     next_table(ts, num, &at, &t);
-    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(kGradParts), dim3(kThreads), 0, s, t, parts, add);
+    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(kGradParts), dim3(kGradThreads), 0, s, t, parts, add);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     add = 1;
@@ -245,18 +213,18 @@ hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *par
   int64_t begin = 0, at = 0;
   std::vector<int64_t> starts;
   do {
-    Table t;
+    GradTable t;
     begin = at;
     next_table(ts, num, &at, &t);
     starts.push_back(begin);
   } while (at < num);
   for (size_t k = starts.size(); k-- > 0;) {
-    Table t;
+    GradTable t;
     at = starts[k];
     next_table(ts, num, &at, &t);
     const int64_t chunks = t.first[t.num];
     const int64_t grid = chunks < 1 ? 1 : chunks < 2048 ? chunks : 2048;
-    hipLaunchKernelGGL(grad_clip_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, t, parts, ranks,
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(static_cast<unsigned>(grid)), dim3(kGradThreads), 0, s, t, parts, ranks,
                        max_norm, eps, norm_out);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

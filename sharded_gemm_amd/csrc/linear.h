@@ -51,6 +51,8 @@ struct LinGemm {
   uint32_t *tickets = nullptr;
 };
 
+// Which kernel takes a product, and how (linear_launch.cpp).
+
 // Whether the grids of the kernels below reach every tile of [M, N].
 bool lin_grid_ok(int64_t M, int64_t N);
 
@@ -58,36 +60,41 @@ bool lin_grid_ok(int64_t M, int64_t N);
 // to be.
 int64_t lin_gemm_ws(const LinGemm& p);
 // Enqueues the product; ws may be null.
-hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws = nullptr, int64_t ws_bytes = 0);
+hipError_t lin_gemm_launch(const LinGemm& p, hipStream_t s, void *ws = nullptr, int64_t ws_bytes = 0);
+
+// Tiles of a launch of bm x bn: kModeDual counts both weights' columns, kModePair both products.
+inline int64_t lin_tiles_count(const LinGemm& p, int bm, int bn) {
+  const int bno = p.mode == kModeDual ? bn / 2 : bn;
+  return (p.M + bm - 1) / bm * ((p.N + bno - 1) / bno) * (p.mode == kModePair ? 2 : 1);
+}
 
 // The general kernel: any layout, alignment and size.
-int64_t lin_staged_ws(const LinGemm& p);
-hipError_t lin_staged_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s);
+constexpr int kStagedRow = 128;   // bytes of K in a stage
+struct StagedShape {
+  int edge, splits;               // of a tile; workgroups that split a tile's K
+  int64_t tiles;
+};
+hipError_t lin_staged_launch(const LinGemm& p, const StagedShape& h, hipStream_t s);
 
-// The tiled bf16 kernels, where lin_tiles_ok: 16-byte aligned operands and rows,
-// K a multiple of 32, a row-contiguous operand of whole 8-column groups.
-bool lin_tiles_ok(const LinGemm& p);
+// The tiled bf16 kernels: 16-byte aligned operands and rows, K a multiple of 32, a
+// row-contiguous operand of whole 8-column groups.
 enum Tile { kTile256, kTile192, kTile128w, kTile128, kTile64, kTile64short, kTile64k32 };
 struct TilePick {
   int tile;     // Tile
   int splits;   // workgroups that split a tile's K
 };
-// Tiles of a launch of bm x bn: kModeDual counts both weights' columns, kModePair both products.
-
-inline int64_t lin_tiles_count(const LinGemm& p, int bm, int bn) {
-  const int bno = p.mode == kModeDual ? bn / 2 : bn;
-  return (p.M + bm - 1) / bm * ((p.N + bno - 1) / bno) * (p.mode == kModePair ? 2 : 1);
-}
 hipError_t lin_tiles_one(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_dual(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_cat(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_pair(const LinGemm& p, const TilePick& t, hipStream_t s);
 
-// The kernel for few rows, where lin_rows_ok.  Given lin_rows_ws bytes of
-// workspace, several workgroups may split a tile's K.
-bool lin_rows_ok(const LinGemm& p);
-int64_t lin_rows_ws(const LinGemm& p);
-hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s);
+// The kernel for few rows.
+constexpr int kRowsWaves = 8;   // of a workgroup, at most (measured against 4 and 16 with one token)
+struct RowsShape {
+  int g, waves, splits;         // columns of a tile (16 g), waves of a workgroup, workgroups of a tile
+  int64_t tiles, cells;         // cells: floats of a workgroup's partial
+};
+hipError_t lin_rows_launch(const LinGemm& p, const RowsShape& h, hipStream_t s);
 
 // ---- gradients at the activation -----------------------------------------
 // kLinear: d_pre = d_out * act'(pre) (pre NULL: d_pre = d_out, not written) and,
@@ -102,7 +109,13 @@ struct ActGrad {
   int32_t f32 = 0, act = 0, gated = 0, accumulate = 0;
   uint32_t *tickets = nullptr;              // kMaxTickets to set to zero, or null
 };
-int64_t act_grad_slabs(int64_t M, int64_t N);   // rows of `parts`
+// The launch: lanes of a row, tiles of columns, rows of a slab, and slabs (rows of `parts`).
+struct ActGrid {
+  int lanes;
+  int64_t tiles, rows, slabs;
+};
+constexpr int kActThreads = 256, kActCols = 8;   // of a workgroup; columns of a lane
+ActGrid act_grad_grid(int64_t M, int64_t N);
 hipError_t act_grad_launch(const ActGrad& p, hipStream_t s);
 hipError_t zero_tickets_launch(uint32_t *tickets, hipStream_t s);
 

@@ -150,7 +150,7 @@ BwdWs linear_ws(const tp_linear_bwd_args *a) {
   BwdWs w;
   w.keeps = a->act != TP_ACT_NONE && (a->dX || a->dW) && a->M > 0;
   w.parts = w.keeps ? round_up(a->M * a->N * dtype_size(a->dtype), kWsAlign) : 0;
-  w.join = w.parts + (a->dbias ? round_up(act_grad_slabs(a->M, a->N) * a->N * 4, kWsAlign) : 0);
+  w.join = w.parts + (a->dbias ? round_up(act_grad_grid(a->M, a->N).slabs * a->N * 4, kWsAlign) : 0);
   const int64_t x = a->dX ? lin_gemm_ws(dx_product(a->M, a->N, a->K, a->dtype, linear, false)) : 0;
   const int64_t y = a->dW ? lin_gemm_ws(dw_product(a->M, a->N, a->K, a->dtype, linear, false)) : 0;
   w.total = w.join + std::max(x, y);

@@ -1,4 +1,6 @@
-// Which kernel a product of the linear layer or the gated block runs on.
+// Which kernel a product of the linear layer or the gated block runs on, its tiles
+// and its workspace.  Host code only: what a launch reads and writes can be checked
+// without a GPU.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -14,18 +16,85 @@ bool aligned(const void *p, int64_t ld, int64_t es, int64_t elems) {
   return !p || (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(elems * es) == 0 && ld % elems == 0);
 }
 
-}  // namespace
-
-bool lin_tiles_ok(const LinGemm& p) {
+// Whether the tiled bf16 kernels take it.
+bool tiles_ok(const LinGemm& p) {
   if (p.f32 || p.K <= 0 || p.K % 32) return false;
   if (!aligned(p.a, p.lda, 2, 8) || !aligned(p.a2, p.lda, 2, 8) || !aligned(p.w, p.ldw, 2, 8) || !aligned(p.w2, p.ldw, 2, 8))
     return false;
   return (!p.a_t || p.M % 8 == 0) && (p.w_t || p.N % 8 == 0);
 }
 
-namespace {
-
 constexpr int64_t kCUs = 256;
+
+// ---- few rows ----------------------------------------------------------------
+// Up to 16 rows (one operand's worth); with a k-contiguous weight up to 64, since
+// there more rows cost accumulators only (an n-contiguous one keeps four columns
+// a lane, and their accumulators spill).
+bool rows_ok(const LinGemm& p) {
+  return p.M <= (p.w_t ? 64 : 16) && !p.a_t && p.K > 0 && (p.mode == kModeOne || p.mode == kModeDual) && !p.acc_c;
+}
+
+RowsShape rows_shape(const LinGemm& p) {
+  const int es = p.f32 ? 4 : 2, mats = p.mode == kModeDual ? 2 : 1;
+  RowsShape s;
+  s.g = p.w_t ? 1 : 8 / es;
+  const int tc = 16 * s.g;
+  s.tiles = (p.N + tc - 1) / tc;
+  s.cells = mats * p.M * tc;
+  const int64_t steps = (p.K * es + 63) / 64;
+  s.waves = kRowsWaves;
+  while (s.waves > 1 && (s.waves * 2 > steps || s.waves * s.cells * 4 > 64 * 1024)) s.waves /= 2;
+  // Workgroups of a tile: until every CU has one (a wave keeping two steps),
+  // then up to two each where a workgroup still reads 256 KiB, which pays for
+  // the join.  MI355X, one token: gated 12288 -> 6144 (k-contiguous) 65 us with
+  // 384 workgroups, 55 with 768; 6144 -> 12288 (n-contiguous) 36 with 384, 31
+  // with 768; but gated 4096 -> 2048 (131 KiB each at 256) 10.4 with 256, 11.7
+  // with 512.
+  s.splits = 1;
+  static_assert(kMaxTickets >= 512, "a ticket for every tile that is split");
+  while (s.splits < 16 && s.splits * 2 * s.waves * 2 <= steps) {
+    const int64_t wgs = s.tiles * s.splits, each = static_cast<int64_t>(mats) * tc * es * p.K / s.splits;
+    if (wgs >= 512 || (wgs >= 256 && each < 256 * 1024)) break;
+    s.splits *= 2;
+  }
+  return s;
+}
+
+int64_t ws_of(const RowsShape& h) { return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * h.cells * 4 : 0; }
+
+// ---- any layout and size -------------------------------------------------------
+// The tile's edge and the workgroups that split its K, by estimated time.  With
+// k workgroups to the busiest CU a stage takes max(alone, k * shared) us, and
+// joining S > 1 splits 2 us and 7 ns a workgroup (their partials' trip to memory
+// and back).  The constants are fitted to MI355X times, e.g. (bf16 / fp32)
+// 2049 x 2047 x 2049: edge 128 60 / 281 us, edge 64 71 / 194; 100 x 4097 x 2049: 29 / 88
+// unsplit, 16 / 36 with three splits; 515 x 1021 x 1531: 13 / 28 unsplit, 20 / 32
+// with four.
+StagedShape staged_shape(const LinGemm& p, bool may_split) {
+  const int64_t stages = (p.K * (p.f32 ? 4 : 2) + kStagedRow - 1) / kStagedRow * (p.mode == kModeCat ? 2 : 1);
+  StagedShape best{64, 1, 0};
+  double least = 0.0;
+  for (int edge = 128; edge >= 64; edge -= 64) {
+    const double shared = p.f32 ? (edge == 128 ? 2.08 : 0.58) : (edge == 128 ? 0.87 : 0.38);
+    const double alone = p.f32 ? (edge == 128 ? 2.35 : 0.72) : (edge == 128 ? 1.1 : 0.55);
+    const int64_t tiles = lin_tiles_count(p, edge, edge);
+    // Only 64 x 64 tiles are split, few enough for a ticket each, down to 4 stages.
+    for (int s = 1; s <= 16 && (s == 1 || (may_split && edge == 64 && tiles <= kMaxTickets && 4 * s <= stages)); ++s) {
+      const int64_t k = (tiles * s + kCUs - 1) / kCUs;
+      const double t = static_cast<double>((stages + s - 1) / s) * std::max(alone, shared * static_cast<double>(k)) +
+                       (s > 1 ? 2.0 + 0.007 * static_cast<double>(tiles * s) : 0.0);
+      if (!best.tiles || t < least) {
+        best = {edge, s, tiles};
+        least = t;
+      }
+    }
+  }
+  return best;
+}
+
+int64_t ws_of(const StagedShape& h) { return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * 64 * 64 * 4 : 0; }
+
+// ---- tiled bf16 ----------------------------------------------------------------
 
 // The small tile: 64 rows by 64 columns (of each weight).
 int64_t small_tiles(const LinGemm& p) { return lin_tiles_count(p, 64, p.mode == kModeDual ? 128 : 64); }
@@ -72,19 +141,35 @@ int64_t ws_of(const LinGemm& p, const TilePick& t) {
 // 8.8 us against 12.9, but 6144 -> 12288 56 against 43, each row group reading
 // its activations again).
 bool takes_rows(const LinGemm& p) {
-  if (!lin_rows_ok(p)) return false;
-  if (p.M <= 16 || !lin_tiles_ok(p)) return true;
+  if (!rows_ok(p)) return false;
+  if (p.M <= 16 || !tiles_ok(p)) return true;
   return p.M <= 32 && (p.mode == kModeDual ? 2 : 1) * p.N * p.K < 50'000'000;
 }
 
+// Splits K only where the workspace holds the tickets and partials.
+void take_ws(LinGemm *p, void *ws) {
+  p->tickets = static_cast<uint32_t *>(ws);
+  p->join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
+}
+
+hipError_t launch_rows(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
+  RowsShape h = rows_shape(p);
+  if (!ws || ws_bytes < ws_of(h)) h.splits = 1;
+  if (h.splits > 1) take_ws(&p, ws);
+  return lin_rows_launch(p, h, s);
+}
+
+hipError_t launch_staged(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
+  StagedShape h = staged_shape(p, true);
+  if (!ws || ws_bytes < ws_of(h)) h = staged_shape(p, false);
+  if (h.splits > 1) take_ws(&p, ws);
+  return lin_staged_launch(p, h, s);
+}
+
 hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
-  if (p.M <= 0 || p.N <= 0) return hipSuccess;
   TilePick t = pick(p);
   if (!ws || ws_bytes < ws_of(p, t)) t.splits = 1;
-  if (t.splits > 1) {
-    p.tickets = static_cast<uint32_t *>(ws);
-    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
-  }
+  if (t.splits > 1) take_ws(&p, ws);
   if (p.a_t) return lin_tiles_pair(p, t, s);
   switch (p.mode) {
     case kModeOne: return lin_tiles_one(p, t, s);
@@ -96,17 +181,42 @@ hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
 
 }  // namespace
 
-// (Asked before the strides are known: enough for either kernel.)
-int64_t lin_gemm_ws(const LinGemm& p) {
-  if (p.M <= 0 || p.N <= 0) return 0;
-  if (takes_rows(p)) return lin_rows_ws(p);
-  return std::max(lin_tiles_ok(p) ? ws_of(p, pick(p)) : 0, lin_staged_ws(p));
+// A launch holds fewer than 2^32 threads. Tiles: up to 2^22 of 64 x 64, 256
+// threads each, twice where two products share a launch (2^31). Few rows: 16
+// columns to a workgroup of up to 512 threads, so N below 2^26 (2^31).
+bool lin_grid_ok(int64_t M, int64_t N) {
+  return N < (int64_t{1} << 26) && ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22);
 }
 
-hipError_t lin_gemm_launch(LinGemm p, hipStream_t s, void *ws, int64_t ws_bytes) {
-  if (takes_rows(p)) return lin_rows_launch(p, ws, ws_bytes, s);
-  if (lin_tiles_ok(p)) return launch_tiles(p, ws, ws_bytes, s);
-  return lin_staged_launch(p, ws, ws_bytes, s);
+// Asked before strides and addresses are known, so for aligned ones.  What an
+// unaligned call runs on instead asks for no more: the general kernel's need is
+// counted, and the few-row kernel's (17 to 64 rows) stays below the others'.
+int64_t lin_gemm_ws(const LinGemm& p) {
+  if (p.M <= 0 || p.N <= 0) return 0;
+  if (takes_rows(p)) return ws_of(rows_shape(p));
+  return std::max(tiles_ok(p) ? ws_of(p, pick(p)) : 0, ws_of(staged_shape(p, true)));
+}
+
+hipError_t lin_gemm_launch(const LinGemm& p, hipStream_t s, void *ws, int64_t ws_bytes) {
+  if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  if (takes_rows(p)) return launch_rows(p, ws, ws_bytes, s);
+  if (tiles_ok(p)) return launch_tiles(p, ws, ws_bytes, s);
+  return launch_staged(p, ws, ws_bytes, s);
+}
+
+// The grid of the activation's gradient: 64 rows to a slab, fewer where that leaves
+// under 1024 workgroups (1021 x 999, gated: 67 us in 32 workgroups), though not
+// so few that the partial rows weigh more than an eighth of the input, nor so
+// many slabs that they exceed the grid.
+ActGrid act_grad_grid(int64_t M, int64_t N) {
+  ActGrid g{64, 0, 64, 0};
+  while (g.lanes > 1 && (g.lanes / 2) * kActCols >= N) g.lanes /= 2;
+  g.tiles = (N + g.lanes * kActCols - 1) / (g.lanes * kActCols);
+  const int64_t least = std::max<int64_t>(16, kActThreads / g.lanes);
+  while (g.rows > least && g.tiles * ((M + g.rows - 1) / g.rows) < 1024) g.rows /= 2;
+  g.rows = std::max(std::max(g.rows, least), (M + 1023) / 1024);
+  g.slabs = (M + g.rows - 1) / g.rows;
+  return g;
 }
 
 }  // namespace tpshard

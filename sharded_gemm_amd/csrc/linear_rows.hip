@@ -99,11 +99,8 @@ struct Cols {
   }
 };
 
-// Waves of a workgroup (measured against 4 and 16 with one token).
-constexpr int kWaves = 8;
-
 template <typename T, bool WKC, bool DUAL, int G, int MT>
-__global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
+__global__ void __launch_bounds__(64 * kRowsWaves) lin_rows_kernel(LinGemm p) {
   constexpr int PER = 16 / sizeof(T);          // k of a lane in a step
   constexpr int STEP = 4 * PER;                // k of a step
   constexpr int MATS = DUAL ? 2 : 1;
@@ -313,41 +310,8 @@ __global__ void __launch_bounds__(64 * kWaves) lin_rows_kernel(LinGemm p) {
   });
 }
 
-// The launch: columns of a tile (16 g), waves of a workgroup and workgroups of a
-// tile.
-struct Shape {
-  int g, waves, splits;
-  int64_t tiles, cells;    // cells: floats of a workgroup's partial
-};
-
-Shape shape_of(const LinGemm& p) {
-  const int es = p.f32 ? 4 : 2, mats = p.mode == kModeDual ? 2 : 1;
-  Shape s;
-  s.g = p.w_t ? 1 : 8 / es;
-  const int tc = 16 * s.g;
-  s.tiles = (p.N + tc - 1) / tc;
-  s.cells = mats * p.M * tc;
-  const int64_t steps = (p.K * es + 63) / 64;
-  s.waves = kWaves;
-  while (s.waves > 1 && (s.waves * 2 > steps || s.waves * s.cells * 4 > 64 * 1024)) s.waves /= 2;
-  // Workgroups of a tile: until every CU has one (a wave keeping two steps),
-  // then up to two each where a workgroup still reads 256 KiB, which pays for
-  // the join.  MI355X, one token: gated 12288 -> 6144 (k-contiguous) 65 us with
-  // 384 workgroups, 55 with 768; 6144 -> 12288 (n-contiguous) 36 with 384, 31
-  // with 768; but gated 4096 -> 2048 (131 KiB each at 256) 10.4 with 256, 11.7
-  // with 512.
-  s.splits = 1;
-  static_assert(kMaxTickets >= 512, "a ticket for every tile that is split");
-  while (s.splits < 16 && s.splits * 2 * s.waves * 2 <= steps) {
-    const int64_t wgs = s.tiles * s.splits, each = static_cast<int64_t>(mats) * tc * es * p.K / s.splits;
-    if (wgs >= 512 || (wgs >= 256 && each < 256 * 1024)) break;
-    s.splits *= 2;
-  }
-  return s;
-}
-
 template <typename T, bool WKC, bool DUAL, int G>
-hipError_t by_rows(const LinGemm& p, const Shape& h, hipStream_t s) {
+hipError_t by_rows(const LinGemm& p, const RowsShape& h, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits)), block(64 * h.waves);
   const unsigned lds = static_cast<unsigned>(h.waves * h.cells * 4);
   if (p.M <= 16) hipLaunchKernelGGL((lin_rows_kernel<T, WKC, DUAL, G, 1>), grid, block, lds, s, p);
@@ -358,34 +322,14 @@ hipError_t by_rows(const LinGemm& p, const Shape& h, hipStream_t s) {
 }
 
 template <typename T, bool DUAL>
-hipError_t by_layout(const LinGemm& p, const Shape& h, hipStream_t s) {
+hipError_t by_layout(const LinGemm& p, const RowsShape& h, hipStream_t s) {
   if (p.w_t) return by_rows<T, true, DUAL, 1>(p, h, s);
   return by_rows<T, false, DUAL, 8 / static_cast<int>(sizeof(T))>(p, h, s);
 }
 
 }  // namespace
 
-// Up to 16 rows (one operand's worth); with a k-contiguous weight up to 64, since
-// there more rows cost accumulators only (an n-contiguous one keeps four columns
-// a lane, and their accumulators spill).
-bool lin_rows_ok(const LinGemm& p) {
-  return p.M <= (p.w_t ? 64 : 16) && !p.a_t && p.K > 0 && (p.mode == kModeOne || p.mode == kModeDual) && !p.acc_c;
-}
-
-int64_t lin_rows_ws(const LinGemm& p) {
-  if (!lin_rows_ok(p) || p.M <= 0 || p.N <= 0) return 0;
-  const Shape h = shape_of(p);
-  return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * h.cells * 4 : 0;
-}
-
-hipError_t lin_rows_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
-  if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  Shape h = shape_of(p);
-  if (!ws || ws_bytes < lin_rows_ws(p)) h.splits = 1;
-  if (h.splits > 1) {
-    p.tickets = static_cast<uint32_t *>(ws);
-    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
-  }
+hipError_t lin_rows_launch(const LinGemm& p, const RowsShape& h, hipStream_t s) {
   const bool dual = p.mode == kModeDual;
   if (p.f32) return dual ? by_layout<uint32_t, true>(p, h, s) : by_layout<uint32_t, false>(p, h, s);
   return dual ? by_layout<uint16_t, true>(p, h, s) : by_layout<uint16_t, false>(p, h, s);

@@ -23,8 +23,6 @@
 // 1021 x 1531 28 us (58); bf16 4097 x 4095 x 4097 270 us (509), the gated
 // backward 1021 x 1337 -> 999 32 + 25 us.  Odd strides cost: a 16-byte load off a
 // 4-byte boundary goes through the address unit a lane at a time.
-#include <algorithm>
-
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -33,7 +31,7 @@ using namespace lin;
 
 namespace {
 
-constexpr int kRow = 128;                 // LDS bytes of a tile row per stage
+constexpr int kRow = kStagedRow;          // LDS bytes of a tile row per stage
 
 __device__ __forceinline__ uint32_t lds_at(int r, int c) {
   return static_cast<uint32_t>(r * kRow + ((c ^ ((r ^ (r >> 3)) & 7)) << 4));
@@ -342,43 +340,8 @@ __global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_ker
   else epilogue<uint16_t, MODE>(p, c, acc, rm, cn);
 }
 
-constexpr int64_t kCUs = 256;
-
-// The tile's edge and the workgroups that split its K, by estimated time.  With
-// k workgroups to the busiest CU a stage takes max(alone, k * shared) us, and
-// joining S > 1 splits 2 us and 7 ns a workgroup (their partials' trip to memory
-// and back).  The constants are fitted to MI355X times, e.g. (bf16 / fp32)
-// 2049 x 2047 x 2049: edge 128 60 / 281 us, edge 64 71 / 194; 100 x 4097 x 2049: 29 / 88
-// unsplit, 16 / 36 with three splits; 515 x 1021 x 1531: 13 / 28 unsplit, 20 / 32
-// with four.
-struct Shape {
-  int edge, splits;
-  int64_t tiles;
-};
-Shape shape_of(const LinGemm& p, bool may_split) {
-  const int64_t stages = (p.K * (p.f32 ? 4 : 2) + kRow - 1) / kRow * (p.mode == kModeCat ? 2 : 1);
-  Shape best{64, 1, 0};
-  double least = 0.0;
-  for (int edge = 128; edge >= 64; edge -= 64) {
-    const double shared = p.f32 ? (edge == 128 ? 2.08 : 0.58) : (edge == 128 ? 0.87 : 0.38);
-    const double alone = p.f32 ? (edge == 128 ? 2.35 : 0.72) : (edge == 128 ? 1.1 : 0.55);
-    const int64_t tiles = lin_tiles_count(p, edge, edge);
-    // Only 64 x 64 tiles are split, few enough for a ticket each, down to 4 stages.
-    for (int s = 1; s <= 16 && (s == 1 || (may_split && edge == 64 && tiles <= kMaxTickets && 4 * s <= stages)); ++s) {
-      const int64_t k = (tiles * s + kCUs - 1) / kCUs;
-      const double t = static_cast<double>((stages + s - 1) / s) * std::max(alone, shared * static_cast<double>(k)) +
-                       (s > 1 ? 2.0 + 0.007 * static_cast<double>(tiles * s) : 0.0);
-      if (!best.tiles || t < least) {
-        best = {edge, s, tiles};
-        least = t;
-      }
-    }
-  }
-  return best;
-}
-
 template <typename T, bool AKC, bool WKC, int MODE>
-hipError_t launch(const LinGemm& p, const Shape& h, hipStream_t s) {
+hipError_t launch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits));
   if (h.edge == 128) hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), grid, dim3(threads_of(128)), 0, s, p);
   else hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), grid, dim3(threads_of(64)), 0, s, p);
@@ -386,7 +349,7 @@ hipError_t launch(const LinGemm& p, const Shape& h, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t dispatch(const LinGemm& p, const Shape& h, hipStream_t s) {
+hipError_t dispatch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
   const bool akc = !p.a_t, wkc = p.w_t != 0;
   switch (p.mode) {
     case kModeOne:
@@ -408,25 +371,7 @@ hipError_t dispatch(const LinGemm& p, const Shape& h, hipStream_t s) {
 
 }  // namespace
 
-// A launch holds fewer than 2^32 threads. Tiles: up to 2^22 of 64 x 64, 256
-// threads each, twice where two products share a launch (2^31). Few rows: 16
-// columns to a workgroup of up to 512 threads, so N below 2^26 (2^31).
-bool lin_grid_ok(int64_t M, int64_t N) {
-  return N < (int64_t{1} << 26) && ((M + 63) / 64) * ((N + 63) / 64) < (int64_t{1} << 22);
-}
-
-int64_t lin_staged_ws(const LinGemm& p) {
-  const Shape h = shape_of(p, true);
-  return h.splits > 1 ? kTicketBytes + h.tiles * h.splits * 64 * 64 * 4 : 0;
-}
-
-hipError_t lin_staged_launch(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
-  if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  const Shape h = shape_of(p, ws && ws_bytes >= lin_staged_ws(p));
-  if (h.splits > 1) {
-    p.tickets = static_cast<uint32_t *>(ws);
-    p.join = reinterpret_cast<float *>(static_cast<char *>(ws) + kTicketBytes);
-  }
+hipError_t lin_staged_launch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
   return p.f32 ? dispatch<uint32_t>(p, h, s) : dispatch<uint16_t>(p, h, s);
 }
 
