@@ -35,7 +35,8 @@ enum {
   TP_ERR_SPEC = -2,        /* ill-formed layout (axis range, device counts, map keys) */
   TP_ERR_INDIVISIBLE = -3, /* a dim is not a multiple of its shard / chunk count */
   TP_ERR_UNSUPPORTED = -4, /* well-formed but outside what this library does */
-  TP_ERR_HIP = -5          /* a HIP runtime call failed (message has hipGetErrorString) */
+  TP_ERR_HIP = -5          /* a HIP runtime call failed (message has hipGetErrorString),
+                              or host memory ran out (tp_grad_*) */
 };
 
 /* Message describing the last failing call on the calling thread ("" if none).

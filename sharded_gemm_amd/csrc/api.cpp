@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstring>
 #include <map>
 #include <string>
 #include <vector>
@@ -17,20 +18,20 @@
 namespace tpshard {
 
 namespace {
-thread_local std::string g_last_error;
+thread_local char g_last_error[512];   // (its use cannot fail)
 }
 
 int fail(int code, const char *fmt, ...) {
-  char buf[512];
+  char buf[sizeof g_last_error];   // (an argument may be the last message)
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof buf, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
+  memcpy(g_last_error, buf, sizeof buf);
   return code;
 }
 
-void clear_error() { g_last_error.clear(); }
+void clear_error() { g_last_error[0] = '\0'; }
 
 namespace {
 
@@ -527,7 +528,7 @@ using namespace tpshard;
 
 extern "C" {
 
-const char *tp_last_error(void) { return g_last_error.c_str(); }
+const char *tp_last_error(void) { return g_last_error; }
 
 const char *tp_version(void) { return "tpshard 0.1 gfx950"; }
 

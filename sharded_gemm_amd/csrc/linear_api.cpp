@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <new>
 #include <vector>
 
 #include "common.h"
@@ -54,14 +56,12 @@ bool share(const Mat& a, const Mat& b) {
   return at < static_cast<uintptr_t>(a.cols * a.es) || at + static_cast<uintptr_t>(b.cols * b.es) > pitch;
 }
 
-int disjoint(const std::vector<Mat>& ins, const std::vector<Mat>& outs) {
-  for (size_t i = 0; i < outs.size(); ++i) {
+int disjoint(std::initializer_list<Mat> ins, std::initializer_list<Mat> outs) {
+  for (const Mat *o = outs.begin(); o != outs.end(); ++o) {
     for (const Mat& in : ins)
-      if (share(outs[i], in))
-        return fail(TP_ERR_ARG, "%s overlaps %s", outs[i].name, in.name);
-    for (size_t j = 0; j < i; ++j)
-      if (share(outs[i], outs[j]))
-        return fail(TP_ERR_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
+      if (share(*o, in)) return fail(TP_ERR_ARG, "%s overlaps %s", o->name, in.name);
+    for (const Mat *e = outs.begin(); e != o; ++e)
+      if (share(*o, *e)) return fail(TP_ERR_ARG, "%s overlaps %s", o->name, e->name);
   }
   return TP_OK;
 }
@@ -227,9 +227,7 @@ int tp_linear(const tp_linear_args *a, tp_stream_t stream) {
     return rc;
   // Each output element is written by the lane that read the residual's.
   const bool in_place = r.p && r.p == o.p && r.ld == o.ld && es == oes;
-  std::vector<Mat> ins = {x, w, b};
-  if (!in_place) ins.push_back(r);
-  if ((rc = disjoint(ins, {o, pre, wsm})) != TP_OK) return rc;
+  if ((rc = disjoint({x, w, b, in_place ? Mat{} : r}, {o, pre, wsm})) != TP_OK) return rc;
   if (in_place && (rc = disjoint({r}, {pre})) != TP_OK) return rc;
   if (!any) return TP_OK;
   LinGemm p;
@@ -511,6 +509,8 @@ int take_grads(const tp_grad_tensor *ts, int64_t num, bool clip, std::vector<Gra
   return TP_OK;
 }
 
+int no_memory() { return fail(TP_ERR_HIP, "out of host memory"); }
+
 double grad_bytes(const std::vector<GradTensor>& ts) {
   double b = 0;
   for (const GradTensor& t : ts) b += static_cast<double>(t.n) * (t.f32 ? 4 : 2);
@@ -521,7 +521,7 @@ double grad_bytes(const std::vector<GradTensor>& ts) {
 
 extern "C" {
 
-int tp_grad_sumsq(const tp_grad_tensor *tensors, int64_t num, double *parts, tp_stream_t stream) {
+int tp_grad_sumsq(const tp_grad_tensor *tensors, int64_t num, double *parts, tp_stream_t stream) try {
   clear_error();
   std::vector<GradTensor> ts;
   int rc = take_grads(tensors, num, false, &ts);
@@ -535,10 +535,12 @@ int tp_grad_sumsq(const tp_grad_tensor *tensors, int64_t num, double *parts, tp_
   if (e != hipSuccess) return hip_fail(e, "sum of squares launch");
   timing_end(t0, s, TP_KERNEL_REDUCE, grad_bytes(ts));
   return TP_OK;
+} catch (const std::bad_alloc&) {
+  return no_memory();
 }
 
 int tp_grad_clip(const tp_grad_tensor *tensors, int64_t num, const double *parts, int64_t ranks, double max_norm,
-                 double eps, float *norm_out, tp_stream_t stream) {
+                 double eps, float *norm_out, tp_stream_t stream) try {
   clear_error();
   std::vector<GradTensor> ts;
   const int rc = take_grads(tensors, num, true, &ts);
@@ -576,6 +578,8 @@ int tp_grad_clip(const tp_grad_tensor *tensors, int64_t num, const double *parts
   if (e != hipSuccess) return hip_fail(e, "clipping launch");
   timing_end(t0, s, TP_KERNEL_REDUCE, 2.0 * grad_bytes(ts));
   return TP_OK;
+} catch (const std::bad_alloc&) {
+  return no_memory();
 }
 
 }  // extern "C"

@@ -6,6 +6,8 @@
 // buffers are fake addresses.
 //
 //   driver            random calls; prints one summary line
+//   driver nomem      every call again with each of its host allocations failing
+//                     in turn: a status comes back, no exception
 //   driver choose     reads lines "op dtype layout M K N odd" (op: linear,
 //                     linear_bwd, gated, gated_bwd; odd: 1 takes operands off
 //                     every vector alignment) and prints the kernels each call
@@ -16,6 +18,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <iostream>
+#include <new>
 #include <random>
 #include <set>
 #include <string>
@@ -23,6 +26,18 @@
 
 #include "../../include/tpshard.h"
 #include "linear_stub.h"
+
+namespace {
+long g_allocs_left = -1;   // allocations until one fails (-1: none does)
+}
+
+void *operator new(std::size_t n) {
+  if (g_allocs_left >= 0 && g_allocs_left-- == 0) throw std::bad_alloc();
+  if (void *p = std::malloc(n ? n : 1)) return p;
+  throw std::bad_alloc();
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
 
 namespace {
 
@@ -289,10 +304,106 @@ void grads(std::mt19937& rng) {
   }
 }
 
+// f() with its n-th allocation failing, for every n.
+template <typename F>
+long starve(F&& f) {
+  long failed = 0;
+  for (long n = 0; n < 1000; ++n) {
+    int rc;
+    lin_stub_quiet(true);
+    g_allocs_left = n;
+    try {
+      rc = f();
+    } catch (...) {
+      g_allocs_left = -1;
+      std::fprintf(stderr, "an exception left a C entry (allocation %ld)\n", n);
+      std::abort();
+    }
+    const bool hit = g_allocs_left < 0;
+    g_allocs_left = -1;
+    lin_stub_quiet(false);
+    if (!hit) {
+      expect(rc == TP_OK || rc == TP_ERR_ARG, "a call with memory");
+      return failed;
+    }
+    ++failed;
+    expect(rc == TP_ERR_HIP || rc == TP_ERR_ARG, "a call without memory");
+    expect(std::strlen(tp_last_error()) > 0, "its message");
+  }
+  return failed;
+}
+
+int nomem() {
+  fresh();
+  char *p = dev(1 << 22), *o = dev(1 << 22);
+  auto at = [&](int i) { return p + i * (1 << 16); };
+  long failed = 0;
+  for (bool good : {true, false}) {      // a valid call, and one refused with a long message
+    tp_linear_args l{};
+    l.dtype = l.out_dtype = TP_BF16;
+    l.M = 32;
+    l.N = l.K = 64;
+    l.X = at(0);
+    l.W = at(1);
+    l.bias = reinterpret_cast<float *>(at(2));
+    l.residual = at(3);
+    l.out = good ? at(4) : at(0);
+    failed += starve([&] { return tp_linear(&l, nullptr); });
+    tp_linear_bwd_args b{};
+    b.dtype = b.dx_dtype = b.dw_dtype = TP_BF16;
+    b.act = TP_ACT_SILU;
+    b.M = 32;
+    b.N = b.K = 64;
+    b.X = at(0);
+    b.W = at(1);
+    b.dOut = at(2);
+    b.pre = at(3);
+    b.dX = good ? at(4) : at(0);
+    b.dW = at(5);
+    b.dbias = reinterpret_cast<float *>(at(6));
+    b.ws = o;
+    b.ws_bytes = 1 << 22;
+    failed += starve([&] { return tp_linear_backward(&b, nullptr); });
+    tp_gated_args g{};
+    g.dtype = TP_BF16;
+    g.M = 32;
+    g.F = g.K = 64;
+    g.X = at(0);
+    g.W_gate = at(1);
+    g.W_up = at(2);
+    g.out = good ? at(3) : at(0);
+    failed += starve([&] { return tp_gated_linear(&g, nullptr); });
+    tp_gated_bwd_args q{};
+    q.dtype = q.dx_dtype = q.dw_dtype = TP_BF16;
+    q.M = 32;
+    q.F = q.K = 64;
+    q.X = at(0);
+    q.W_gate = at(1);
+    q.W_up = at(2);
+    q.gate = at(3);
+    q.up = at(4);
+    q.dOut = at(5);
+    q.dX = good ? at(6) : at(0);
+    q.dW_gate = at(7);
+    q.dW_up = at(8);
+    q.ws = o;
+    q.ws_bytes = 1 << 22;
+    failed += starve([&] { return tp_gated_linear_backward(&q, nullptr); });
+    std::vector<tp_grad_tensor> ts;
+    for (int i = 0; i < 40; ++i) ts.push_back({at(i), good ? at(i) : at(0), 100, TP_F32});
+    auto *parts = reinterpret_cast<double *>(o);
+    failed += starve([&] { return tp_grad_sumsq(ts.data(), 40, parts, nullptr); });
+    failed += starve([&] { return tp_grad_clip(ts.data(), 40, parts, 2, 1.0, 1e-6, nullptr, nullptr); });
+  }
+  std::printf("failed %ld\n", failed);
+  return 0;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
   if (argc > 1 && !std::strcmp(argv[1], "choose")) return choose();
+  if (argc > 1 && !std::strcmp(argv[1], "nomem")) return nomem();
   std::mt19937 rng(1);
   std::set<std::string> kernels;
   long calls = 0, split = 0;

@@ -18,6 +18,7 @@ struct Range {
 };
 std::vector<Range> g_allocs;
 std::vector<std::string> g_seen;
+bool g_quiet = false;
 
 void check(bool ok, const char *what) {
   if (ok) return;
@@ -77,8 +78,9 @@ void split(const tpshard::LinGemm& p, int splits, int64_t tiles, int64_t floats)
   need(p.tickets, 1, kTicketBytes + tiles * splits * floats * 4, kTicketBytes + tiles * splits * floats * 4, 1, "workspace", 8);
 }
 
-void seen(const std::string& kernel, const tpshard::LinGemm& p, int splits) {
-  std::string s = kernel + " " + mode_name(p.mode) + (p.a_t ? " a^T" : " a") + (p.w_t ? " w^T" : " w");
+void seen(const char *type, const char *kernel, int n, const tpshard::LinGemm& p, int splits) {
+  if (g_quiet) return;
+  std::string s = std::string(type) + kernel + (n ? std::to_string(n) : "") + " " + mode_name(p.mode) + (p.a_t ? " a^T" : " a") + (p.w_t ? " w^T" : " w");
   if (splits > 1) g_seen.push_back(s + " split");
   g_seen.push_back(s);
 }
@@ -95,6 +97,7 @@ void lin_stub_register(const void *p, int64_t bytes) {
   g_allocs.push_back({lo, lo + static_cast<uintptr_t>(bytes)});
 }
 void lin_stub_reset() { g_allocs.clear(); }
+void lin_stub_quiet(bool on) { g_quiet = on; }
 
 namespace tpshard {
 
@@ -110,7 +113,7 @@ hipError_t lin_rows_launch(const LinGemm& p, const RowsShape& h, hipStream_t) {
   grid(h.tiles, h.splits, 64 * h.waves);
   split(p, h.splits, h.tiles, h.cells);
   const int mt = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-  seen(std::string(p.f32 ? "f32 " : "bf16 ") + "rows" + std::to_string(16 * mt), p, h.splits);
+  seen(p.f32 ? "f32 " : "bf16 ", "rows", 16 * mt, p, h.splits);
   return hipSuccess;
 }
 
@@ -122,7 +125,7 @@ hipError_t lin_staged_launch(const LinGemm& p, const StagedShape& h, hipStream_t
   check(p.a_t ? (p.mode == kModeOne || p.mode == kModePair) && !p.w_t : p.mode != kModePair, "general: no such instance");
   grid(h.tiles, h.splits, h.edge == 128 ? 512 : 256);
   split(p, h.splits, h.tiles, 64 * 64);
-  seen(std::string(p.f32 ? "f32 " : "bf16 ") + "general" + std::to_string(h.edge), p, h.splits);
+  seen(p.f32 ? "f32 " : "bf16 ", "general", h.edge, p, h.splits);
   return hipSuccess;
 }
 
@@ -147,7 +150,7 @@ hipError_t tiles(const LinGemm& p, const TilePick& t, bool dual, bool cat) {
   grid(lin_tiles_count(p, bm[t.tile], n), t.splits, 512);
   check(lin_tiles_count(p, bm[t.tile], n) < (int64_t{1} << 31), "tiled: 32-bit tile numbers");
   split(p, t.splits, lin_tiles_count(p, bm[t.tile], n), 64 * n);
-  seen(names[t.tile], p, t.splits);
+  seen("", names[t.tile], 0, p, t.splits);
   return hipSuccess;
 }
 }  // namespace
@@ -190,7 +193,7 @@ hipError_t act_grad_launch(const ActGrad& p, hipStream_t) {
   if (p.M > 0) {
     grid(g.tiles, g.slabs, kActThreads);
     const bool flat = p.gated && p.ld_dout == p.N && p.ld_pre == p.N;
-    g_seen.push_back(std::string(p.f32 ? "f32 " : "bf16 ") + (flat ? "gated gradient, flat" : p.gated ? "gated gradient, rows" : "activation gradient"));
+    if (!g_quiet) g_seen.push_back(std::string(p.f32 ? "f32 " : "bf16 ") + (flat ? "gated gradient, flat" : p.gated ? "gated gradient, rows" : "activation gradient"));
   }
   if (p.colsum) grid((p.N + 63) / 64, 1, 1024);
   return hipSuccess;
@@ -220,7 +223,6 @@ void tables(const GradTensor *ts, int64_t num, bool outs) {
 hipError_t grad_sumsq_launch(const GradTensor *ts, int64_t num, double *parts, hipStream_t) {
   need(parts, 1, kGradParts, kGradParts, 8, "parts");
   tables(ts, num, false);
-  g_seen.push_back("sum of squares");
   return hipSuccess;
 }
 hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *parts, int64_t ranks, double, double,
@@ -228,7 +230,6 @@ hipError_t grad_clip_launch(const GradTensor *ts, int64_t num, const double *par
   need(parts, ranks, kGradParts, kGradParts, 8, "parts");
   if (norm_out) need(norm_out, 1, 1, 1, 4, "norm");
   tables(ts, num, true);
-  g_seen.push_back("clipping");
   return hipSuccess;
 }
 

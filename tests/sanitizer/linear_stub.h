@@ -9,3 +9,5 @@
 std::vector<std::string> lin_stub_take();
 void lin_stub_register(const void *p, int64_t bytes);
 void lin_stub_reset();
+// No names are kept (and nothing allocated) while quiet.
+void lin_stub_quiet(bool on);

@@ -56,6 +56,12 @@ def test_random_calls(driver):
     assert set(kernels.strip().split("\n")) == every_kernel()
 
 
+def test_no_exception_leaves_a_c_entry(driver):
+    """Each host allocation of each call failing in turn: a status and a message come back."""
+    out, _ = driver("nomem")
+    assert int(out.split()[1]) >= 10
+
+
 def every_kernel():
     """What the library is compiled for, by name: kernel, what its two weight operands mean, and their layouts."""
     forward = ["one a w", "one a w^T", "dual a w", "dual a w^T"]
