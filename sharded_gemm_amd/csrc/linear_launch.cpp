@@ -136,14 +136,22 @@ int64_t ws_of(const LinGemm& p, const TilePick& t) {
   return kTicketBytes + tiles * t.splits * 64 * (p.mode == kModeDual ? 128 : 64) * 4;
 }
 
-// Whether few rows run on their own kernel: always where the tiled ones cannot,
-// and up to 32 rows (16 < M with a weight of under 100 MB: 2048 -> 4096 at 32 rows
-// 8.8 us against 12.9, but 6144 -> 12288 56 against 43, each row group reading
-// its activations again).
-bool takes_rows(const LinGemm& p) {
+// Whether few rows run on their own kernel: always where the tiled ones cannot, up
+// to 16 rows, and up to 32 with a weight of under 20 million elements (which it
+// reads once, but every 16 columns' workgroup all activations), or of under 50
+// million where the workspace does not let the tiled ones split K.  At 17 / 32
+// rows, this kernel against the tiled ones (us), with the workspace: 4096 -> 2048
+// 8.4 / 9.7 : 12.5 / 12.6, 4096 -> 4096 11.1 / 13.7 : 14.2 / 14.3, gated 4096 -> 2048 11.1 / 12.3 :
+// 15.6 / 15.6, 2048 -> 8192 14.3 / 16.3 : 12.9 / 13.0; 4096 -> 6144 20.7 / 25.9 : 14.9 / 15.0, gated
+// 4096 -> 4096 17.0 / 19.2 : 17.8 / 17.8, 6144 -> 8192 30.5 / 37.6 : 24.6 / 25.8.  Without: 4096 ->
+// 6144 20.7 / 25.8 : 30.7 / 30.8, gated 4096 -> 4096 16.6 / 18.5 : 35.0 / 35.2, 6144 -> 6144
+// 28.4 / 36.2 : 29.9 / 29.9; 6144 -> 8192 28.5 / 36.3 : 29.8 / 29.9, 8192 -> 8192 36.3 / 46.6 : 38.6 / 38.6.
+bool takes_rows(const LinGemm& p, int64_t ws_bytes) {
   if (!rows_ok(p)) return false;
   if (p.M <= 16 || !tiles_ok(p)) return true;
-  return p.M <= 32 && (p.mode == kModeDual ? 2 : 1) * p.N * p.K < 50'000'000;
+  if (p.M > 32) return false;
+  const int64_t most = ws_bytes >= ws_of(p, pick(p)) ? 20'000'000 : 50'000'000;
+  return (p.mode == kModeDual ? 2 : 1) * p.N * p.K < most;
 }
 
 // Splits K only where the workspace holds the tickets and partials.
@@ -154,21 +162,21 @@ void take_ws(LinGemm *p, void *ws) {
 
 hipError_t launch_rows(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   RowsShape h = rows_shape(p);
-  if (!ws || ws_bytes < ws_of(h)) h.splits = 1;
+  if (ws_bytes < ws_of(h)) h.splits = 1;
   if (h.splits > 1) take_ws(&p, ws);
   return lin_rows_launch(p, h, s);
 }
 
 hipError_t launch_staged(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   StagedShape h = staged_shape(p, true);
-  if (!ws || ws_bytes < ws_of(h)) h = staged_shape(p, false);
+  if (ws_bytes < ws_of(h)) h = staged_shape(p, false);
   if (h.splits > 1) take_ws(&p, ws);
   return lin_staged_launch(p, h, s);
 }
 
 hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   TilePick t = pick(p);
-  if (!ws || ws_bytes < ws_of(p, t)) t.splits = 1;
+  if (ws_bytes < ws_of(p, t)) t.splits = 1;
   if (t.splits > 1) take_ws(&p, ws);
   if (p.a_t) return lin_tiles_pair(p, t, s);
   switch (p.mode) {
@@ -193,13 +201,14 @@ bool lin_grid_ok(int64_t M, int64_t N) {
 // counted, and the few-row kernel's (17 to 64 rows) stays below the others'.
 int64_t lin_gemm_ws(const LinGemm& p) {
   if (p.M <= 0 || p.N <= 0) return 0;
-  if (takes_rows(p)) return ws_of(rows_shape(p));
+  if (takes_rows(p, INT64_MAX)) return ws_of(rows_shape(p));
   return std::max(tiles_ok(p) ? ws_of(p, pick(p)) : 0, ws_of(staged_shape(p, true)));
 }
 
 hipError_t lin_gemm_launch(const LinGemm& p, hipStream_t s, void *ws, int64_t ws_bytes) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
-  if (takes_rows(p)) return launch_rows(p, ws, ws_bytes, s);
+  if (!ws) ws_bytes = 0;
+  if (takes_rows(p, ws_bytes)) return launch_rows(p, ws, ws_bytes, s);
   if (tiles_ok(p)) return launch_tiles(p, ws, ws_bytes, s);
   return launch_staged(p, ws, ws_bytes, s);
 }

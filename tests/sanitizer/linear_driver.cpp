@@ -9,7 +9,7 @@
 //   driver nomem      every call again with each of its host allocations failing
 //                     in turn: a status comes back, no exception
 //   driver choose     reads lines "op dtype layout M K N odd" (op: linear,
-//                     linear_bwd, gated, gated_bwd; odd: 1 takes operands off
+//                     linear_bwd, gated, gated_bwd, with a - behind it without a workspace; odd: 1 takes operands off
 //                     every vector alignment) and prints the kernels each call
 //                     launches, joined by "; "
 #include <algorithm>
@@ -238,6 +238,8 @@ int choose() {
     k.dtype = dtype == "f32" ? TP_F32 : TP_BF16;
     k.layout = layout == "linear" ? TP_WEIGHTS_LINEAR : TP_WEIGHTS_MATH;
     k.pad = k.skew = odd;
+    k.ws = op.back() == '-' ? 0 : 2;
+    if (!k.ws) op.pop_back();
     expect(run(op, k) == TP_OK, "a call to choose for");
     const auto names = lin_stub_take();
     for (size_t i = 0; i < names.size(); ++i) std::printf("%s%s", i ? "; " : "", names[i].c_str());

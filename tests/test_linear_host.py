@@ -100,6 +100,17 @@ def test_the_gpu_tests_reach_every_kernel(driver):
     assert all(k in deep for k in every_kernel() if "128" in k or "256" in k or "192" in k)
 
 
+def test_few_rows_against_wide_weights(driver):
+    """The few-row kernel where it was measured to be the faster one: with a workspace, and (op ending in -) without."""
+    rows = [("linear", 4096, 2048), ("linear", 4096, 4096), ("gated", 4096, 2048), ("linear-", 4096, 6144), ("gated-", 4096, 4096),
+            ("linear-", 6144, 6144)]
+    tiles = [("linear", 4096, 6144), ("linear", 8192, 4096), ("linear", 6144, 8192), ("gated", 6144, 4096),
+             ("linear-", 8192, 8192), ("gated-", 4096, 8192)]
+    text = "\n".join(f"{op} bf16 linear {M} {K} {N} 0" for M in (17, 32) for op, K, N in rows + tiles)
+    out, _ = driver("choose", text=text)
+    assert ["rows" in line for line in out.strip().split("\n")] == ([True] * len(rows) + [False] * len(tiles)) * 2
+
+
 @pytest.mark.parametrize("rows", [17, 24, 32, 33, 47, 64])
 def test_a_workspace_suffices_whatever_the_alignment(rows):
     """A workspace is asked for before addresses are known, for the kernels that need aligned rows: one K fewer has the same
