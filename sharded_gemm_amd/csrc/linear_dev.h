@@ -39,6 +39,25 @@ __device__ __forceinline__ float load1(const T *p) {
   else return from_bf16(*reinterpret_cast<const uint16_t *>(p));
 }
 
+// ---- 16 bytes ------------------------------------------------------------------
+// 16 bytes of T at p, of which `left` elements exist (the rest read as zero).
+template <typename T>
+__device__ __forceinline__ u32x4 load16(const T *p, int64_t left) {
+  constexpr int V = 16 / sizeof(T);
+  if (left >= V) return *reinterpret_cast<const u32x4_any *>(p);
+  u32x4 v{0, 0, 0, 0};
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) v[e] = p[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+  }
+  return v;
+}
+
 // ---- activations -------------------------------------------------------------
 // All in fp32 on the hardware's exp2 and reciprocal (about 1 ulp each).
 //  gelu_erf : x Phi(x); with a = |x|, q = Phi(-a) = e^{-x^2/2} t P(t), t = 1 / (1 + 0.21 a), Phi = 1 - q

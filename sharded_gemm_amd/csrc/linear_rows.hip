@@ -47,21 +47,6 @@ __device__ __forceinline__ f32x4 mma(u32x4 w, u32x4 x, f32x4 acc) {
   }
 }
 
-// 16 bytes at p, of which `left` elements exist.
-template <typename T>
-__device__ __forceinline__ u32x4 load16(const T *p, int64_t left) {
-  constexpr int V = 16 / sizeof(T);
-  if (left >= V) return *reinterpret_cast<const u32x4_any *>(p);
-  u32x4 v{0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    if (e < left) {
-      if constexpr (sizeof(T) == 4) v[e] = p[e];
-      else v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
-    }
-  return v;
-}
-
 // G elements of T at p as dwords, of which `left` exist.
 template <typename T, int G>
 struct Cols {

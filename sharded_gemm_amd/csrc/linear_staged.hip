@@ -37,24 +37,6 @@ __device__ __forceinline__ uint32_t lds_at(int r, int c) {
   return static_cast<uint32_t>(r * kRow + ((c ^ ((r ^ (r >> 3)) & 7)) << 4));
 }
 
-// 16 bytes of T at p, of which `left` elements exist (the rest read as zero).
-template <typename T>
-__device__ __forceinline__ u32x4 load16(const T *p, int64_t left) {
-  constexpr int V = 16 / sizeof(T);
-  if (left >= V) return *reinterpret_cast<const u32x4_any *>(p);
-  u32x4 v{0, 0, 0, 0};
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) v[e] = p[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
-  }
-  return v;
-}
-
 // One operand's tile: ROWS output rows (or columns) by one stage of K.
 // KC: k is contiguous in memory.  T: uint32_t (fp32) or uint16_t (bf16).
 //

@@ -39,7 +39,6 @@ struct WTile {
 };
 
 // What a workgroup computes: its tile, and its part of K.
-template <int BM, int BNO>
 struct Place {
   int m0, n0;
   bool second;          // kModePair's second product
@@ -47,11 +46,11 @@ struct Place {
 };
 
 template <int BM, int BNO, int BK, int MODE>
-__device__ __forceinline__ Place<BM, BNO> place_of(const LinGemm& p) {
+__device__ __forceinline__ Place place_of(const LinGemm& p) {
   const int tiles_m = static_cast<int>((p.M + BM - 1) / BM), tiles_n = static_cast<int>((p.N + BNO - 1) / BNO);
   const int ntiles = tiles_m * tiles_n;
   int bid = blockIdx.x;
-  Place<BM, BNO> q;
+  Place q;
   q.second = MODE == kModePair && bid >= ntiles;
   if (q.second) bid -= ntiles;
   int tm, tn;
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(Lin
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
-  const auto pl = place_of<BM, BNO, BK, MODE>(p);
+  const Place pl = place_of<BM, BNO, BK, MODE>(p);
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((TP_LDS char *)smem));
   const uint16_t *A = static_cast<const uint16_t *>(pl.second ? p.a2 : p.a);
   const uint16_t *W = static_cast<const uint16_t *>(pl.second ? p.w2 : p.w);
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinGemm p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
   const bool grpA = wave < 4;
-  const auto pl = place_of<BM, BNO, BK, MODE>(p);
+  const Place pl = place_of<BM, BNO, BK, MODE>(p);
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((TP_LDS char *)smem));
   const uint32_t step = static_cast<uint32_t>((grpA ? TA::step(p.lda) : TW::step(p.ldw)) * 2);
   const void *a_base = pl.second ? p.a2 : p.a;
@@ -204,16 +203,10 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinGemm p) {
 
 // ---- launchers -----------------------------------------------------------------
 
-template <int MODE>
-int64_t tiles_of(const LinGemm& p, int bm, int bn) {
-  static_assert(MODE >= kModeOne && MODE <= kModePair, "mode");
-  return lin_tiles_count(p, bm, bn);
-}
-
 template <int BM, int BN, int BK, int S, int MODE, bool AT, bool WT, int WAVES_M, int WAVES_N>
 hipError_t launch_ring(const LinGemm& p, int splits, hipStream_t s) {
   hipLaunchKernelGGL((lin_ring_kernel<BM, BN, BK, S, MODE, AT, WT, WAVES_M, WAVES_N>),
-                     dim3(static_cast<unsigned>(tiles_of<MODE>(p, BM, BN)), static_cast<unsigned>(splits)),
+                     dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN)), static_cast<unsigned>(splits)),
                      dim3(64 * WAVES_M * WAVES_N), 0, s, p);
   return hipGetLastError();
 }
@@ -221,7 +214,7 @@ hipError_t launch_ring(const LinGemm& p, int splits, hipStream_t s) {
 template <int BM, int BN, int MODE, bool AT, bool WT, int WGM = 2>
 hipError_t launch_lin_pps(const LinGemm& p, hipStream_t s) {
   hipLaunchKernelGGL((lin_pps_kernel<BM, BN, MODE, AT, WT, WGM>),
-                     dim3(static_cast<unsigned>(tiles_of<MODE>(p, BM, BN))), dim3(512), 0, s, p);
+                     dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN))), dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
