@@ -558,7 +558,8 @@ typedef struct {
   int64_t pre_ld;
   void *ws;              /* optional, tp_linear_ws bytes: lets few rows (a decode step)
                             and small batches split K over the whole chip.  16-byte
-                            aligned, zero before its first use; any calls may follow one
+                            aligned, zero before its first use (ordered before the
+                            call, on whichever stream); any calls may follow one
                             another on it (of tp_gated_linear too), but calls that may
                             overlap need one each.  NULL or smaller: K is not split */
   int64_t ws_bytes;
@@ -571,7 +572,10 @@ int tp_linear_ws(const tp_linear_args *args, int64_t *bytes);
 /*
  * out = act(X W + bias) + residual, in one launch; the value is rounded once, when
  * it is stored.  Rows are independent: a row's result does not depend on the
- * other rows' values.  Deterministic.  Capturable into a HIP graph.
+ * other rows' values.  Reproducible: the same bits for the same sizes, types,
+ * layout, strides and alignment, and the same answer to whether the workspace
+ * suffices (it decides how K is split, and the sums' order with it; sums over
+ * splits are added in order).  Capturable into a HIP graph.
  * Errors: TP_ERR_ARG (NULL or overlapping buffers, unknown dtype / act / layout,
  *         bad sizes or strides), TP_ERR_UNSUPPORTED (sizes beyond the kernels'
  *         32-bit indexes or the grid), TP_ERR_HIP.
@@ -613,7 +617,8 @@ int tp_linear_backward_ws(const tp_linear_bwd_args *args, int64_t *bytes);
 /*
  * dPre = dOut * act'(pre) (rounded to dtype for the two products);
  * dX = dPre W^T;  dW (+)= X^T dPre;  dbias (+)= column sums of the unrounded dPre.
- * Deterministic: no atomics.  Capturable into a HIP graph.
+ * Reproducible, as tp_linear: every sum has its order, atomics only count a
+ * tile's finished parts.  Capturable into a HIP graph.
  * Errors: as tp_linear, plus TP_ERR_ARG for a missing or too small workspace.
  */
 int tp_linear_backward(const tp_linear_bwd_args *args, tp_stream_t stream);

@@ -103,7 +103,7 @@ int64_t small_tiles(const LinGemm& p) { return lin_tiles_count(p, 64, p.mode == 
 // relative throughput (measured in gemm.hip).  Problems too small to give every
 // CU a 128 x 128 tile take small ones, several of which share a CU: with three
 // stages in flight (2048 -> 4096 at 256 rows 12.7 us against 17.4 with two; gated
-// 12288 -> 6144 160 against 173, and 199 with four), or two where a workgroup has
+// 12288 -> 6144 at 256 rows 160 against 173, and 199 with four), or two where a workgroup has
 // at most 16 (1024^3 9.0 us against 10.3).  They split K until there is one for
 // every CU, and on to two where each still has 24 stages to pay for the join
 // (gated 4096 -> 2048 at 64 rows: 40 -> 17 us; at 8 stages each the second split

@@ -4,8 +4,9 @@
 //   kModeOne  c = epi(X W)        kModeDual  c = act(X W) * (X W2)
 //
 // A workgroup owns 16 G output columns and all rows; its waves split K between
-// them and join through LDS, so one launch does everything, with no partial
-// sums in memory.  The weight never passes through LDS: each lane's loads are
+// them and join through LDS.  Given a workspace, several workgroups may split a
+// tile's K too: each leaves its sums there, and the last to finish adds them up,
+// still in the one launch.  The weight never passes through LDS: each lane's loads are
 // already an MFMA operand (v_mfma_f32_16x16x32_bf16 takes the weight first, so
 // its 16 rows are output columns and its columns are tokens).
 //  * k-contiguous weight ([N][K]): lane l loads 16 bytes (8 k) of column
@@ -22,8 +23,8 @@
 // Bound by HBM where the weight is large: on an MI355X (copy 5.2 TB/s) one token
 // takes 30 us from 6144 to 12288 (151 MB, 5.0 TB/s) and 55 us through the gated
 // block from 12288 to 6144 (302 MB, 5.5 TB/s); by latency where it is small: 768 x
-// 768 4 us, gated 4096 -> 2048 (33.5 MB) 10 us, of which launch, first load and
-// join take about 6.  16 columns a tile for a k-contiguous weight, 128 bytes of
+// 768 4 us, gated 4096 -> 2048 (33.5 MB) 10 us (12 at 12 tokens), of which launch,
+// first load and join take about 6.  fp32: 6144 -> 12288 (302 MB) 56 us (5.4 TB/s).  16 columns a tile for a k-contiguous weight, 128 bytes of
 // columns for an n-contiguous one: with 64 bytes two workgroups on different XCDs
 // fetch every line twice (gated 12288 -> 6144 93 us against 59).
 #include "linear_dev.h"
