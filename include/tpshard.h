@@ -36,7 +36,7 @@ enum {
   TP_ERR_INDIVISIBLE = -3, /* a dim is not a multiple of its shard / chunk count */
   TP_ERR_UNSUPPORTED = -4, /* well-formed but outside what this library does */
   TP_ERR_HIP = -5          /* a HIP runtime call failed (message has hipGetErrorString),
-                              or host memory ran out (tp_grad_*) */
+                              or host memory ran out (tp_grad_*, tp_adamw_*) */
 };
 
 /* Message describing the last failing call on the calling thread ("" if none).
@@ -725,6 +725,167 @@ int tp_grad_sumsq(const tp_grad_tensor *tensors, int64_t num, double *parts, tp_
 int tp_grad_clip(const tp_grad_tensor *tensors, int64_t num, const double *parts, int64_t ranks, double max_norm,
                  double eps, float *norm_out, tp_stream_t stream);
 
+/* ---- cross entropy of a vocabulary projection ----------------------------- */
+/* Logits z = X W of a vocabulary, or of one rank's piece of it (W's columns are
+ * the ids vocab_begin .. vocab_begin + V - 1), which are never kept:
+ *   lse[m] = ln sum over the whole vocabulary of e^z,  loss[m] = lse[m] - z[m, target]
+ * A target equal to ignore_index has loss 0 and no gradient (its lse is the row's
+ * all the same); one that no piece holds has loss +inf.  Targets, losses and the
+ * gradients at them are per token, so that a mean, a sum or weights are the
+ * caller's: dloss = 1 / count for the mean over the tokens that count.
+ * Statistics of a piece, [3][M] fp32: the largest logit; the sum of e^(z - largest)
+ * (of e^z where the largest is not finite); the target's logit, -inf where the piece
+ * does not hold it.  Ranks gather theirs into [pieces][3][M] for tp_ce_join. */
+typedef struct {
+  int32_t dtype;         /* TP_BF16 or TP_F32: X, W (fp32 accumulation and statistics) */
+  int32_t weight_layout; /* TP_WEIGHTS_MATH: W is [K, V]; TP_WEIGHTS_LINEAR: [V, K] */
+  int64_t M, V, K;       /* M >= 0 tokens (0 = nothing to do), V, K >= 1 */
+  const void *X;         /* [M, K] */
+  int64_t X_ld;          /* row strides in elements, 0 = contiguous, as in tp_linear_args */
+  const void *W;
+  int64_t W_ld;
+  const int64_t *targets;/* [M] ids of the whole vocabulary (device memory) */
+  int64_t vocab_begin;   /* >= 0 */
+  int64_t ignore_index;
+  float *stats;          /* optional [3][M] */
+  float *loss;           /* optional [M]: of this piece alone, so of the loss where it is */
+  float *lse;            /* the whole vocabulary; optional [M] */
+  void *ws;              /* tp_linear_ce_ws bytes, 16-byte aligned.  Its first 4096 bytes are
+                            zero before its first use, and again after every call; calls of any
+                            sizes may follow one another on it, calls that may overlap need
+                            one each */
+  int64_t ws_bytes;
+} tp_linear_ce_args;
+
+/* Bytes of workspace the call needs.  Reads dtype, weight_layout and the sizes.
+ * Host only. */
+int tp_linear_ce_ws(const tp_linear_ce_args *args, int64_t *bytes);
+
+/*
+ * The statistics of a piece, and (as if it were the whole vocabulary) loss and lse.
+ * At least one of stats, loss and lse is asked for.  Rows are independent.
+ * Reproducible: every sum has its order.  Capturable into a HIP graph.
+ * Errors: TP_ERR_ARG (NULL or overlapping buffers, unknown dtype or layout, bad sizes
+ *         or strides, a workspace too small), TP_ERR_UNSUPPORTED (sizes beyond the
+ *         kernels' indexes or grid), TP_ERR_HIP.
+ */
+int tp_linear_ce(const tp_linear_ce_args *args, tp_stream_t stream);
+
+/*
+ * loss and lse (each optional [M]) from the statistics of 1 to 64 pieces,
+ * [pieces][3][M], in any order of the pieces.
+ * Errors: TP_ERR_ARG, TP_ERR_UNSUPPORTED (M of 2^31 and more), TP_ERR_HIP.
+ */
+int tp_ce_join(const float *stats, int64_t pieces, int64_t M, const int64_t *targets, int64_t ignore_index, float *loss,
+               float *lse, tp_stream_t stream);
+
+typedef struct {
+  int32_t dtype;         /* as the forward: X, W */
+  int32_t weight_layout;
+  int32_t dx_dtype;      /* of dX: dtype, or TP_F32 (a rank's partial, for tp_partial_reduce) */
+  int32_t dw_dtype;      /* of dW: dtype, or TP_F32 */
+  int32_t accumulate;    /* 1: dW is added to (needs TP_F32 dW, if dW is asked for) */
+  int64_t M, V, K;       /* M >= 0: with M = 0 dW is zero (or unchanged: accumulate) */
+  const void *X;
+  int64_t X_ld;
+  const void *W;
+  int64_t W_ld;
+  const int64_t *targets;
+  int64_t vocab_begin;
+  int64_t ignore_index;
+  const float *lse;      /* [M]: the forward's, over the whole vocabulary */
+  const float *dloss;    /* gradient at loss; NULL = 1 */
+  int64_t dloss_stride;  /* 1: [M]; 0: one value for all tokens */
+  const float *dlse;     /* optional gradient at lse, besides loss's (e.g. of a penalty on lse^2) */
+  int64_t dlse_stride;   /* as dloss_stride */
+  void *dX;              /* optional [M, K] */
+  int64_t dX_ld;
+  void *dW;              /* optional, in W's layout */
+  int64_t dW_ld;
+  int64_t piece;         /* 0, or the most columns of the vocabulary to work on at a time (taken
+                            in multiples of 64): the workspace grows with it, and with few the
+                            time */
+  void *ws;              /* tp_linear_ce_backward_ws bytes, 16-byte aligned; need not be cleared */
+  int64_t ws_bytes;
+} tp_linear_ce_bwd_args;
+
+/* Bytes of workspace the call needs.  Reads dtype, weight_layout, dx_dtype, the sizes,
+ * piece, and which of dX and dW are asked for (non-NULL).  Host only. */
+int tp_linear_ce_backward_ws(const tp_linear_ce_bwd_args *args, int64_t *bytes);
+
+/*
+ * dz[m, n] = (dloss + dlse) e^(z - lse) - (n is the target) dloss, 0 for ignored
+ * targets, from the product computed again, a piece of the vocabulary at a time,
+ * rounded to dtype for the two products; dX = dz W^T, dW (+)= X^T dz.
+ * Rows of X with ignored targets are not part of dW, whatever they hold.
+ * Reproducible and capturable, as the forward.
+ * Errors: as tp_linear_ce.
+ */
+int tp_linear_ce_backward(const tp_linear_ce_bwd_args *args, tp_stream_t stream);
+
+/* ---- AdamW ------------------------------------------------------------------ */
+/* Elements that share a scale in 8-bit states, counted from the tensor's start. */
+enum { TP_ADAMW_BLOCK = 256 };
+/* States: TP_ADAMW_F32: m and v in fp32.  TP_ADAMW_8BIT: m as int8 codes and v as uint8
+ * codes, each with an fp32 scale for every TP_ADAMW_BLOCK elements (the last may be
+ * short):
+ *   m = scale sign(q) (q / 127)^2,  v = (scale (q / 255)^2)^2
+ * to the nearest code, scale the block's largest |m| (largest sqrt(v)); a v that is
+ * not zero has a code of at least 1.  Zeros everywhere are the state before the first step. */
+enum { TP_ADAMW_F32 = 0, TP_ADAMW_8BIT = 1 };
+
+typedef struct {
+  void *param;           /* updated; contiguous, its element's alignment, as every buffer here */
+  const void *grad;
+  void *m, *v;           /* updated */
+  float *m_scale, *v_scale; /* TP_ADAMW_8BIT: updated, ceil(n / TP_ADAMW_BLOCK) values; else ignored */
+  void *copy;            /* optional: the new param in bf16 */
+  int64_t n;             /* elements, >= 0; every pointer may be NULL with 0 */
+  int32_t param_dtype;   /* TP_F32 or TP_BF16 (rounded to nearest after each step) */
+  int32_t grad_dtype;    /* TP_F32 or TP_BF16 */
+  double weight_decay;   /* >= 0, of this tensor */
+} tp_adamw_tensor;
+
+typedef struct {
+  int32_t states;        /* TP_ADAMW_F32 or TP_ADAMW_8BIT */
+  double lr;             /* >= 0 */
+  double beta1, beta2;   /* in [0, 1) */
+  double eps;            /* >= 0 */
+  int64_t step;          /* t >= 1, counting this one */
+  const int64_t *step_dev; /* optional device value in step's place (below 1: 1), and */
+  const float *lr_dev;     /* in lr's: a captured step then follows them */
+  const double *parts;   /* optional: clip by the norm that tp_grad_sumsq left here */
+  int64_t ranks;         /* blocks of TP_GRAD_PARTS in parts, 1..64 */
+  double max_norm;       /* as tp_grad_clip's, with its eps */
+  double clip_eps;
+  float *norm_out;       /* optional: the norm (with parts only) */
+  int32_t skip_nonfinite;/* 1: where the norm is infinite or NaN, nothing but norm_out is written
+                            (with parts only) */
+} tp_adamw_args;
+
+/*
+ * One step of every tensor, in fp32 and in one pass:
+ *   g = grad * min(1, max_norm / (norm + clip_eps))   (not rounded to grad's type)
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   param -= lr (weight_decay param + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ * With 8-bit states the update uses m and v before they are rounded to codes.
+ * Buffers must not overlap, but gradients may be one another's.  Capturable.
+ * Errors: TP_ERR_ARG, TP_ERR_HIP.
+ */
+int tp_adamw_step(const tp_adamw_tensor *tensors, int64_t num, const tp_adamw_args *args, tp_stream_t stream);
+
+typedef struct {
+  const void *m, *v;     /* codes */
+  const float *m_scale, *v_scale;
+  void *m_out, *v_out;   /* [n] in out_dtype */
+  int64_t n;
+  int32_t out_dtype;     /* TP_F32 or TP_BF16 */
+} tp_adamw_state;
+
+/* The values that 8-bit states stand for (to save or inspect them).
+ * Errors: TP_ERR_ARG, TP_ERR_HIP. */
+int tp_adamw_unpack(const tp_adamw_state *states, int64_t num, tp_stream_t stream);
+
 /* ---- per-kernel timing (measurement support) ---------------------------- */
 /* Kernel families timed by the optional instrumentation below: the forward's
  * GEMMs, the backward's input-gradient GEMMs (dH and dX) and its
@@ -738,7 +899,9 @@ int tp_grad_clip(const tp_grad_tensor *tensors, int64_t num, const double *parts
  * The products of tp_linear and tp_gated_linear are filed under GEMM1, those of
  * their backward passes under GEMM_DGRAD and GEMM_WGRAD, and the passes that
  * only stream (gradients at the activation, bias gradients, the gradient norm
- * and clipping) under REDUCE. */
+ * and clipping) under REDUCE.  Likewise the cross entropy's: its logits under GEMM1
+ * (in both directions), its gradients' products under GEMM_DGRAD and GEMM_WGRAD, its
+ * other passes and the AdamW step under REDUCE. */
 enum { TP_KERNEL_MATERIALIZE = 0, TP_KERNEL_GEMM1 = 1, TP_KERNEL_GEMM2 = 2, TP_KERNEL_REDUCE = 3,
        TP_KERNEL_GEMM_DGRAD = 4, TP_KERNEL_GEMM_WGRAD = 5, TP_KERNEL_GATHER = 6,
        TP_KERNEL_GEMM2_REDUCE = 7, TP_KERNEL_GEMM_DGRAD_REDUCE = 8, TP_KERNEL_REDUCE_TAIL = 9,

@@ -43,7 +43,9 @@ TP_REDUCE_OP_MIN = 2
 EXPORTS = ("tp_last_error", "tp_version", "tp_layout_plan", "tp_check_broadcast_binary", "tp_infer_matmul_dims_mapping", "tp_shard_materialize", "tp_shard_materialize_batch", "tp_shard_gather",
            "tp_partial_reduce", "tp_partial_reduce_ex", "tp_colrow_mlp", "tp_colrow_mlp_noalloc", "tp_colrow_mlp_stack", "tp_colrow_mlp_backward",
            "tp_linear", "tp_linear_ws", "tp_linear_backward_ws", "tp_linear_backward", "tp_gated_linear", "tp_gated_linear_ws",
-           "tp_gated_linear_backward_ws", "tp_gated_linear_backward", "tp_grad_sumsq", "tp_grad_clip", "tp_timing_enable", "tp_timing_read")
+           "tp_gated_linear_backward_ws", "tp_gated_linear_backward", "tp_grad_sumsq", "tp_grad_clip", "tp_linear_ce",
+           "tp_linear_ce_ws", "tp_ce_join", "tp_linear_ce_backward", "tp_linear_ce_backward_ws", "tp_adamw_step", "tp_adamw_unpack",
+           "tp_timing_enable", "tp_timing_read")
 
 TP_KERNEL_NAMES = ("materialize", "gemm1", "gemm2", "reduce", "gemm_dgrad", "gemm_wgrad", "gather", "gemm2_reduce",
                    "gemm_dgrad_reduce", "reduce_tail")
@@ -52,6 +54,10 @@ TP_REDUCE_FUSION_AUTO = 0
 TP_REDUCE_FUSION_OFF = 1
 
 TP_GRAD_PARTS = 1024
+
+TP_ADAMW_BLOCK = 256
+TP_ADAMW_F32 = 0
+TP_ADAMW_8BIT = 1
 
 TP_WEIGHTS_MATH = 0
 TP_WEIGHTS_LINEAR = 1
@@ -167,6 +173,45 @@ class tp_grad_tensor(C.Structure):
     _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32)]
 
 
+class tp_linear_ce_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("weight_layout", C.c_int32),
+                ("M", C.c_int64), ("V", C.c_int64), ("K", C.c_int64),
+                ("X", C.c_void_p), ("X_ld", C.c_int64), ("W", C.c_void_p), ("W_ld", C.c_int64),
+                ("targets", C.c_void_p), ("vocab_begin", C.c_int64), ("ignore_index", C.c_int64),
+                ("stats", C.c_void_p), ("loss", C.c_void_p), ("lse", C.c_void_p),
+                ("ws", C.c_void_p), ("ws_bytes", C.c_int64)]
+
+
+class tp_linear_ce_bwd_args(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("weight_layout", C.c_int32), ("dx_dtype", C.c_int32), ("dw_dtype", C.c_int32),
+                ("accumulate", C.c_int32),
+                ("M", C.c_int64), ("V", C.c_int64), ("K", C.c_int64),
+                ("X", C.c_void_p), ("X_ld", C.c_int64), ("W", C.c_void_p), ("W_ld", C.c_int64),
+                ("targets", C.c_void_p), ("vocab_begin", C.c_int64), ("ignore_index", C.c_int64),
+                ("lse", C.c_void_p), ("dloss", C.c_void_p), ("dloss_stride", C.c_int64),
+                ("dlse", C.c_void_p), ("dlse_stride", C.c_int64),
+                ("dX", C.c_void_p), ("dX_ld", C.c_int64), ("dW", C.c_void_p), ("dW_ld", C.c_int64),
+                ("piece", C.c_int64), ("ws", C.c_void_p), ("ws_bytes", C.c_int64)]
+
+
+class tp_adamw_tensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p), ("copy", C.c_void_p), ("n", C.c_int64),
+                ("param_dtype", C.c_int32), ("grad_dtype", C.c_int32), ("weight_decay", C.c_double)]
+
+
+class tp_adamw_args(C.Structure):
+    _fields_ = [("states", C.c_int32), ("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("step", C.c_int64), ("step_dev", C.c_void_p), ("lr_dev", C.c_void_p),
+                ("parts", C.c_void_p), ("ranks", C.c_int64), ("max_norm", C.c_double), ("clip_eps", C.c_double),
+                ("norm_out", C.c_void_p), ("skip_nonfinite", C.c_int32)]
+
+
+class tp_adamw_state(C.Structure):
+    _fields_ = [("m", C.c_void_p), ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("m_out", C.c_void_p), ("v_out", C.c_void_p), ("n", C.c_int64), ("out_dtype", C.c_int32)]
+
+
 class tp_kernel_stat(C.Structure):
     _fields_ = [("launches", C.c_int64), ("total_ms", C.c_double), ("min_ms", C.c_double),
                 ("max_ms", C.c_double), ("work", C.c_double)]
@@ -221,12 +266,15 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.tp_colrow_mlp_backward.argtypes = [C.POINTER(tp_mlp_bwd_args), C.c_void_p, C.c_void_p]
     lib.tp_colrow_mlp_backward.restype = C.c_int
     for name, struct in (("tp_linear", tp_linear_args), ("tp_linear_backward", tp_linear_bwd_args),
-                         ("tp_gated_linear", tp_gated_args), ("tp_gated_linear_backward", tp_gated_bwd_args)):
+                         ("tp_gated_linear", tp_gated_args), ("tp_gated_linear_backward", tp_gated_bwd_args),
+                         ("tp_linear_ce", tp_linear_ce_args), ("tp_linear_ce_backward", tp_linear_ce_bwd_args)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = C.c_int, [C.POINTER(struct), C.c_void_p]
     for name, struct in (("tp_linear_ws", tp_linear_args), ("tp_gated_linear_ws", tp_gated_args),
                          ("tp_linear_backward_ws", tp_linear_bwd_args),
-                         ("tp_gated_linear_backward_ws", tp_gated_bwd_args)):
+                         ("tp_gated_linear_backward_ws", tp_gated_bwd_args),
+                         ("tp_linear_ce_ws", tp_linear_ce_args),
+                         ("tp_linear_ce_backward_ws", tp_linear_ce_bwd_args)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = C.c_int, [C.POINTER(struct), i64p]
     lib.tp_grad_sumsq.restype = C.c_int
@@ -234,6 +282,12 @@ def load(path: str = LIB_PATH) -> C.CDLL:
     lib.tp_grad_clip.restype = C.c_int
     lib.tp_grad_clip.argtypes = [C.POINTER(tp_grad_tensor), C.c_int64, C.c_void_p, C.c_int64, C.c_double, C.c_double,
                                  C.c_void_p, C.c_void_p]
+    lib.tp_ce_join.restype = C.c_int
+    lib.tp_ce_join.argtypes = [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.tp_adamw_step.restype = C.c_int
+    lib.tp_adamw_step.argtypes = [C.POINTER(tp_adamw_tensor), C.c_int64, C.POINTER(tp_adamw_args), C.c_void_p]
+    lib.tp_adamw_unpack.restype = C.c_int
+    lib.tp_adamw_unpack.argtypes = [C.POINTER(tp_adamw_state), C.c_int64, C.c_void_p]
     lib.tp_timing_enable.restype = C.c_int
     lib.tp_timing_enable.argtypes = [C.c_int32]
     lib.tp_timing_read.restype = C.c_int
@@ -1055,6 +1109,245 @@ def tp_grad_clip(grads, outs, parts, *, max_norm, eps=1e-6, norm_out=None, ranks
     if prepare:
         return Prepared(lib.tp_grad_clip, args, [], [_stream_ptr(stream)], _tensors(grads, written, parts, norm_out))
     _check(lib.tp_grad_clip(*args, _stream_ptr(stream)))
+
+
+def _vec(t, name, shape, dtype, optional=True):
+    """The pointer of a contiguous tensor of this shape and type."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} must be a tensor")
+    if not hasattr(t, "data_ptr") or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)}, not {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _per_token(t, name, M):
+    """(pointer, stride) of a gradient that every token has of its own, or all share."""
+    import torch
+    if t is None:
+        return None, 0
+    if not hasattr(t, "data_ptr") or t.dtype != torch.float32:
+        raise TypeError(f"{name} must be an fp32 tensor")
+    if t.numel() == 1 or (t.dim() == 1 and t.shape[0] == M and t.stride(0) == 0):
+        return t.data_ptr(), 0
+    return _vec(t, name, (M,), torch.float32), 1
+
+
+def tp_linear_ce_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH):
+    """A workspace (uint8 tensor, its tickets zeroed on the current stream) for ``tp_linear_ce``
+    of these shapes.  It serves any number of calls one after another, also of smaller shapes."""
+    import torch
+    args = tp_linear_ce_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
+                             V=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]))
+    ws = torch.empty(_ws_bytes(load().tp_linear_ce_ws, args), dtype=torch.uint8, device=X.device)
+    ws[:4096].zero_()
+    return ws
+
+
+def tp_linear_ce(X, W, targets, *, loss=None, lse=None, stats=None, vocab_begin=0, ignore_index=-100,
+                 weight_layout=TP_WEIGHTS_MATH, ws=None, stream=None, prepare=False):
+    """Softmax cross entropy of the logits X W, which are not kept: lse[m] = ln sum e^z,
+    loss[m] = lse[m] - z[m, target] (0 where the target is ``ignore_index``).
+
+    X [M, K] and W [K, V] (or [V, K], TP_WEIGHTS_LINEAR) in bf16 or fp32, targets [M] int64;
+    loss and lse fp32 [M].  W may be one rank's piece of the vocabulary, the ids from
+    ``vocab_begin`` on: then ``stats`` (fp32 [3, M]) takes what ``tp_ce_join`` needs of it, and
+    loss and lse, if asked for, are of the piece alone.  ``ws``: from ``tp_linear_ce_ws``."""
+    import torch
+    lib = load()
+    M, K = (int(v) for v in X.shape)
+    V = _weight_dims(W, weight_layout)[1]
+    args = tp_linear_ce_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=M, V=V, K=K,
+                             vocab_begin=int(vocab_begin), ignore_index=int(ignore_index))
+    args.X, args.X_ld = _mat(X, "X")
+    args.W, args.W_ld = _mat(W, "W", (V, K) if weight_layout == TP_WEIGHTS_LINEAR else (K, V), X.dtype)
+    args.targets = _vec(targets, "targets", (M,), torch.int64, optional=False)
+    args.stats = _vec(stats, "stats", (3, M), torch.float32)
+    args.loss = _vec(loss, "loss", (M,), torch.float32)
+    args.lse = _vec(lse, "lse", (M,), torch.float32)
+    args.ws, args.ws_bytes = _ws(ws)
+    return _call(lib.tp_linear_ce, args, stream, prepare, (X, W, targets, stats, loss, lse, ws))
+
+
+def tp_ce_join(stats, targets, *, loss=None, lse=None, ignore_index=-100, stream=None, prepare=False):
+    """loss and lse over the whole vocabulary from every piece's statistics, ``stats`` fp32
+    [pieces, 3, M] (gathered from the ranks, in any order)."""
+    import torch
+    lib = load()
+    if not hasattr(stats, "data_ptr") or stats.dim() != 3:
+        raise TypeError("stats must be a 3-D tensor")
+    pieces, M = int(stats.shape[0]), int(stats.shape[2])
+    args = (C.c_void_p(_vec(stats, "stats", (pieces, 3, M), torch.float32)), pieces, M,
+            C.c_void_p(_vec(targets, "targets", (M,), torch.int64, optional=False)), int(ignore_index),
+            C.c_void_p(_vec(loss, "loss", (M,), torch.float32)), C.c_void_p(_vec(lse, "lse", (M,), torch.float32)))
+    tensors = (stats, targets, loss, lse)
+    _on_gpu(*tensors)
+    if prepare:
+        return Prepared(lib.tp_ce_join, args, [], [_stream_ptr(stream)], _tensors(*tensors))
+    _check(lib.tp_ce_join(*args, _stream_ptr(stream)))
+
+
+def tp_linear_ce_backward_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH, dX=None, dW=True, piece=0):
+    """A workspace (uint8 tensor) for ``tp_linear_ce_backward`` of these shapes.  ``dX``: the
+    tensor that is passed there (its type decides whether the sum over pieces is kept here),
+    None without it; ``dW``: whether it is asked for."""
+    args = tp_linear_ce_bwd_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
+                                 V=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]), piece=int(piece),
+                                 dx_dtype=_either(dX, "dX", X.dtype), dX=None if dX is None else 16,
+                                 dW=16 if dW is not None and dW is not False else None)
+    return _new_ws(load().tp_linear_ce_backward_ws, args, X.device)
+
+
+def tp_linear_ce_backward(X, W, targets, lse, *, dloss=None, dlse=None, dX=None, dW=None, vocab_begin=0,
+                          ignore_index=-100, weight_layout=TP_WEIGHTS_MATH, accumulate=False, piece=0, ws=None,
+                          stream=None, prepare=False):
+    """The gradients of ``tp_linear_ce`` (after ``tp_ce_join``, where the vocabulary is in pieces):
+    dz = (dloss + dlse) e^(z - lse) - [target] dloss, dX = dz W^T, dW (+)= X^T dz (in W's
+    layout), the logits computed again a piece of the vocabulary at a time.
+
+    ``lse``: the forward's, over the whole vocabulary.  ``dloss`` and ``dlse``: fp32 [M], or one
+    value for all tokens (dloss None: 1, dlse None: 0).  dX and dW are in the inputs' dtype or
+    fp32; outputs left None are not computed; ``accumulate`` adds to an fp32 dW.  On a rank's
+    piece dX is that piece's partial sum.  ``piece``: the most columns at a time (0: chosen).
+    ``ws``: from ``tp_linear_ce_backward_ws`` with the same dX, dW and piece."""
+    import torch
+    lib = load()
+    M, K = (int(v) for v in X.shape)
+    V = _weight_dims(W, weight_layout)[1]
+    dt, wshape = X.dtype, (V, K) if weight_layout == TP_WEIGHTS_LINEAR else (K, V)
+    args = tp_linear_ce_bwd_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=M, V=V, K=K,
+                                 dx_dtype=_either(dX, "dX", dt), dw_dtype=_either(dW, "dW", dt),
+                                 accumulate=1 if accumulate else 0, vocab_begin=int(vocab_begin),
+                                 ignore_index=int(ignore_index), piece=int(piece))
+    args.X, args.X_ld = _mat(X, "X")
+    args.W, args.W_ld = _mat(W, "W", wshape, dt)
+    args.targets = _vec(targets, "targets", (M,), torch.int64, optional=False)
+    args.lse = _vec(lse, "lse", (M,), torch.float32, optional=False)
+    args.dloss, args.dloss_stride = _per_token(dloss, "dloss", M)
+    args.dlse, args.dlse_stride = _per_token(dlse, "dlse", M)
+    args.dX, args.dX_ld = _mat(dX, "dX", (M, K))
+    args.dW, args.dW_ld = _mat(dW, "dW", wshape)
+    args.ws, args.ws_bytes = _ws(ws)
+    return _call(lib.tp_linear_ce_backward, args, stream, prepare, (X, W, targets, lse, dloss, dlse, dX, dW, ws))
+
+
+def _one_dtype(ts, name, dtype):
+    for i, t in enumerate(ts):
+        if not hasattr(t, "data_ptr") or t.dtype != dtype:
+            raise TypeError(f"{name}[{i}] must be a {dtype} tensor")
+
+
+def _states(params, m, v, m_scale, v_scale):
+    """Checks the moments of these tensors; whether they are in 8 bits."""
+    import torch
+    if not len(params) == len(m) == len(v):
+        raise ValueError("one m and one v per tensor")
+    eight = any(t.dtype == torch.int8 for t in m) or m_scale is not None or v_scale is not None
+    _one_dtype(m, "m", torch.int8 if eight else torch.float32)
+    _one_dtype(v, "v", torch.uint8 if eight else torch.float32)
+    if eight:
+        if m_scale is None or v_scale is None or not len(m_scale) == len(v_scale) == len(params):
+            raise ValueError("8-bit states need one m_scale and one v_scale per tensor")
+        _one_dtype(m_scale, "m_scale", torch.float32)
+        _one_dtype(v_scale, "v_scale", torch.float32)
+    for i, p in enumerate(params):
+        n = p.numel()
+        if m[i].numel() != n or v[i].numel() != n:
+            raise ValueError(f"m[{i}] and v[{i}] must have {n} elements")
+        blocks = (n + TP_ADAMW_BLOCK - 1) // TP_ADAMW_BLOCK
+        if eight and (m_scale[i].numel() != blocks or v_scale[i].numel() != blocks):
+            raise ValueError(f"m_scale[{i}] and v_scale[{i}] must have {blocks} elements")
+    return eight
+
+
+def tp_adamw_step(params, grads, m, v, *, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, m_scale=None,
+                  v_scale=None, copies=None, parts=None, max_norm=None, clip_eps=1e-6, norm_out=None, ranks=1,
+                  skip_nonfinite=False, stream=None, prepare=False):
+    """One AdamW step of every tensor in one pass, in fp32:
+
+        m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+        p -= lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+
+    params and grads are lists of fp32 or bf16 tensors.  States: fp32 m and v, or int8 m and
+    uint8 v with fp32 scales, one for every TP_ADAMW_BLOCK elements (all zero before the first
+    step).  ``step`` counts from 1; it may be an int64 tensor of one element on the GPU, and
+    ``lr`` an fp32 one: a prepared or captured step then follows them.  ``weight_decay``: a number,
+    or one per tensor.  ``copies``: bf16 tensors (or None) that receive the new weights.  ``parts``
+    (from ``tp_grad_sumsq``) and ``max_norm`` clip as ``tp_grad_clip`` does, in the same pass;
+    ``norm_out`` (fp32 [1]) receives the norm, and with ``skip_nonfinite`` a step whose norm is
+    infinite or NaN changes nothing else."""
+    import torch
+    lib = load()
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    num = len(params)
+    if len(grads) != num:
+        raise ValueError("one gradient per tensor")
+    m_scale, v_scale = (None if s is None else list(s) for s in (m_scale, v_scale))
+    eight = _states(params, m, v, m_scale, v_scale)
+    copies = [None] * num if copies is None else list(copies)
+    decays = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * num
+    if len(copies) != num or len(decays) != num:
+        raise ValueError("one copy and one weight decay per tensor")
+    arr = (tp_adamw_tensor * max(1, num))()
+    for i, (p, g, c) in enumerate(zip(params, grads, copies)):
+        if g.numel() != p.numel() or (c is not None and (c.numel() != p.numel() or c.dtype != torch.bfloat16)):
+            raise ValueError(f"grads[{i}] must have its tensor's size, and copies[{i}] be bf16 of it")
+        arr[i] = tp_adamw_tensor(_ptr(p), _ptr(g), _ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]) if eight else None,
+                                 _ptr(v_scale[i]) if eight else None, _ptr(c), p.numel(), _dtype_code(p), _dtype_code(g),
+                                 float(decays[i]))
+    args = tp_adamw_args(states=TP_ADAMW_8BIT if eight else TP_ADAMW_F32, beta1=float(beta1), beta2=float(beta2),
+                         eps=float(eps), ranks=int(ranks), clip_eps=float(clip_eps), skip_nonfinite=1 if skip_nonfinite else 0)
+    if hasattr(step, "data_ptr"):
+        if step.dtype != torch.int64 or step.numel() != 1:
+            raise TypeError("step must be a number or one int64 value")
+        args.step_dev = step.data_ptr()
+    else:
+        args.step = int(step)
+    if hasattr(lr, "data_ptr"):
+        if lr.dtype != torch.float32 or lr.numel() != 1:
+            raise TypeError("lr must be a number or one fp32 value")
+        args.lr_dev = lr.data_ptr()
+    else:
+        args.lr = float(lr)
+    if parts is not None:
+        _check_parts(parts, ranks)
+        if max_norm is None:
+            raise ValueError("parts needs max_norm")
+        args.parts, args.max_norm = parts.data_ptr(), float(max_norm)
+    elif max_norm is not None:
+        raise ValueError("max_norm needs parts (tp_grad_sumsq)")
+    if norm_out is not None and (norm_out.dtype != torch.float32 or norm_out.numel() != 1):
+        raise ValueError("norm_out must be one fp32 value")
+    args.norm_out = _ptr(norm_out)
+    tensors = _tensors(params, grads, m, v, m_scale, v_scale, copies, step, lr, parts, norm_out)
+    _on_gpu(*tensors)
+    if prepare:
+        return Prepared(lib.tp_adamw_step, (arr, num, C.byref(args)), [args], [_stream_ptr(stream)], tensors)
+    _check(lib.tp_adamw_step(arr, num, C.byref(args), _stream_ptr(stream)))
+
+
+def tp_adamw_unpack(m, v, m_out, v_out, *, m_scale, v_scale, stream=None, prepare=False):
+    """The values that 8-bit states stand for, tensor by tensor, into ``m_out`` and ``v_out``
+    (lists of fp32 or bf16 tensors): what to save or to look at."""
+    lib = load()
+    m, v, m_out, v_out, m_scale, v_scale = (list(ts) for ts in (m, v, m_out, v_out, m_scale, v_scale))
+    _states(m_out, m, v, m_scale, v_scale)
+    if len(v_out) != len(m_out):
+        raise ValueError("one v_out per tensor")
+    arr = (tp_adamw_state * max(1, len(m)))()
+    for i in range(len(m)):
+        if v_out[i].dtype != m_out[i].dtype or v_out[i].numel() != m_out[i].numel():
+            raise ValueError(f"m_out[{i}] and v_out[{i}] must have one type and size")
+        arr[i] = tp_adamw_state(_ptr(m[i]), _ptr(v[i]), _ptr(m_scale[i]), _ptr(v_scale[i]), _ptr(m_out[i]),
+                                _ptr(v_out[i]), m[i].numel(), _dtype_code(m_out[i]))
+    tensors = _tensors(m, v, m_out, v_out, m_scale, v_scale)
+    _on_gpu(*tensors)
+    if prepare:
+        return Prepared(lib.tp_adamw_unpack, (arr, len(m)), [], [_stream_ptr(stream)], tensors)
+    _check(lib.tp_adamw_unpack(arr, len(m), _stream_ptr(stream)))
 
 
 def tp_timing_enable(on: bool = True):

@@ -1,0 +1,149 @@
+// Device code of the vocabulary cross entropy: row statistics of logits, how they
+// combine, and the epilogues of the products whose output are logits.
+//
+// A set of logits of one row is held as {top, s}: its maximum, and s = sum of
+// 2^(z log2 e - r) against r = top log2 e as rounded to fp32, so
+//   ln sum e^z = top + ln 2 (log2 s + (r - top log2 e)).
+// z log2 e - r is one fma: what rounding r changed is common to all terms, and the
+// last line takes it out again.  Where the maximum is not finite (or r is not) the
+// exponents are taken against 0 instead: an infinite logit makes s infinite, a NaN
+// makes it NaN, and minus infinity everywhere leaves 0.
+#pragma once
+
+#include "linear_dev.h"
+
+namespace tpshard {
+namespace ce {
+
+using lin::f32x2;
+using lin::f32x4;
+using lin::kLog2e;
+
+constexpr float kLn2 = 0.693147180559945309417f;
+
+__device__ __forceinline__ float minus_inf() { return -__builtin_inff(); }
+// What the exponents of a set with maximum `top` are taken against.
+__device__ __forceinline__ float shift_of(float top) {
+  const float r = top * kLog2e;
+  return __builtin_isfinite(r) ? r : 0.0f;
+}
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The part of {top, s} in a sum against `to`.  A set with nothing in it (s = 0, any maximum) stays out of it.
+__device__ __forceinline__ float part_of(f32x2 a, float to) { return a[1] == 0.0f ? 0.0f : a[1] * exp2_(shift_of(a[0]) - to); }
+
+__device__ __forceinline__ f32x2 join(f32x2 a, f32x2 b) {
+  const float top = fmaxf(a[0], b[0]), to = shift_of(top);
+  return f32x2{top, part_of(a, to) + part_of(b, to)};
+}
+
+// r - top log2 e, which the fma leaves unrounded (0 where the exponents were taken against 0).
+__device__ __forceinline__ float rest_of(float top) {
+  const float r = top * kLog2e;
+  return __builtin_isfinite(r) ? fmaf(-top, kLog2e, r) : 0.0f;
+}
+
+// ln sum e^z of the set.
+__device__ __forceinline__ float lse_of(f32x2 a) {
+  const float base = __builtin_isfinite(a[0] * kLog2e) ? a[0] : 0.0f;
+  return fmaf(kLn2, __builtin_amdgcn_logf(a[1]) + rest_of(a[0]), base);
+}
+
+// The column of target t among the n that begin with id `begin`, or -1 (the subtraction may wrap).
+__device__ __forceinline__ int column_of(int64_t t, int64_t begin, int64_t n) {
+  const uint64_t c = static_cast<uint64_t>(t) - static_cast<uint64_t>(begin);
+  return c < static_cast<uint64_t>(n) ? static_cast<int>(c) : -1;
+}
+
+// kModeStats: the statistics of a tile's rows.  Four lanes and WAVES_N waves share a
+// row: they join through `lds` (WAVES_N * BM pairs, the operand tiles' memory), so
+// that a tile leaves one pair a row: per wave, the pairs of 4096 x 768 x 50000 would
+// be 26 MB.
+template <int BM, int WAVES_N, int THREADS, int TM, int TN, typename RM, typename CN>
+__device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t slot,
+                                      int wn, RM&& rm, CN&& cn) {
+  f32x2 *rows = reinterpret_cast<f32x2 *>(lds);
+  const int lane = threadIdx.x & 63, N = static_cast<int>(p.N);
+  __syncthreads();   // the operand tiles have been read
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = rm(i);
+    const int t = m < p.M ? column_of(p.targets[m], p.begin, p.N) : -1;
+    float top = minus_inf();
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int n = static_cast<int>(cn(j));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < N) top = fmaxf(top, acc[i][j][e]);
+      if (static_cast<unsigned>(t - n) < 4u) {   // (t is a column or -1)
+        const float z01 = t - n == 0 ? acc[i][j][0] : acc[i][j][1], z23 = t - n == 2 ? acc[i][j][2] : acc[i][j][3];
+        p.logit[m] = t - n < 2 ? z01 : z23;
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float to = shift_of(top);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int n = static_cast<int>(cn(j));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < N) s += exp2_(fmaf(acc[i][j][e], kLog2e, -to));
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) rows[wn * BM + (m - m0)] = f32x2{top, s};
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < BM; i += THREADS) {
+    if (m0 + i >= p.M) continue;
+    f32x2 a = rows[i];
+#pragma unroll
+    for (int w = 1; w < WAVES_N; ++w) a = join(a, rows[w * BM + i]);
+    *reinterpret_cast<f32x2 *>(p.part + 2 * (slot * p.M + m0 + i)) = a;
+  }
+}
+
+// kModeProb: the gradient at the logits, rounded to the operands' type T for the two
+// products that read it.
+template <typename T, int TM, int TN, typename RM, typename CN>
+__device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN], RM&& rm, CN&& cn) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = rm(i);
+    if (m >= p.pad_rows) continue;
+    float g = 0.0f, gh = 0.0f, lse = 0.0f;
+    int t = -1;
+    bool on = false;
+    if (m < p.M) {
+      const int64_t id = p.targets[m];
+      on = id != p.ignore;
+      t = column_of(id, p.begin, p.N);
+      lse = p.lse[m];
+      g = p.g ? p.g[m * p.g_step] : 1.0f;
+      gh = p.h ? g + p.h[m * p.h_step] : g;
+    }
+    // (z - lse) log2 e: in bf16 as one fma, whose common error of 2^-24 |lse| is far below the rounding of
+    // the result; in fp32 the difference first, which is exact where z and lse are close.
+    const float far = -lse * kLog2e;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int64_t n = cn(j), left = p.N - n;
+      if (left <= 0) continue;
+      f32x4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z = acc[i][j][e];
+        const float q = sizeof(T) == 4 ? exp2_((z - lse) * kLog2e) : exp2_(fmaf(z, kLog2e, far));
+        const float d = t == static_cast<int>(n) + e ? fmaf(gh, q, -g) : gh * q;
+        y[e] = on ? d : 0.0f;
+      }
+      lin::store4<T>(p.c, m * p.ldc + n, y, left);
+    }
+  }
+}
+
+}  // namespace ce
+}  // namespace tpshard

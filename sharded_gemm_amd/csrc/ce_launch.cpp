@@ -1,0 +1,344 @@
+// The vocabulary cross entropy: which kernels run, over which pieces of the
+// vocabulary, and where in the workspace.  Host code only: what a launch reads and
+// writes can be checked without a GPU.
+#include "ce.h"
+
+#include <algorithm>
+
+#include "common.h"
+#include "timing.h"
+
+namespace tpshard {
+
+namespace {
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t cut(int64_t n, int64_t by) { return (n + by - 1) / by; }
+constexpr int64_t kAlign = 256;   // of the workspace's parts
+
+LinGemm logits_product(const CeSizes& c, int mode, int64_t N) {
+  LinGemm p;
+  p.mode = mode;
+  p.M = c.M;
+  p.N = N;
+  p.K = c.K;
+  p.f32 = c.f32;
+  p.w_t = c.linear;
+  return p;
+}
+
+// The weight from column n on.
+const void *weight_at(const CeSizes& c, const void *W, int64_t ld, int64_t n) {
+  return static_cast<const char *>(W) + (c.linear ? n * ld : n) * (c.f32 ? 4 : 2);
+}
+
+// ---- forward ---------------------------------------------------------------------
+// Few rows: the few-row kernel leaves the logits, M of them a column (64 at most,
+// where a column of the weight has K), and a pass of its own reduces them; 2^18
+// columns at a time.
+// Otherwise a product whose epilogue reduces each tile: in one launch, unless the
+// weight's bytes pass the 2^31 up to which the ping-pong kernels' offsets reach,
+// or its tiles the grid; then in even pieces of whole tiles.
+constexpr int64_t kLogitCols = int64_t{1} << 18;
+constexpr int64_t kTileCols = 768;   // a multiple of every tile's columns
+
+struct Forward {
+  bool rows = false, small = false;   // few rows; tiles of 64 columns may be picked
+  int64_t piece = 0, slots = 0;       // columns of a launch; pairs of a row at most
+  int64_t join = 0, part = 0, logit = 0, logits = 0, total = 0;   // offsets; total: bytes
+};
+
+Forward forward_plan(const CeSizes& c) {
+  Forward f;
+  if (c.M <= 0) return f;
+  const LinGemm one = logits_product(c, kModeOne, std::min(c.V, kLogitCols)), st = logits_product(c, kModeStats, c.V);
+  f.rows = lin_takes_rows(one);
+  f.small = lin_tiles_count(st, 128, 128) < 256;
+  int64_t joined = 0;
+  if (f.rows) {
+    f.piece = std::min(c.V, kLogitCols);
+    f.slots = cut(c.V, kCeStatCols);
+    joined = lin_gemm_ws(one);
+    if (c.V % f.piece) joined = std::max(joined, lin_gemm_ws(logits_product(c, kModeOne, c.V % f.piece)));
+  } else if (f.small) {
+    f.piece = c.V;
+    f.slots = cut(c.V, 64);
+    joined = lin_gemm_ws(st);
+  } else {
+    const int64_t span = std::max(kTileCols, ((int64_t{1} << 31) - 1) / (2 * c.K));
+    const int64_t grid = ((int64_t{1} << 22) - 1) / cut(c.M, 64) * 64;
+    const int64_t most = std::min(c.linear && !c.f32 ? std::min(span, grid) : grid, int64_t{1} << 25) / kTileCols * kTileCols;
+    f.piece = up(cut(c.V, cut(c.V, most)), kTileCols);
+    f.slots = cut(c.V, c.f32 ? 64 : 128) + cut(c.V, f.piece);
+  }
+  f.join = 0;
+  f.part = up(std::max(joined, kTicketBytes), kAlign);
+  f.logit = f.part + up(f.slots * c.M * 8, kAlign);
+  f.logits = f.logit + up(c.M * 4, kAlign);
+  f.total = f.logits + (f.rows ? c.M * up(f.piece, 4) * 4 : 0);
+  return f;
+}
+
+// Columns of a tile.
+int64_t columns_of(const LinChoice& h) {
+  if (!h.tiles) return h.staged.edge;
+  switch (h.tile.tile) {
+    case kTile256: return 256;
+    case kTile192: return 192;
+    case kTile128w:
+    case kTile128: return 128;
+  }
+  return 64;
+}
+
+// ---- backward ----------------------------------------------------------------------
+// For each piece of the vocabulary: the gradient at its logits, P [M, columns] in the
+// operands' type, from the product computed again; dX += P W^T; dW = X^T P.
+//
+// P has zero rows up to a multiple of 64 tokens, and X^T is kept transposed with as
+// many zero columns, those of ignored tokens among them: so the products over tokens
+// run on the tiled kernels whatever M is, what lies in X at an ignored token (a
+// padded batch's rest) does not reach dW, and only one of their operands (P, or
+// with a [K, V] weight none but P again) goes through the transposing LDS read.
+// The vocabulary's last V % 64 columns are a piece of their own, since dX's product
+// sums over columns and the tiled kernels take whole stages of them.
+//
+// Pieces: 2^28 elements of P (512 MiB in bf16), so that dX is not read and
+// written again often: with 8192 x 4096 tokens every further piece costs 268 MB.
+struct Backward {
+  int64_t rows = 0, piece = 0, whole = 0;   // tokens of P; its columns; the vocabulary in pieces of them
+  bool split_tail = false, keeps = false;   // a last piece of V - whole columns; dX is summed in the workspace
+  int64_t xt = 0, p = 0, acc = 0, total = 0;
+};
+
+LinGemm dx_product(const CeSizes& c, int64_t n) {
+  LinGemm p;
+  p.M = c.M;
+  p.N = c.K;
+  p.K = n;
+  p.f32 = c.f32;
+  p.w_t = !c.linear;
+  return p;
+}
+LinGemm dw_product(const CeSizes& c, int64_t n, int64_t rows) {
+  LinGemm p;
+  p.M = c.linear ? n : c.K;
+  p.N = c.linear ? c.K : n;
+  p.K = rows;
+  p.f32 = c.f32;
+  p.a_t = p.w_t = c.linear;
+  return p;
+}
+
+// f(first column, columns) of each piece, until one fails.
+template <typename F>
+hipError_t each_piece(const CeSizes& c, const Backward& b, F&& f) {
+  for (int64_t n = 0; n < c.V;) {
+    const int64_t left = n < b.whole ? b.whole - n : c.V - n, cols = std::min(left, b.piece);
+    const hipError_t e = f(n, cols);
+    if (e != hipSuccess) return e;
+    n += cols;
+  }
+  return hipSuccess;
+}
+
+Backward backward_plan(const CeSizes& c, const CeBackward& b) {
+  Backward q;
+  q.rows = up(c.M, 64);
+  q.split_tail = !c.f32 && c.K % 8 == 0 && c.V % 64 && c.V > 64;
+  q.whole = q.split_tail ? c.V / 64 * 64 : c.V;
+  const int64_t grid = ((int64_t{1} << 22) - 1) / std::max<int64_t>(1, std::max(cut(c.M, 64), cut(c.K, 64))) * 64;
+  int64_t most = b.piece > 0 ? std::max<int64_t>(64, b.piece / 64 * 64)
+                             : std::max<int64_t>(8192, (int64_t{1} << 28) / std::max<int64_t>(1, q.rows));
+  most = std::max<int64_t>(64, std::min(std::min(most, grid), int64_t{1} << 25) / 64 * 64);
+  const int64_t pieces = cut(q.whole, most);
+  q.piece = up(cut(q.whole, pieces), 64);
+  q.keeps = b.dX && !c.f32 && !b.dx_f32 && (pieces > 1 || q.split_tail);
+  const int64_t es = c.f32 ? 4 : 2;
+  int64_t joined = kTicketBytes;
+  if (c.M > 0)
+    (void)each_piece(c, q, [&](int64_t, int64_t n) {
+      joined = std::max(joined, lin_gemm_ws(logits_product(c, kModeProb, n)));
+      if (b.dX) joined = std::max(joined, lin_gemm_ws(dx_product(c, n)));
+      if (b.dW) joined = std::max(joined, lin_gemm_ws(dw_product(c, n, q.rows)));
+      return hipSuccess;
+    });
+  q.xt = up(joined, kAlign);
+  q.p = q.xt + (b.dW ? up(c.K * q.rows * es, kAlign) : 0);
+  q.acc = q.p + up(q.rows * q.piece * es, kAlign);
+  q.total = q.acc + (q.keeps ? c.M * c.K * 4 : 0);
+  return q;
+}
+
+template <typename F>
+hipError_t timed(hipStream_t s, int kind, double work, F&& f) {
+  hipEvent_t t0 = timing_begin(s);
+  const hipError_t e = f();
+  if (e == hipSuccess) timing_end(t0, s, kind, work);
+  return e;
+}
+
+}  // namespace
+
+bool ce_sizes_ok(const CeSizes& c) {
+  // A piece of kTileCols columns against all rows, and of all of K against them, within the grid.
+  return c.M < (int64_t{1} << 31) && c.V < (int64_t{1} << 31) && c.K < (int64_t{1} << 24) &&
+         cut(c.M, 64) * (kTileCols / 64) < (int64_t{1} << 22) && cut(c.M, 64) * cut(c.K, 64) < (int64_t{1} << 22) &&
+         c.M * 8 < (int64_t{1} << 40);
+}
+
+int64_t ce_forward_ws(const CeSizes& c) { return forward_plan(c).total; }
+
+hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats, float *loss, float *lse, void *ws,
+                             hipStream_t s) {
+  const Forward f = forward_plan(c);
+  char *base = static_cast<char *>(ws);
+  float *part = reinterpret_cast<float *>(base + f.part), *logit = reinterpret_cast<float *>(base + f.logit);
+  int64_t slots = 0;
+  for (int64_t n = 0; n < c.V; n += f.piece) {
+    CeGemm p;
+    static_cast<LinGemm&>(p) = logits_product(c, f.rows ? kModeOne : kModeStats, std::min(f.piece, c.V - n));
+    p.a = o.X;
+    p.lda = o.X_ld;
+    p.w = weight_at(c, o.W, o.W_ld, n);
+    p.ldw = o.W_ld;
+    const double flops = 2.0 * static_cast<double>(c.M) * static_cast<double>(p.N) * static_cast<double>(c.K);
+    hipError_t e;
+    if (f.rows) {
+      p.c = base + f.logits;
+      p.ldc = up(f.piece, 4);
+      p.c_f32 = 1;
+      e = timed(s, TP_KERNEL_GEMM1, flops, [&] { return lin_gemm_launch(p, s, ws, f.part); });
+      if (e != hipSuccess) return e;
+      CeLogits q;
+      q.z = reinterpret_cast<const float *>(base + f.logits);
+      q.ld = p.ldc;
+      q.M = c.M;
+      q.n = p.N;
+      q.targets = o.targets;
+      q.begin = o.begin + n;
+      q.part = part + 2 * slots * c.M;
+      q.logit = logit;
+      e = timed(s, TP_KERNEL_REDUCE, 4.0 * static_cast<double>(c.M) * static_cast<double>(p.N), [&] { return ce_logits_launch(q, s); });
+      slots += cut(p.N, kCeStatCols);
+    } else {
+      p.targets = o.targets;
+      p.begin = o.begin + n;
+      p.part = part;
+      p.slot0 = slots;
+      p.logit = logit;
+      LinChoice h = lin_choose(&p, ws, f.small ? f.part : 0);
+      if (!f.small) {   // what the workspace was measured for
+        if (h.tiles && columns_of(h) < 128) h.tile = {kTile128, 1};
+        if (!h.tiles && !c.f32) h.staged = {128, 1, lin_tiles_count(p, 128, 128)};
+      }
+      e = timed(s, TP_KERNEL_GEMM1, flops, [&] { return h.tiles ? lin_tiles_stats(p, h.tile, s) : lin_staged_launch(p, h.staged, s); });
+      slots += cut(p.N, columns_of(h));
+    }
+    if (e != hipSuccess) return e;
+  }
+  CeJoin j;
+  j.part = part;
+  j.logit = logit;
+  j.targets = o.targets;
+  j.M = c.M;
+  j.V = c.V;
+  j.slots = slots;
+  j.begin = o.begin;
+  j.ignore = o.ignore;
+  j.stats = stats;
+  j.loss = loss;
+  j.lse = lse;
+  return timed(s, TP_KERNEL_REDUCE, 8.0 * static_cast<double>(slots) * static_cast<double>(c.M), [&] { return ce_join_launch(j, s); });
+}
+
+int64_t ce_backward_ws(const CeSizes& c, const CeBackward& b) { return b.dX || b.dW ? backward_plan(c, b).total : 0; }
+
+hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBackward& b, void *ws, hipStream_t s) {
+  if (!b.dX && !b.dW) return hipSuccess;
+  const Backward q = backward_plan(c, b);
+  char *base = static_cast<char *>(ws);
+  const int64_t es = c.f32 ? 4 : 2, dw_es = b.dw_f32 ? 4 : 2;
+  const double MK = static_cast<double>(c.M) * static_cast<double>(c.K);
+  hipError_t e;
+  if (b.dW && c.M > 0) {
+    CeTranspose t;
+    t.X = o.X;
+    t.xt = base + q.xt;
+    t.M = c.M;
+    t.K = c.K;
+    t.X_ld = o.X_ld;
+    t.rows = q.rows;
+    t.targets = o.targets;
+    t.ignore = o.ignore;
+    t.f32 = c.f32;
+    t.tickets = reinterpret_cast<uint32_t *>(base);
+    e = timed(s, TP_KERNEL_REDUCE, 2.0 * static_cast<double>(es) * MK, [&] { return ce_transpose_launch(t, s); });
+  } else {
+    e = zero_tickets_launch(reinterpret_cast<uint32_t *>(base), s);
+  }
+  if (e != hipSuccess) return e;
+  e = each_piece(c, q, [&](int64_t n, int64_t cols) {
+    const double flops = 2.0 * MK * static_cast<double>(cols);
+    hipError_t r = hipSuccess;
+    if (c.M > 0) {
+      CeGemm p;
+      static_cast<LinGemm&>(p) = logits_product(c, kModeProb, cols);
+      p.a = o.X;
+      p.lda = o.X_ld;
+      p.w = weight_at(c, o.W, o.W_ld, n);
+      p.ldw = o.W_ld;
+      p.c = base + q.p;
+      p.ldc = q.piece;
+      p.c_f32 = c.f32;
+      p.targets = o.targets;
+      p.begin = o.begin + n;
+      p.ignore = o.ignore;
+      p.lse = b.lse;
+      p.g = b.g;
+      p.g_step = b.g_step;
+      p.h = b.h;
+      p.h_step = b.h_step;
+      p.pad_rows = q.rows;
+      const LinChoice h = lin_choose(&p, ws, q.xt);
+      r = timed(s, TP_KERNEL_GEMM1, flops, [&] { return h.tiles ? lin_tiles_prob(p, h.tile, s) : lin_staged_launch(p, h.staged, s); });
+      if (r != hipSuccess) return r;
+    }
+    if (b.dX && c.M > 0) {
+      LinGemm p = dx_product(c, cols);
+      p.a = base + q.p;
+      p.lda = q.piece;
+      p.w = weight_at(c, o.W, o.W_ld, n);
+      p.ldw = o.W_ld;
+      p.c = q.keeps ? base + q.acc : static_cast<char *>(b.dX);
+      p.ldc = q.keeps ? c.K : b.dX_ld;
+      p.c_f32 = q.keeps || b.dx_f32;
+      p.acc_c = n > 0;
+      r = timed(s, TP_KERNEL_GEMM_DGRAD, flops, [&] { return lin_gemm_launch(p, s, ws, q.xt); });
+      if (r != hipSuccess) return r;
+    }
+    if (b.dW) {
+      LinGemm p = dw_product(c, cols, q.rows);
+      const void *P = base + q.p, *xt = base + q.xt;
+      p.a = c.linear ? P : xt;
+      p.lda = c.linear ? q.piece : q.rows;
+      p.w = c.linear ? xt : P;
+      p.ldw = c.linear ? q.rows : q.piece;
+      p.c = static_cast<char *>(b.dW) + (c.linear ? n * b.dW_ld : n) * dw_es;
+      p.ldc = b.dW_ld;
+      p.c_f32 = b.dw_f32;
+      p.acc_c = b.accumulate;
+      r = timed(s, TP_KERNEL_GEMM_WGRAD, flops, [&] {
+        if (!c.linear) return lin_gemm_launch(p, s, ws, q.xt);
+        const LinChoice h = lin_choose(&p, ws, q.xt);
+        return h.tiles ? lin_tiles_wgrad(p, h.tile, s) : lin_staged_launch(p, h.staged, s);
+      });
+    }
+    return r;
+  });
+  if (e != hipSuccess || !q.keeps || c.M <= 0) return e;
+  return timed(s, TP_KERNEL_REDUCE, 6.0 * MK,
+               [&] { return ce_round_launch(reinterpret_cast<const float *>(base + q.acc), b.dX, c.M, c.K, b.dX_ld, s); });
+}
+
+}  // namespace tpshard

@@ -9,12 +9,14 @@
 
 namespace tpshard {
 
-// What a product's two weight operands mean.
+// What a product's two weight operands mean, or what becomes of it.
 enum {
   kModeOne = 0,   // c = epi(A W)
   kModeDual = 1,  // gated: G = A W, U = A W2, c = act(G) * U; aux, aux2 keep G, U
   kModeCat = 2,   // c = A W + A2 W2 (one accumulator over both)
   kModePair = 3,  // c = A W and c2 = A2 W2, two products of one shape in one launch
+  kModeStats = 4, // logits z = A W: each tile's row maxima and sums of exponentials (CeGemm)
+  kModeProb = 5,  // logits z = A W: c = the loss's gradient at z (CeGemm)
 };
 
 // A workspace's first bytes are tickets (zero before and after every launch), its
@@ -50,6 +52,40 @@ struct LinGemm {
   float *join = nullptr;
   uint32_t *tickets = nullptr;
 };
+
+// A product whose columns are logits, those of the ids begin .. begin + N - 1.
+struct CeGemm : LinGemm {
+  const int64_t *targets = nullptr;   // [M]
+  int64_t begin = 0;
+  // kModeStats: part[(slot0 + column tile) * M + m] <- {maximum, sum} of that tile's logits of row m (ce_dev.h);
+  // logit[m] <- the target's logit, where it is one of these columns.
+  float *part = nullptr;
+  int64_t slot0 = 0;
+  float *logit = nullptr;
+  // kModeProb: c[m, n] <- (g + h) exp(z - lse) - (id n is the target) g, 0 in the rows of ignored targets and
+  // in the rows M .. pad_rows - 1.  g = g[m * g_step], h likewise or 0.
+  const float *lse = nullptr, *g = nullptr, *h = nullptr;
+  int64_t g_step = 0, h_step = 0, ignore = 0, pad_rows = 0;
+};
+// A kernel's arguments.  (By specialisation: an expression of the unnamed enum above in a
+// kernel's signature would be part of its symbol, and numbered differently in host and device
+// code.)
+template <int MODE>
+struct LinArgsOf {
+  using type = LinGemm;
+};
+template <>
+struct LinArgsOf<kModeStats> {
+  using type = CeGemm;
+};
+template <>
+struct LinArgsOf<kModeProb> {
+  using type = CeGemm;
+};
+template <int MODE>
+using LinArgs = typename LinArgsOf<MODE>::type;
+template <int MODE>
+inline const LinArgs<MODE>& lin_args(const LinGemm& p) { return static_cast<const LinArgs<MODE>&>(p); }
 
 // Which kernel takes a product, and how (linear_launch.cpp).
 
@@ -87,6 +123,9 @@ hipError_t lin_tiles_one(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_dual(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_cat(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_pair(const LinGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_stats(const CeGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_prob(const CeGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_wgrad(const LinGemm& p, const TilePick& t, hipStream_t s);   // kModeOne, a_t and w_t
 
 // The kernel for few rows.
 constexpr int kRowsWaves = 8;   // of a workgroup, at most (measured against 4 and 16 with one token)
@@ -95,6 +134,17 @@ struct RowsShape {
   int64_t tiles, cells;         // cells: floats of a workgroup's partial
 };
 hipError_t lin_rows_launch(const LinGemm& p, const RowsShape& h, hipStream_t s);
+
+// The choices that lin_gemm_launch makes, for products that are launched elsewhere: the
+// kernel for many rows (with its splits' place in the workspace put into *p), and whether few
+// rows run on their own.
+struct LinChoice {
+  bool tiles;          // on the tiled bf16 kernels, else on the general one
+  TilePick tile;
+  StagedShape staged;
+};
+LinChoice lin_choose(LinGemm *p, void *ws, int64_t ws_bytes);
+bool lin_takes_rows(const LinGemm& p);
 
 // ---- gradients at the activation -----------------------------------------
 // kLinear: d_pre = d_out * act'(pre) (pre NULL: d_pre = d_out, not written) and,

@@ -8,63 +8,16 @@
 #include <new>
 #include <vector>
 
-#include "common.h"
+#include "args.h"
 #include "linear.h"
 #include "timing.h"
 
 namespace tpshard {
 namespace {
 
-constexpr int64_t kMaxDim = int64_t{1} << 31;
 constexpr int64_t kMaxRanks = 64;
 constexpr int64_t kWsAlign = 256;
 static_assert(kGradParts == TP_GRAD_PARTS, "the header's count");
-
-int hip_fail(hipError_t e, const char *what) {
-  return fail(TP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-// A matrix argument: rows x cols at row stride ld (0 = contiguous).
-struct Mat {
-  const void *p = nullptr;
-  int64_t rows = 0, cols = 0, ld = 0, es = 0;
-  const char *name = "";
-  int64_t bytes() const { return rows <= 0 || cols <= 0 || !p ? 0 : ((rows - 1) * ld + cols) * es; }
-};
-
-// Fills *m; the stride must cover a row, the pointer be aligned to its element.
-int take(Mat *m, const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t es, bool needed) {
-  *m = Mat{p, rows, cols, ld ? ld : cols, es, name};
-  if (!p) return needed ? fail(TP_ERR_ARG, "%s must be non-NULL", name) : TP_OK;
-  if (m->ld < cols) return fail(TP_ERR_ARG, "%s: row stride %lld < %lld", name, (long long)m->ld, (long long)cols);
-  if (m->ld >= kMaxDim)
-    return fail(TP_ERR_UNSUPPORTED, "%s: row stride %lld exceeds the kernels' range", name, (long long)m->ld);
-  if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(es))
-    return fail(TP_ERR_ARG, "%s is not aligned to its elements", name);
-  return TP_OK;
-}
-
-// Whether two matrices share an element.  Column blocks of one larger matrix
-// (one row pitch) interleave in memory without sharing any: then the columns'
-// places within the pitch decide.
-bool share(const Mat& a, const Mat& b) {
-  if (!overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
-  if (reinterpret_cast<uintptr_t>(b.p) < reinterpret_cast<uintptr_t>(a.p)) return share(b, a);
-  const uintptr_t pitch = static_cast<uintptr_t>(a.ld * a.es);
-  if (a.ld * a.es != b.ld * b.es) return true;
-  const uintptr_t at = (reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % pitch;
-  return at < static_cast<uintptr_t>(a.cols * a.es) || at + static_cast<uintptr_t>(b.cols * b.es) > pitch;
-}
-
-int disjoint(std::initializer_list<Mat> ins, std::initializer_list<Mat> outs) {
-  for (const Mat *o = outs.begin(); o != outs.end(); ++o) {
-    for (const Mat& in : ins)
-      if (share(*o, in)) return fail(TP_ERR_ARG, "%s overlaps %s", o->name, in.name);
-    for (const Mat *e = outs.begin(); e != o; ++e)
-      if (share(*o, *e)) return fail(TP_ERR_ARG, "%s overlaps %s", o->name, e->name);
-  }
-  return TP_OK;
-}
 
 int check_common(int32_t dtype, int32_t act, int32_t layout, int64_t M, int64_t N, int64_t K, const char *n_name) {
   if (!dtype_size(dtype)) return fail(TP_ERR_ARG, "unknown dtype %d", dtype);
@@ -74,30 +27,6 @@ int check_common(int32_t dtype, int32_t act, int32_t layout, int64_t M, int64_t 
   if (M < 0 || N < 1 || K < 1) return fail(TP_ERR_ARG, "need M >= 0, %s >= 1 and K >= 1", n_name);
   if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || !lin_grid_ok(M, N) || !lin_grid_ok(M, K) || !lin_grid_ok(K, N))
     return fail(TP_ERR_UNSUPPORTED, "sizes exceed the kernels' index range or grid");
-  return TP_OK;
-}
-
-// An output's type: the operands', or fp32.
-int check_out_dtype(int32_t out, int32_t dtype, const char *name) {
-  if (out != dtype && out != TP_F32) return fail(TP_ERR_ARG, "%s = %d is neither dtype nor TP_F32", name, out);
-  return TP_OK;
-}
-
-int check_ws(const void *ws, int64_t have, int64_t need) {
-  if (!need) return TP_OK;
-  if (!ws || have < need)
-    return fail(TP_ERR_ARG, "the workspace holds %lld bytes, %lld are needed", (long long)(ws ? have : 0), (long long)need);
-  if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(TP_ERR_ARG, "ws is not 16-byte aligned");
-  return TP_OK;
-}
-
-int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
-
-// An optional workspace: given at all, it has to be aligned and apart.
-int take_ws(Mat *m, void *ws, int64_t bytes) {
-  if (!ws || bytes <= 0) return TP_OK;
-  if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(TP_ERR_ARG, "ws is not 16-byte aligned");
-  *m = Mat{ws, 1, bytes, bytes, 1, "ws"};
   return TP_OK;
 }
 

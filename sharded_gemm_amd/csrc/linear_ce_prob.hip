@@ -1,0 +1,10 @@
+// Tiled bf16 kernels: logits computed again and turned into the loss's gradient at them.
+#include "linear_tiles.h"
+
+namespace tpshard {
+
+hipError_t lin_tiles_prob(const CeGemm& p, const TilePick& t, hipStream_t s) {
+  return p.w_t ? dispatch_tiles<kModeProb, false, true>(p, t, s) : dispatch_tiles<kModeProb, false, false>(p, t, s);
+}
+
+}  // namespace tpshard

@@ -167,17 +167,28 @@ hipError_t launch_rows(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
   return lin_rows_launch(p, h, s);
 }
 
-hipError_t launch_staged(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
-  StagedShape h = staged_shape(p, true);
-  if (ws_bytes < ws_of(h)) h = staged_shape(p, false);
-  if (h.splits > 1) take_ws(&p, ws);
-  return lin_staged_launch(p, h, s);
+}  // namespace
+
+LinChoice lin_choose(LinGemm *p, void *ws, int64_t ws_bytes) {
+  LinChoice c{tiles_ok(*p), {}, {}};
+  if (c.tiles) {
+    c.tile = pick(*p);
+    if (ws_bytes < ws_of(*p, c.tile)) c.tile.splits = 1;
+    if (c.tile.splits > 1) take_ws(p, ws);
+  } else {
+    c.staged = staged_shape(*p, true);
+    if (ws_bytes < ws_of(c.staged)) c.staged = staged_shape(*p, false);
+    if (c.staged.splits > 1) take_ws(p, ws);
+  }
+  return c;
 }
 
-hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
-  TilePick t = pick(p);
-  if (ws_bytes < ws_of(p, t)) t.splits = 1;
-  if (t.splits > 1) take_ws(&p, ws);
+namespace {
+
+hipError_t launch_many(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
+  const LinChoice c = lin_choose(&p, ws, ws_bytes);
+  if (!c.tiles) return lin_staged_launch(p, c.staged, s);
+  const TilePick& t = c.tile;
   if (p.a_t) return lin_tiles_pair(p, t, s);
   switch (p.mode) {
     case kModeOne: return lin_tiles_one(p, t, s);
@@ -188,6 +199,8 @@ hipError_t launch_tiles(LinGemm p, void *ws, int64_t ws_bytes, hipStream_t s) {
 }
 
 }  // namespace
+
+bool lin_takes_rows(const LinGemm& p) { return takes_rows(p, INT64_MAX); }
 
 // A launch holds fewer than 2^32 threads. Tiles: up to 2^22 of 64 x 64, 256
 // threads each, twice where two products share a launch (2^31). Few rows: 16
@@ -209,8 +222,7 @@ hipError_t lin_gemm_launch(const LinGemm& p, hipStream_t s, void *ws, int64_t ws
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
   if (!ws) ws_bytes = 0;
   if (takes_rows(p, ws_bytes)) return launch_rows(p, ws, ws_bytes, s);
-  if (tiles_ok(p)) return launch_tiles(p, ws, ws_bytes, s);
-  return launch_staged(p, ws, ws_bytes, s);
+  return launch_many(p, ws, ws_bytes, s);
 }
 
 // The grid of the activation's gradient: 64 rows to a slab, fewer where that leaves

@@ -3,6 +3,7 @@
 //
 //   kModeOne  c = epi(A W)              kModeDual  c = act(A W) * (A W2)
 //   kModeCat  c = A W + A2 W2           kModePair  c = A W, c2 = A2 W2
+//   kModeStats, kModeProb: the vocabulary cross entropy's (ce_dev.h)
 //
 // A workgroup of 4 or 8 waves owns a BM x BN tile of the output (kModeDual: BM x
 // BN/2, with the gate's and the up projection's columns side by side in the W
@@ -23,6 +24,9 @@
 // 1021 x 1531 28 us (58); bf16 4097 x 4095 x 4097 270 us (509), the gated
 // backward 1021 x 1337 -> 999 32 + 25 us.  Odd strides cost: a 16-byte load off a
 // 4-byte boundary goes through the address unit a lane at a time.
+#include <type_traits>
+
+#include "ce_dev.h"
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -141,7 +145,7 @@ constexpr int threads_of(int edge) { return edge == 128 ? 512 : 256; }
 constexpr int waves_simd(int edge) { return edge == 128 ? 4 : 2; }
 
 template <typename T, int BM, int BN, bool AKC, bool WKC, int MODE>
-__global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_kernel(LinGemm p) {
+__global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_kernel(LinArgs<MODE> p) {
   constexpr int THREADS = threads_of(BM);
   using TA = Tile<T, BM, AKC, THREADS>;
   using TW = Tile<T, BN, WKC, THREADS>;
@@ -318,15 +322,17 @@ __global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_ker
     const int wcols = MODE == kModeDual ? WN / 2 : WN;
     return n0 + wn * wcols + j * 16 + 4 * (lane >> 4);
   };
-  if constexpr (sizeof(T) == 4) epilogue<float, MODE>(p, c, acc, rm, cn);
+  if constexpr (MODE == kModeStats) ce::stats<BM, WAVES_N, THREADS>(p, smem, acc, m0, p.slot0 + n0 / BN, wn, rm, cn);
+  else if constexpr (MODE == kModeProb) ce::prob<std::conditional_t<sizeof(T) == 4, float, uint16_t>>(p, acc, rm, cn);
+  else if constexpr (sizeof(T) == 4) epilogue<float, MODE>(p, c, acc, rm, cn);
   else epilogue<uint16_t, MODE>(p, c, acc, rm, cn);
 }
 
 template <typename T, bool AKC, bool WKC, int MODE>
 hipError_t launch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(h.tiles), static_cast<unsigned>(h.splits));
-  if (h.edge == 128) hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), grid, dim3(threads_of(128)), 0, s, p);
-  else hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), grid, dim3(threads_of(64)), 0, s, p);
+  if (h.edge == 128) hipLaunchKernelGGL((lin_staged_kernel<T, 128, 128, AKC, WKC, MODE>), grid, dim3(threads_of(128)), 0, s, lin_args<MODE>(p));
+  else hipLaunchKernelGGL((lin_staged_kernel<T, 64, 64, AKC, WKC, MODE>), grid, dim3(threads_of(64)), 0, s, lin_args<MODE>(p));
   return hipGetLastError();
 }
 
@@ -346,8 +352,14 @@ hipError_t dispatch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
     case kModePair:
       if (!akc && !wkc) return launch<T, false, false, kModePair>(p, h, s);
       break;
+    case kModeStats:
+      if (akc) return wkc ? launch<T, true, true, kModeStats>(p, h, s) : launch<T, true, false, kModeStats>(p, h, s);
+      break;
+    case kModeProb:
+      if (akc) return wkc ? launch<T, true, true, kModeProb>(p, h, s) : launch<T, true, false, kModeProb>(p, h, s);
+      break;
   }
-  if (p.mode == kModeOne && !akc && !wkc) return launch<T, false, false, kModeOne>(p, h, s);
+  if (p.mode == kModeOne && !akc) return wkc ? launch<T, false, true, kModeOne>(p, h, s) : launch<T, false, false, kModeOne>(p, h, s);
   return hipErrorInvalidValue;
 }
 

@@ -9,6 +9,7 @@
 // the up projection would read X twice and pass both results through memory.
 #pragma once
 
+#include "ce_dev.h"
 #include "gemm_tiles.h"
 #include "linear_dev.h"
 
@@ -66,7 +67,7 @@ __device__ __forceinline__ Place place_of(const LinGemm& p) {
 // Ring kernel (gemm_tiles.h, ring_loop): tiles for problems that fill the chip
 // with smaller ones only, any K that is a multiple of BK.
 template <int BM, int BN, int BK, int S, int MODE, bool AT, bool WT, int WAVES_M, int WAVES_N>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(LinGemm p) {
+__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(LinArgs<MODE> p) {
   using C = DmaCfg<BM, BN, BK, S, AT, WT, WAVES_M, WAVES_N>;
   using TA = typename C::TA;
   using TW = typename C::TW;
@@ -140,12 +141,15 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(Lin
   auto cn = [&](int j) -> int64_t {
     return pl.n0 + wn * (MODE == kModeDual ? C::WN / 2 : C::WN) + j * 16 + 4 * (lane >> 4);
   };
-  lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
+  if constexpr (MODE == kModeStats)
+    ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, rm, cn);
+  else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
+  else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
 }
 
 // Ping-pong kernel (gemm_tiles.h, pps_loop) on 256-row tiles.
 template <int BM, int BN, int MODE, bool AT, bool WT, int WGM = 2>
-__global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinGemm p) {
+__global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
   constexpr int BK = 64, NG = 4, SA = 3, SW = 2;
   using C = DmaCfg<BM, BN, BK, 2, AT, WT, WGM, 8 / WGM>;
   using TA = typename C::TA;
@@ -198,7 +202,10 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinGemm p) {
   auto cn = [&](int j) -> int64_t {
     return pl.n0 + wn * (MODE == kModeDual ? C::WN / 2 : C::WN) + j * 16 + 4 * (lane >> 4);
   };
-  lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
+  if constexpr (MODE == kModeStats)
+    ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, rm, cn);
+  else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
+  else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
 }
 
 // ---- launchers -----------------------------------------------------------------
@@ -207,14 +214,16 @@ template <int BM, int BN, int BK, int S, int MODE, bool AT, bool WT, int WAVES_M
 hipError_t launch_ring(const LinGemm& p, int splits, hipStream_t s) {
   hipLaunchKernelGGL((lin_ring_kernel<BM, BN, BK, S, MODE, AT, WT, WAVES_M, WAVES_N>),
                      dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN)), static_cast<unsigned>(splits)),
-                     dim3(64 * WAVES_M * WAVES_N), 0, s, p);
+                     dim3(64 * WAVES_M * WAVES_N), 0, s,
+                     lin_args<MODE>(p));
   return hipGetLastError();
 }
 
 template <int BM, int BN, int MODE, bool AT, bool WT, int WGM = 2>
 hipError_t launch_lin_pps(const LinGemm& p, hipStream_t s) {
   hipLaunchKernelGGL((lin_pps_kernel<BM, BN, MODE, AT, WT, WGM>),
-                     dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN))), dim3(512), 0, s, p);
+                     dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN))), dim3(512), 0, s,
+                     lin_args<MODE>(p));
   return hipGetLastError();
 }
 
