@@ -85,6 +85,14 @@ struct CeTranspose {
 };
 hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t s);
 
+// to [rows, cols] (bf16, contiguous, both multiples of 8) <- from [m, n] at stride ld, zero beyond.
+struct CePad {
+  const void *from = nullptr;
+  void *to = nullptr;
+  int64_t m = 0, n = 0, ld = 0, rows = 0, cols = 0;
+};
+hipError_t ce_pad_launch(const CePad& p, hipStream_t s);
+
 // out [M, K] (bf16, stride ld) <- from [M, K] (fp32, contiguous).
 hipError_t ce_round_launch(const float *from, void *out, int64_t M, int64_t K, int64_t ld, hipStream_t s);
 

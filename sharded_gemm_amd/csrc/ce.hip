@@ -161,6 +161,15 @@ __global__ void __launch_bounds__(kThreads) ce_transpose_kernel(CeTranspose p) {
   }
 }
 
+// ---- a padded copy -------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) ce_pad_kernel(CePad p) {
+  const int64_t per = p.cols / 8, i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= p.rows * per) return;
+  const int64_t r = i / per, c = i % per * 8, left = r < p.m ? p.n - c : 0;
+  *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.to) + i * 8) =
+      left > 0 ? load16<uint16_t>(static_cast<const uint16_t *>(p.from) + r * p.ld + c, left) : u32x4{0, 0, 0, 0};
+}
+
 // ---- the rounded sum over pieces ------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) ce_round_kernel(const float *from, uint16_t *out, int64_t M, int64_t K, int64_t ld) {
   const int64_t per = (K + 3) / 4, i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -194,6 +203,11 @@ hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.K + 63) / 64 * (p.rows / 64)));
   if (p.f32) hipLaunchKernelGGL(ce_transpose_kernel<uint32_t>, grid, dim3(kThreads), 0, s, p);
   else hipLaunchKernelGGL(ce_transpose_kernel<uint16_t>, grid, dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t ce_pad_launch(const CePad& p, hipStream_t s) {
+  hipLaunchKernelGGL(ce_pad_kernel, dim3(grid_of(p.rows * (p.cols / 8), kThreads)), dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 

@@ -59,23 +59,26 @@ __device__ __forceinline__ int column_of(int64_t t, int64_t begin, int64_t n) {
 // row: they join through `lds` (WAVES_N * BM pairs, the operand tiles' memory), so
 // that a tile leaves one pair a row: per wave, the pairs of 4096 x 768 x 50000 would
 // be 26 MB.
+//
+// A lane's share is max, fma, exp2 and add for each of its elements; the columns' bounds
+// are only checked in tiles that reach past the last one (checked everywhere: TIMES).
 template <int BM, int WAVES_N, int THREADS, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t slot,
-                                      int wn, RM&& rm, CN&& cn) {
+                                      int wn, bool whole, RM&& rm, CN&& cn) {
   f32x2 *rows = reinterpret_cast<f32x2 *>(lds);
-  const int lane = threadIdx.x & 63, N = static_cast<int>(p.N);
+  const int lane = threadIdx.x & 63, N = static_cast<int>(p.cols);
   __syncthreads();   // the operand tiles have been read
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  auto row = [&](auto checked, int i) {
+    constexpr bool CHECK = decltype(checked)::value != 0;
     const int64_t m = rm(i);
-    const int t = m < p.M ? column_of(p.targets[m], p.begin, p.N) : -1;
+    const int t = m < p.M ? column_of(p.targets[m], p.begin, p.cols) : -1;
     float top = minus_inf();
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int n = static_cast<int>(cn(j));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < N) top = fmaxf(top, acc[i][j][e]);
+        if (!CHECK || n + e < N) top = fmaxf(top, acc[i][j][e]);
       if (static_cast<unsigned>(t - n) < 4u) {   // (t is a column or -1)
         const float z01 = t - n == 0 ? acc[i][j][0] : acc[i][j][1], z23 = t - n == 2 ? acc[i][j][2] : acc[i][j][3];
         p.logit[m] = t - n < 2 ? z01 : z23;
@@ -90,11 +93,18 @@ __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&
       const int n = static_cast<int>(cn(j));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < N) s += exp2_(fmaf(acc[i][j][e], kLog2e, -to));
+        if (!CHECK || n + e < N) s += exp2_(fmaf(acc[i][j][e], kLog2e, -to));
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (lane < 16) rows[wn * BM + (m - m0)] = f32x2{top, s};
+  };
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) row(lin::Const<0>{}, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) row(lin::Const<1>{}, i);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < BM; i += THREADS) {
@@ -120,7 +130,7 @@ __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN]
     if (m < p.M) {
       const int64_t id = p.targets[m];
       on = id != p.ignore;
-      t = column_of(id, p.begin, p.N);
+      t = column_of(id, p.begin, p.cols);
       lse = p.lse[m];
       g = p.g ? p.g[m * p.g_step] : 1.0f;
       gh = p.h ? g + p.h[m * p.h_step] : g;
@@ -136,9 +146,19 @@ __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN]
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float z = acc[i][j][e];
-        const float q = sizeof(T) == 4 ? exp2_((z - lse) * kLog2e) : exp2_(fmaf(z, kLog2e, far));
-        const float d = t == static_cast<int>(n) + e ? fmaf(gh, q, -g) : gh * q;
-        y[e] = on ? d : 0.0f;
+        y[e] = gh * (sizeof(T) == 4 ? exp2_((z - lse) * kLog2e) : exp2_(fmaf(z, kLog2e, far)));
+      }
+      const int at = t - static_cast<int>(n);
+      if (static_cast<unsigned>(at) < 4u) {   // (t is a column or -1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at == e) y[e] -= g;
+      }
+      const int64_t there = on ? p.cols - n : 0;
+      if (there < 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e >= there) y[e] = 0.0f;
       }
       lin::store4<T>(p.c, m * p.ldc + n, y, left);
     }

@@ -32,6 +32,47 @@ const void *weight_at(const CeSizes& c, const void *W, int64_t ld, int64_t n) {
   return static_cast<const char *>(W) + (c.linear ? n * ld : n) * (c.f32 ? 4 : 2);
 }
 
+// Whether X and W are copied into the workspace, K padded to whole stages and W's
+// rows aligned, so that the tiled bf16 kernels take sizes that are no multiple of
+// anything.  The copy moves four bytes for each element of W; the general kernel
+// runs at 300 to 500 TFLOP/s where the tiled ones reach 1300: from some hundred
+// tokens on the copy pays.  (MI355X, COPYTIMES.)
+bool padded(const CeSizes& c, int64_t least) {
+  return !c.f32 && c.M >= least && (c.K % 32 || (c.K % 64 && c.K >= 256) || (!c.linear && c.V % 8));
+}
+// Columns from n on of W, `cols` of them, as [columns][K] or [K][columns], padded.
+CePad pad_weight(const CeSizes& c, const CeOperands& o, int64_t n, int64_t cols, int64_t cols_pad, int64_t K_pad, void *to) {
+  CePad p;
+  p.from = weight_at(c, o.W, o.W_ld, n);
+  p.ld = o.W_ld;
+  p.to = to;
+  p.m = c.linear ? cols : c.K;
+  p.n = c.linear ? c.K : cols;
+  p.rows = c.linear ? cols_pad : K_pad;
+  p.cols = c.linear ? K_pad : cols_pad;
+  return p;
+}
+CePad pad_x(const CeSizes& c, const CeOperands& o, int64_t K_pad, void *to) {
+  CePad p;
+  p.from = o.X;
+  p.ld = o.X_ld;
+  p.to = to;
+  p.m = p.rows = c.M;
+  p.n = c.K;
+  p.cols = K_pad;
+  return p;
+}
+template <typename F>
+hipError_t timed(hipStream_t s, int kind, double work, F&& f) {
+  hipEvent_t t0 = timing_begin(s);
+  const hipError_t e = f();
+  if (e == hipSuccess) timing_end(t0, s, kind, work);
+  return e;
+}
+hipError_t pad(const CePad& p, hipStream_t s) {
+  return timed(s, TP_KERNEL_REDUCE, 4.0 * static_cast<double>(p.rows) * static_cast<double>(p.cols), [&] { return ce_pad_launch(p, s); });
+}
+
 // ---- forward ---------------------------------------------------------------------
 // Few rows: the few-row kernel leaves the logits, M of them a column (64 at most,
 // where a column of the weight has K), and a pass of its own reduces them; 2^18
@@ -42,10 +83,11 @@ const void *weight_at(const CeSizes& c, const void *W, int64_t ld, int64_t n) {
 constexpr int64_t kLogitCols = int64_t{1} << 18;
 constexpr int64_t kTileCols = 768;   // a multiple of every tile's columns
 
+constexpr int64_t kPadLeast = 512;   // tokens from which on X and W are padded
 struct Forward {
-  bool rows = false, small = false;   // few rows; tiles of 64 columns may be picked
-  int64_t piece = 0, slots = 0;       // columns of a launch; pairs of a row at most
-  int64_t join = 0, part = 0, logit = 0, logits = 0, total = 0;   // offsets; total: bytes
+  bool rows = false, small = false, pad = false;   // few rows; tiles of 64 columns may be picked; padded copies
+  int64_t piece = 0, slots = 0, K = 0;             // columns of a launch; pairs of a row at most; K as multiplied
+  int64_t part = 0, logit = 0, logits = 0, x = 0, w = 0, total = 0;   // offsets; total: bytes
 };
 
 Forward forward_plan(const CeSizes& c) {
@@ -54,6 +96,8 @@ Forward forward_plan(const CeSizes& c) {
   const LinGemm one = logits_product(c, kModeOne, std::min(c.V, kLogitCols)), st = logits_product(c, kModeStats, c.V);
   f.rows = lin_takes_rows(one);
   f.small = lin_tiles_count(st, 128, 128) < 256;
+  f.pad = !f.rows && padded(c, kPadLeast);
+  f.K = f.pad ? up(c.K, 64) : c.K;
   int64_t joined = 0;
   if (f.rows) {
     f.piece = std::min(c.V, kLogitCols);
@@ -63,19 +107,25 @@ Forward forward_plan(const CeSizes& c) {
   } else if (f.small) {
     f.piece = c.V;
     f.slots = cut(c.V, 64);
-    joined = lin_gemm_ws(st);
+    LinGemm q = st;
+    q.K = f.K;
+    q.groups = f.pad;
+    joined = lin_gemm_ws(q);
   } else {
     const int64_t span = std::max(kTileCols, ((int64_t{1} << 31) - 1) / (2 * c.K));
     const int64_t grid = ((int64_t{1} << 22) - 1) / cut(c.M, 64) * 64;
-    const int64_t most = std::min(c.linear && !c.f32 ? std::min(span, grid) : grid, int64_t{1} << 25) / kTileCols * kTileCols;
+    int64_t most = std::min(c.linear && !c.f32 ? std::min(span, grid) : grid, int64_t{1} << 25);
+    if (f.pad) most = std::min(most, std::max(16 * kTileCols, (int64_t{1} << 27) / f.K));   // 256 MiB of W
+    most = most / kTileCols * kTileCols;
     f.piece = up(cut(c.V, cut(c.V, most)), kTileCols);
     f.slots = cut(c.V, c.f32 ? 64 : 128) + cut(c.V, f.piece);
   }
-  f.join = 0;
   f.part = up(std::max(joined, kTicketBytes), kAlign);
   f.logit = f.part + up(f.slots * c.M * 8, kAlign);
   f.logits = f.logit + up(c.M * 4, kAlign);
-  f.total = f.logits + (f.rows ? c.M * up(f.piece, 4) * 4 : 0);
+  f.x = f.logits + (f.rows ? up(c.M * up(f.piece, 4) * 4, kAlign) : 0);
+  f.w = f.x + (f.pad && c.K != f.K ? up(c.M * f.K * 2, kAlign) : 0);
+  f.total = f.w + (f.pad ? up(std::min(f.piece, c.V), 64) * f.K * 2 : 0);
   return f;
 }
 
@@ -98,21 +148,25 @@ int64_t columns_of(const LinChoice& h) {
 // P has zero rows up to a multiple of 64 tokens, and X^T is kept transposed with as
 // many zero columns, those of ignored tokens among them: so the products over tokens
 // run on the tiled kernels whatever M is, what lies in X at an ignored token (a
-// padded batch's rest) does not reach dW, and only one of their operands (P, or
-// with a [K, V] weight none but P again) goes through the transposing LDS read.
-// The vocabulary's last V % 64 columns are a piece of their own, since dX's product
-// sums over columns and the tiled kernels take whole stages of them.
+// padded batch's rest) does not reach dW, and only one of their operands goes
+// through the transposing LDS read.
+// The product over columns, dX's, takes whole stages of them on the tiled kernels, so
+// the vocabulary's last V % 64 columns are a piece of their own, with a padded copy
+// of their part of W; where X and W are padded anyway every piece is copied.
 //
 // Pieces: 2^28 elements of P (512 MiB in bf16), so that dX is not read and
 // written again often: with 8192 x 4096 tokens every further piece costs 268 MB.
+constexpr int64_t kPadLeastBwd = 256;
 struct Backward {
-  int64_t rows = 0, piece = 0, whole = 0;   // tokens of P; its columns; the vocabulary in pieces of them
-  bool split_tail = false, keeps = false;   // a last piece of V - whole columns; dX is summed in the workspace
-  int64_t xt = 0, p = 0, acc = 0, total = 0;
+  int64_t rows = 0, piece = 0, whole = 0, K = 0;   // tokens of P; its columns; the vocabulary in pieces of them; K as multiplied
+  bool pad = false, tail = false;                  // every piece of W is copied; the last V - whole columns are
+  bool keeps = false;                              // dX is summed in the workspace
+  int64_t xt = 0, p = 0, acc = 0, x = 0, w = 0, total = 0;
 };
 
-LinGemm dx_product(const CeSizes& c, int64_t n) {
+LinGemm dx_product(const CeSizes& c, int64_t n, bool copied) {
   LinGemm p;
+  p.groups = copied;
   p.M = c.M;
   p.N = c.K;
   p.K = n;
@@ -122,6 +176,7 @@ LinGemm dx_product(const CeSizes& c, int64_t n) {
 }
 LinGemm dw_product(const CeSizes& c, int64_t n, int64_t rows) {
   LinGemm p;
+  p.groups = !c.f32;   // P's rows go on to a multiple of 64
   p.M = c.linear ? n : c.K;
   p.N = c.linear ? c.K : n;
   p.K = rows;
@@ -130,12 +185,13 @@ LinGemm dw_product(const CeSizes& c, int64_t n, int64_t rows) {
   return p;
 }
 
-// f(first column, columns) of each piece, until one fails.
+// f(first column, columns, columns as multiplied) of each piece, until one fails.
 template <typename F>
 hipError_t each_piece(const CeSizes& c, const Backward& b, F&& f) {
   for (int64_t n = 0; n < c.V;) {
     const int64_t left = n < b.whole ? b.whole - n : c.V - n, cols = std::min(left, b.piece);
-    const hipError_t e = f(n, cols);
+    const bool copied = b.pad || (b.tail && n >= b.whole);
+    const hipError_t e = f(n, cols, copied ? up(cols, 64) : cols);
     if (e != hipSuccess) return e;
     n += cols;
   }
@@ -145,37 +201,35 @@ hipError_t each_piece(const CeSizes& c, const Backward& b, F&& f) {
 Backward backward_plan(const CeSizes& c, const CeBackward& b) {
   Backward q;
   q.rows = up(c.M, 64);
-  q.split_tail = !c.f32 && c.K % 8 == 0 && c.V % 64 && c.V > 64;
-  q.whole = q.split_tail ? c.V / 64 * 64 : c.V;
+  q.pad = padded(c, kPadLeastBwd);
+  q.tail = !q.pad && !c.f32 && c.K % 32 == 0 && c.V % 64 && c.V > 64;
+  q.whole = q.tail ? c.V / 64 * 64 : c.V;
+  q.K = q.pad ? up(c.K, 64) : c.K;
   const int64_t grid = ((int64_t{1} << 22) - 1) / std::max<int64_t>(1, std::max(cut(c.M, 64), cut(c.K, 64))) * 64;
   int64_t most = b.piece > 0 ? std::max<int64_t>(64, b.piece / 64 * 64)
                              : std::max<int64_t>(8192, (int64_t{1} << 28) / std::max<int64_t>(1, q.rows));
   most = std::max<int64_t>(64, std::min(std::min(most, grid), int64_t{1} << 25) / 64 * 64);
   const int64_t pieces = cut(q.whole, most);
   q.piece = up(cut(q.whole, pieces), 64);
-  q.keeps = b.dX && !c.f32 && !b.dx_f32 && (pieces > 1 || q.split_tail);
+  q.keeps = b.dX && !c.f32 && !b.dx_f32 && (pieces > 1 || q.tail);
   const int64_t es = c.f32 ? 4 : 2;
   int64_t joined = kTicketBytes;
   if (c.M > 0)
-    (void)each_piece(c, q, [&](int64_t, int64_t n) {
-      joined = std::max(joined, lin_gemm_ws(logits_product(c, kModeProb, n)));
-      if (b.dX) joined = std::max(joined, lin_gemm_ws(dx_product(c, n)));
-      if (b.dW) joined = std::max(joined, lin_gemm_ws(dw_product(c, n, q.rows)));
+    (void)each_piece(c, q, [&](int64_t, int64_t cols, int64_t wide) {
+      LinGemm z = logits_product(c, kModeProb, wide);
+      z.K = q.K;
+      joined = std::max(joined, lin_gemm_ws(z));
+      if (b.dX) joined = std::max(joined, lin_gemm_ws(dx_product(c, wide, cols != wide || q.pad)));
+      if (b.dW) joined = std::max(joined, lin_gemm_ws(dw_product(c, cols, q.rows)));
       return hipSuccess;
     });
   q.xt = up(joined, kAlign);
   q.p = q.xt + (b.dW ? up(c.K * q.rows * es, kAlign) : 0);
   q.acc = q.p + up(q.rows * q.piece * es, kAlign);
-  q.total = q.acc + (q.keeps ? c.M * c.K * 4 : 0);
+  q.x = q.acc + (q.keeps ? up(c.M * c.K * 4, kAlign) : 0);
+  q.w = q.x + (q.K != c.K ? up(c.M * q.K * 2, kAlign) : 0);
+  q.total = q.w + (q.pad ? q.piece * q.K * 2 : q.tail ? 64 * c.K * 2 : 0);
   return q;
-}
-
-template <typename F>
-hipError_t timed(hipStream_t s, int kind, double work, F&& f) {
-  hipEvent_t t0 = timing_begin(s);
-  const hipError_t e = f();
-  if (e == hipSuccess) timing_end(t0, s, kind, work);
-  return e;
 }
 
 }  // namespace
@@ -195,15 +249,28 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
   char *base = static_cast<char *>(ws);
   float *part = reinterpret_cast<float *>(base + f.part), *logit = reinterpret_cast<float *>(base + f.logit);
   int64_t slots = 0;
+  hipError_t e;
+  if (f.w != f.x && (e = pad(pad_x(c, o, f.K, base + f.x), s)) != hipSuccess) return e;
   for (int64_t n = 0; n < c.V; n += f.piece) {
+    const int64_t cols = std::min(f.piece, c.V - n), cols_pad = up(cols, 64);
     CeGemm p;
-    static_cast<LinGemm&>(p) = logits_product(c, f.rows ? kModeOne : kModeStats, std::min(f.piece, c.V - n));
+    static_cast<LinGemm&>(p) = logits_product(c, f.rows ? kModeOne : kModeStats, cols);
     p.a = o.X;
     p.lda = o.X_ld;
     p.w = weight_at(c, o.W, o.W_ld, n);
     p.ldw = o.W_ld;
-    const double flops = 2.0 * static_cast<double>(c.M) * static_cast<double>(p.N) * static_cast<double>(c.K);
-    hipError_t e;
+    if (f.pad) {
+      if ((e = pad(pad_weight(c, o, n, cols, cols_pad, f.K, base + f.w), s)) != hipSuccess) return e;
+      p.w = base + f.w;
+      p.ldw = c.linear ? f.K : cols_pad;
+      p.K = f.K;
+      p.groups = 1;
+      if (f.w != f.x) {
+        p.a = base + f.x;
+        p.lda = f.K;
+      }
+    }
+    const double flops = 2.0 * static_cast<double>(c.M) * static_cast<double>(cols) * static_cast<double>(c.K);
     if (f.rows) {
       p.c = base + f.logits;
       p.ldc = up(f.piece, 4);
@@ -224,6 +291,7 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
     } else {
       p.targets = o.targets;
       p.begin = o.begin + n;
+      p.cols = cols;
       p.part = part;
       p.slot0 = slots;
       p.logit = logit;
@@ -278,16 +346,27 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
     e = zero_tickets_launch(reinterpret_cast<uint32_t *>(base), s);
   }
   if (e != hipSuccess) return e;
-  e = each_piece(c, q, [&](int64_t n, int64_t cols) {
+  if (c.M > 0 && q.K != c.K && (e = pad(pad_x(c, o, q.K, base + q.x), s)) != hipSuccess) return e;
+  e = each_piece(c, q, [&](int64_t n, int64_t cols, int64_t wide) {
     const double flops = 2.0 * MK * static_cast<double>(cols);
+    const bool copied = q.pad || cols != wide;
+    const void *W = weight_at(c, o.W, o.W_ld, n);
+    int64_t W_ld = o.W_ld;
     hipError_t r = hipSuccess;
+    if (c.M > 0 && copied) {
+      if ((r = pad(pad_weight(c, o, n, cols, wide, q.K, base + q.w), s)) != hipSuccess) return r;
+      W = base + q.w;
+      W_ld = c.linear ? q.K : wide;
+    }
     if (c.M > 0) {
       CeGemm p;
-      static_cast<LinGemm&>(p) = logits_product(c, kModeProb, cols);
-      p.a = o.X;
-      p.lda = o.X_ld;
-      p.w = weight_at(c, o.W, o.W_ld, n);
-      p.ldw = o.W_ld;
+      static_cast<LinGemm&>(p) = logits_product(c, kModeProb, wide);
+      p.a = q.K != c.K ? base + q.x : o.X;
+      p.lda = q.K != c.K ? q.K : o.X_ld;
+      p.K = q.K;
+      p.w = W;
+      p.ldw = W_ld;
+      p.cols = cols;
       p.c = base + q.p;
       p.ldc = q.piece;
       p.c_f32 = c.f32;
@@ -305,11 +384,11 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
       if (r != hipSuccess) return r;
     }
     if (b.dX && c.M > 0) {
-      LinGemm p = dx_product(c, cols);
+      LinGemm p = dx_product(c, wide, copied);
       p.a = base + q.p;
       p.lda = q.piece;
-      p.w = weight_at(c, o.W, o.W_ld, n);
-      p.ldw = o.W_ld;
+      p.w = W;
+      p.ldw = W_ld;
       p.c = q.keeps ? base + q.acc : static_cast<char *>(b.dX);
       p.ldc = q.keeps ? c.K : b.dX_ld;
       p.c_f32 = q.keeps || b.dx_f32;
@@ -328,8 +407,9 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
       p.ldc = b.dW_ld;
       p.c_f32 = b.dw_f32;
       p.acc_c = b.accumulate;
+      if (c.M == 0) p.w_t = 0;   // a sum of nothing, on the general kernel
       r = timed(s, TP_KERNEL_GEMM_WGRAD, flops, [&] {
-        if (!c.linear) return lin_gemm_launch(p, s, ws, q.xt);
+        if (!p.w_t) return lin_gemm_launch(p, s, ws, q.xt);
         const LinChoice h = lin_choose(&p, ws, q.xt);
         return h.tiles ? lin_tiles_wgrad(p, h.tile, s) : lin_staged_launch(p, h.staged, s);
       });

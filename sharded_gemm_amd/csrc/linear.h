@@ -48,22 +48,24 @@ struct LinGemm {
   int32_t act = 0;      // TP_ACT_*
   int32_t c_f32 = 0;    // c holds fp32 (always with f32)
   int32_t acc_c = 0;
+  int32_t groups = 0;   // row-contiguous operands can be read to whole groups of 8 (a row of the output at least)
   // Several workgroups to a tile: their partials and arrival counts.
   float *join = nullptr;
   uint32_t *tickets = nullptr;
 };
 
-// A product whose columns are logits, those of the ids begin .. begin + N - 1.
+// A product whose columns are logits: the first `cols` of them those of the ids from
+// `begin` on, the rest (where the weight was padded) nothing.
 struct CeGemm : LinGemm {
   const int64_t *targets = nullptr;   // [M]
-  int64_t begin = 0;
+  int64_t begin = 0, cols = 0;
   // kModeStats: part[(slot0 + column tile) * M + m] <- {maximum, sum} of that tile's logits of row m (ce_dev.h);
   // logit[m] <- the target's logit, where it is one of these columns.
   float *part = nullptr;
   int64_t slot0 = 0;
   float *logit = nullptr;
-  // kModeProb: c[m, n] <- (g + h) exp(z - lse) - (id n is the target) g, 0 in the rows of ignored targets and
-  // in the rows M .. pad_rows - 1.  g = g[m * g_step], h likewise or 0.
+  // kModeProb: c[m, n] <- (g + h) exp(z - lse) - (id n is the target) g, 0 in the rows of ignored targets, in
+  // the rows M .. pad_rows - 1 and in the columns from `cols` on.  g = g[m * g_step], h likewise or 0.
   const float *lse = nullptr, *g = nullptr, *h = nullptr;
   int64_t g_step = 0, h_step = 0, ignore = 0, pad_rows = 0;
 };

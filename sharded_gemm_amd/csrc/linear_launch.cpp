@@ -21,7 +21,7 @@ bool tiles_ok(const LinGemm& p) {
   if (p.f32 || p.K <= 0 || p.K % 32) return false;
   if (!aligned(p.a, p.lda, 2, 8) || !aligned(p.a2, p.lda, 2, 8) || !aligned(p.w, p.ldw, 2, 8) || !aligned(p.w2, p.ldw, 2, 8))
     return false;
-  return (!p.a_t || p.M % 8 == 0) && (p.w_t || p.N % 8 == 0);
+  return p.groups || ((!p.a_t || p.M % 8 == 0) && (p.w_t || p.N % 8 == 0));
 }
 
 constexpr int64_t kCUs = 256;
@@ -124,7 +124,7 @@ TilePick pick(const LinGemm& p) {
   };
   const int64_t a_span = (p.a_t ? p.K : p.M) * p.lda * 2, w_span = (p.w_t ? p.N : p.K) * p.ldw * 2;
   const bool pps = k64 && a_span < (int64_t{1} << 31) && w_span < (int64_t{1} << 31);
-  const double c256 = !p.a_t && pps ? cost(256, 256, 1.0) : 1e300, c192 = !dual && pps ? cost(256, 192, 0.95) : 1e300;
+  const double c256 = (!p.a_t || p.w_t) && pps ? cost(256, 256, 1.0) : 1e300, c192 = !dual && pps ? cost(256, 192, 0.95) : 1e300;
   const double c128w = pps ? cost(256, 128, 0.85) : 1e300, c128 = cost(128, 128, 0.7);
   const double best = std::min(std::min(c256, c192), std::min(c128w, c128));
   return {c256 == best ? kTile256 : c192 == best ? kTile192 : c128w == best ? kTile128w : kTile128, 1};

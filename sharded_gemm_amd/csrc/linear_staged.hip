@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_ker
     const int wcols = MODE == kModeDual ? WN / 2 : WN;
     return n0 + wn * wcols + j * 16 + 4 * (lane >> 4);
   };
-  if constexpr (MODE == kModeStats) ce::stats<BM, WAVES_N, THREADS>(p, smem, acc, m0, p.slot0 + n0 / BN, wn, rm, cn);
+  if constexpr (MODE == kModeStats) ce::stats<BM, WAVES_N, THREADS>(p, smem, acc, m0, p.slot0 + n0 / BN, wn, n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<std::conditional_t<sizeof(T) == 4, float, uint16_t>>(p, acc, rm, cn);
   else if constexpr (sizeof(T) == 4) epilogue<float, MODE>(p, c, acc, rm, cn);
   else epilogue<uint16_t, MODE>(p, c, acc, rm, cn);
@@ -359,7 +359,9 @@ hipError_t dispatch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
       if (akc) return wkc ? launch<T, true, true, kModeProb>(p, h, s) : launch<T, true, false, kModeProb>(p, h, s);
       break;
   }
-  if (p.mode == kModeOne && !akc) return wkc ? launch<T, false, true, kModeOne>(p, h, s) : launch<T, false, false, kModeOne>(p, h, s);
+  if (p.mode == kModeOne && !akc && !wkc) return launch<T, false, false, kModeOne>(p, h, s);
+  if constexpr (sizeof(T) == 4)   // (bf16: always on the tiled kernels)
+    if (p.mode == kModeOne && !akc) return launch<T, false, true, kModeOne>(p, h, s);
   return hipErrorInvalidValue;
 }
 

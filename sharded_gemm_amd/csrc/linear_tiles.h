@@ -39,6 +39,10 @@ struct WTile {
   }
 };
 
+// Rows that an operand's groups can be read to: whole groups of 8 of a row-contiguous one.
+template <bool KC>
+__device__ __forceinline__ int64_t rows_of(int64_t n) { return KC ? n : (n + 7) / 8 * 8; }
+
 // What a workgroup computes: its tile, and its part of K.
 struct Place {
   int m0, n0;
@@ -85,10 +89,10 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(Lin
   const uint16_t *A2 = static_cast<const uint16_t *>(p.a2);
   int64_t a_src[C::A_PW], w_src[C::W_PW];
 #pragma unroll
-  for (int q = 0; q < C::A_PW; ++q) a_src[q] = TA::src(wave * C::A_PW + q, lane, pl.m0, p.M, p.lda);
+  for (int q = 0; q < C::A_PW; ++q) a_src[q] = TA::src(wave * C::A_PW + q, lane, pl.m0, rows_of<!AT>(p.M), p.lda);
 #pragma unroll
   for (int q = 0; q < C::W_PW; ++q)
-    w_src[q] = WO::src(min(wave + q * C::NW, TW::PIECES - 1), lane, pl.n0, p.N, p.ldw);
+    w_src[q] = WO::src(min(wave + q * C::NW, TW::PIECES - 1), lane, pl.n0, rows_of<WT>(p.N), p.ldw);
   const int64_t a_step = TA::step(p.lda), w_step = TW::step(p.ldw);
   const int half = static_cast<int>(p.K / BK);
   auto issue = [&](int st, int slot) {
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(Lin
     return pl.n0 + wn * (MODE == kModeDual ? C::WN / 2 : C::WN) + j * 16 + 4 * (lane >> 4);
   };
   if constexpr (MODE == kModeStats)
-    ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, rm, cn);
+    ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, pl.n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
   else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
 }
@@ -172,13 +176,13 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
   const void *w_base = pl.second || WO::second((wave & 3) * W_PW) ? p.w2 : p.w;
   const int half = static_cast<int>(p.K / BK);
   auto dma_a = [&](int q, int st, int slot_st) {
-    const uint32_t src = static_cast<uint32_t>(TA::src((wave & 3) * A_PW + q, lane, pl.m0, p.M, p.lda) * 2);
+    const uint32_t src = static_cast<uint32_t>(TA::src((wave & 3) * A_PW + q, lane, pl.m0, rows_of<!AT>(p.M), p.lda) * 2);
     const bool far = MODE == kModeCat && st >= half;
     lds_dma16_s(far ? p.a2 : a_base, src + (far ? st - half : st) * step,
                 lds0 + (slot_st % SA) * TA::BYTES + ((wave & 3) * A_PW + q) * 1024);
   };
   auto dma_w = [&](int q, int st, int slot_st) {
-    const uint32_t src = static_cast<uint32_t>(WO::src((wave & 3) * W_PW + q, lane, pl.n0, p.N, p.ldw) * 2);
+    const uint32_t src = static_cast<uint32_t>(WO::src((wave & 3) * W_PW + q, lane, pl.n0, rows_of<WT>(p.N), p.ldw) * 2);
     const bool far = MODE == kModeCat && st >= half;
     lds_dma16_s(far ? p.w2 : w_base, src + (far ? st - half : st) * step,
                 lds0 + W_BASE + (slot_st % SW) * TW::BYTES + ((wave & 3) * W_PW + q) * 1024);
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
     return pl.n0 + wn * (MODE == kModeDual ? C::WN / 2 : C::WN) + j * 16 + 4 * (lane >> 4);
   };
   if constexpr (MODE == kModeStats)
-    ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, rm, cn);
+    ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, pl.n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
   else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
 }
@@ -233,7 +237,7 @@ hipError_t dispatch_tiles(const LinGemm& p, const TilePick& t, hipStream_t s) {
   constexpr int WGM = AT ? 4 : 2;
   switch (t.tile) {
     case kTile256:
-      if constexpr (!AT) return launch_lin_pps<256, 256, MODE, AT, WT>(p, s);
+      if constexpr (!AT || WT) return launch_lin_pps<256, 256, MODE, AT, WT, WGM>(p, s);
       break;
     case kTile192:
       if constexpr (!dual) return launch_lin_pps<256, 192, MODE, AT, WT, WGM>(p, s);

@@ -70,6 +70,7 @@ void product(const LinGemm& p, int64_t align, int64_t bm, int64_t bn) {
   }
   const CeGemm& q = static_cast<const CeGemm&>(p);
   vec(q.targets, q.M, 8, "targets");
+  check(q.cols > 0 && q.cols <= q.N, "columns");
   if (p.mode == kModeStats) {
     const int64_t tiles = (q.N + bn - 1) / bn;
     check(q.slot0 >= 0, "slots");
@@ -101,7 +102,9 @@ hipError_t tiles(const LinGemm& p, const TilePick& t) {
   check(!p.f32 && p.lda % 8 == 0 && p.ldw % 8 == 0, "tiled: strides");
   check(p.K > 0 && p.K % 32 == 0, "tiled: K");
   if (t.tile != kTile128 && t.tile != kTile64k32) check(p.K % 64 == 0, "tiled: K of a 64-wide stage");
-  check((!p.a_t || p.M % 8 == 0) && (p.w_t || p.N % 8 == 0), "tiled: whole column groups");
+  check(p.groups || ((!p.a_t || p.M % 8 == 0) && (p.w_t || p.N % 8 == 0)), "tiled: whole column groups");
+  if (p.a_t) need(p.a, p.K, (p.M + 7) / 8 * 8, p.lda, 2, "A's groups", 16);
+  if (!p.w_t) need(p.w, p.K, (p.N + 7) / 8 * 8, p.ldw, 2, "W's groups", 16);
   check(!(t.tile == kTile256 && p.a_t && !p.w_t), "tiled: no such instance");
   if (t.tile == kTile256 || t.tile == kTile192 || t.tile == kTile128w)
     check((p.a_t ? p.K : p.M) * p.lda * 2 < (int64_t{1} << 31) && (p.w_t ? p.N : p.K) * p.ldw * 2 < (int64_t{1} << 31),
@@ -147,7 +150,7 @@ hipError_t lin_staged_launch(const LinGemm& p, const StagedShape& h, hipStream_t
   product(p, 0, h.edge, h.edge);
   check(h.edge == 64 || h.splits == 1, "general: only the small tile is split");
   check(h.tiles == lin_tiles_count(p, h.edge, h.edge), "general: tiles");
-  check(!p.a_t || p.mode == kModeOne, "general: no such instance");
+  check(!p.a_t || (p.mode == kModeOne && (p.f32 || !p.w_t)), "general: no such instance");
   grid(h.tiles, h.splits, h.edge == 128 ? 512 : 256);
   split(p, h.splits, h.tiles, 64 * 64);
   seen_product(p.f32 ? "f32 " : "bf16 ", "general", h.edge, p, h.splits);
@@ -219,6 +222,14 @@ hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t) {
   vec(p.targets, p.M, 8, "targets");
   if (p.tickets) vec(p.tickets, kMaxTickets, 4, "tickets");
   seen("transpose");
+  return hipSuccess;
+}
+hipError_t ce_pad_launch(const CePad& p, hipStream_t) {
+  check(p.cols % 8 == 0 && p.rows >= p.m && p.cols >= p.n && p.m > 0 && p.n > 0, "pad: sizes");
+  grid((p.rows * (p.cols / 8) + 255) / 256, 1, 256);
+  need(p.from, p.m, p.n, p.ld, 2, "padded from");
+  vec(p.to, p.rows * p.cols, 2, "padded copy", 16);
+  seen("pad");
   return hipSuccess;
 }
 hipError_t ce_round_launch(const float *from, void *out, int64_t M, int64_t K, int64_t ld, hipStream_t) {
