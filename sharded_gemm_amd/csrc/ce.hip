@@ -95,16 +95,7 @@ __global__ void __launch_bounds__(kThreads) ce_join_kernel(CeJoin p) {
     __syncthreads();
   }
   if (q || m >= p.M) return;
-  const int64_t id = p.targets[m];
-  const float logit = column_of(id, p.begin, p.V) >= 0 ? p.logit[m] : minus_inf();
-  if (p.stats) {
-    p.stats[m] = a[0];
-    p.stats[p.M + m] = a[1] * exp2_(rest_of(a[0]));   // against the maximum itself
-    p.stats[2 * p.M + m] = logit;
-  }
-  const float lse = lse_of(a);
-  if (p.lse) p.lse[m] = lse;
-  if (p.loss) p.loss[m] = id == p.ignore ? 0.0f : lse - logit;
+  finish(p, m, a, p.logit[m]);
 }
 
 // Pieces' statistics: {max, sum of e^(z - max) (of e^z where max is not finite), target's logit or -inf}.

@@ -10,6 +10,7 @@
 // makes it NaN, and minus infinity everywhere leaves 0.
 #pragma once
 
+#include "ce.h"
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -53,6 +54,20 @@ __device__ __forceinline__ float lse_of(f32x2 a) {
 __device__ __forceinline__ int column_of(int64_t t, int64_t begin, int64_t n) {
   const uint64_t c = static_cast<uint64_t>(t) - static_cast<uint64_t>(begin);
   return c < static_cast<uint64_t>(n) ? static_cast<int>(c) : -1;
+}
+
+// A row's outputs from the set of all its logits and its target's (where the piece holds it).
+__device__ __forceinline__ void finish(const CeJoin& p, int64_t m, f32x2 a, float logit) {
+  const int64_t id = p.targets[m];
+  if (column_of(id, p.begin, p.V) < 0) logit = minus_inf();
+  if (p.stats) {
+    p.stats[m] = a[0];
+    p.stats[p.M + m] = a[1] * exp2_(rest_of(a[0]));   // against the maximum itself
+    p.stats[2 * p.M + m] = logit;
+  }
+  const float lse = lse_of(a);
+  if (p.lse) p.lse[m] = lse;
+  if (p.loss) p.loss[m] = id == p.ignore ? 0.0f : lse - logit;
 }
 
 // kModeStats: the statistics of a tile's rows.  Four lanes and WAVES_N waves share a

@@ -34,11 +34,14 @@ const void *weight_at(const CeSizes& c, const void *W, int64_t ld, int64_t n) {
 
 // Whether X and W are copied into the workspace, K padded to whole stages and W's
 // rows aligned, so that the tiled bf16 kernels take sizes that are no multiple of
-// anything.  The copy moves four bytes for each element of W; the general kernel
-// runs at 300 to 500 TFLOP/s where the tiled ones reach 1300: from some hundred
-// tokens on the copy pays.  (MI355X, COPYTIMES.)
-bool padded(const CeSizes& c, int64_t least) {
-  return !c.f32 && c.M >= least && (c.K % 32 || (c.K % 64 && c.K >= 256) || (!c.linear && c.V % 8));
+// anything.  The copy moves four bytes for each element of W, so it pays from some
+// number of tokens on; later where rows are aligned anyway and only K's last stage is
+// not whole.  MI355X, general kernel : padded (us), 4095 -> 32001 forward at 256
+// tokens 138 : 168, 512 251 : 191, 1024 445 : 292; backward at 65 tokens 372 : 414, 129 468 :
+// 452, 512 893 : 701; aligned, 1000 -> 8000 forward at 512 25 : 33, backward 69 : 70, at 1024 100 : 96.
+bool padded(const CeSizes& c, bool backward) {
+  if (c.f32 || (c.K % 32 == 0 && (c.K % 64 == 0 || c.K < 256) && (c.linear || c.V % 8 == 0))) return false;
+  return c.M >= (c.K % 8 == 0 && (c.linear || c.V % 8 == 0) ? 1024 : backward ? 128 : 512);
 }
 // Columns from n on of W, `cols` of them, as [columns][K] or [K][columns], padded.
 CePad pad_weight(const CeSizes& c, const CeOperands& o, int64_t n, int64_t cols, int64_t cols_pad, int64_t K_pad, void *to) {
@@ -74,18 +77,23 @@ hipError_t pad(const CePad& p, hipStream_t s) {
 }
 
 // ---- forward ---------------------------------------------------------------------
-// Few rows: the few-row kernel leaves the logits, M of them a column (64 at most,
-// where a column of the weight has K), and a pass of its own reduces them; 2^18
-// columns at a time.
-// Otherwise a product whose epilogue reduces each tile: in one launch, unless the
-// weight's bytes pass the 2^31 up to which the ping-pong kernels' offsets reach,
-// or its tiles the grid; then in even pieces of whole tiles.
+// A product whose epilogue reduces each tile: in one launch, unless the weight's bytes
+// pass the 2^31 up to which the ping-pong kernels' offsets reach, or its tiles the
+// grid; then in even pieces of whole tiles.
+// Up to 64 rows run in 64-column tiles of 32 or 64 rows, three or more of which share a
+// CU: bound by the weight's bytes, whether there is one row or 32.  (MI355X, 16 rows,
+// us, against the few-row kernel and a pass over its logits: 768 -> 32000 13.8 : 23.7, 4096
+// -> 131072 175.8 : 257; one row 13.0 : 21.0, 172.9 : 172.5, but 4096 -> 65536 103 : 92.  32 rows
+// a tile and four stages: 64 rows and three took 14.7 and 112 at 4096 -> 65536.)
+// fp32 has no such tiles; up to 16 rows of it take the few-row kernel, which leaves
+// the logits (M of them a column, where a column of the weight has K), and a pass of
+// its own reduces them, 2^18 columns at a time: one row of 1024 -> 40000 39 us, the
+// general kernel 63.
 constexpr int64_t kLogitCols = int64_t{1} << 18;
 constexpr int64_t kTileCols = 768;   // a multiple of every tile's columns
 
-constexpr int64_t kPadLeast = 512;   // tokens from which on X and W are padded
 struct Forward {
-  bool rows = false, small = false, pad = false;   // few rows; tiles of 64 columns may be picked; padded copies
+  bool rows = false, small = false, pad = false;   // the few-row kernel; tiles of 64 columns; padded copies
   int64_t piece = 0, slots = 0, K = 0;             // columns of a launch; pairs of a row at most; K as multiplied
   int64_t part = 0, logit = 0, logits = 0, x = 0, w = 0, total = 0;   // offsets; total: bytes
 };
@@ -94,9 +102,9 @@ Forward forward_plan(const CeSizes& c) {
   Forward f;
   if (c.M <= 0) return f;
   const LinGemm one = logits_product(c, kModeOne, std::min(c.V, kLogitCols)), st = logits_product(c, kModeStats, c.V);
-  f.rows = lin_takes_rows(one);
-  f.small = lin_tiles_count(st, 128, 128) < 256;
-  f.pad = !f.rows && padded(c, kPadLeast);
+  f.rows = c.f32 && lin_takes_rows(one) && c.M <= 16;
+  f.small = c.M <= 64 || lin_tiles_count(st, 128, 128) < 256;
+  f.pad = !f.rows && padded(c, false);
   f.K = f.pad ? up(c.K, 64) : c.K;
   int64_t joined = 0;
   if (f.rows) {
@@ -105,7 +113,7 @@ Forward forward_plan(const CeSizes& c) {
     joined = lin_gemm_ws(one);
     if (c.V % f.piece) joined = std::max(joined, lin_gemm_ws(logits_product(c, kModeOne, c.V % f.piece)));
   } else if (f.small) {
-    f.piece = c.V;
+    f.piece = std::min(c.V, int64_t{1} << 24);   // (a launch's threads stay below 2^32)
     f.slots = cut(c.V, 64);
     LinGemm q = st;
     q.K = f.K;
@@ -156,7 +164,6 @@ int64_t columns_of(const LinChoice& h) {
 //
 // Pieces: 2^28 elements of P (512 MiB in bf16), so that dX is not read and
 // written again often: with 8192 x 4096 tokens every further piece costs 268 MB.
-constexpr int64_t kPadLeastBwd = 256;
 struct Backward {
   int64_t rows = 0, piece = 0, whole = 0, K = 0;   // tokens of P; its columns; the vocabulary in pieces of them; K as multiplied
   bool pad = false, tail = false;                  // every piece of W is copied; the last V - whole columns are
@@ -201,7 +208,7 @@ hipError_t each_piece(const CeSizes& c, const Backward& b, F&& f) {
 Backward backward_plan(const CeSizes& c, const CeBackward& b) {
   Backward q;
   q.rows = up(c.M, 64);
-  q.pad = padded(c, kPadLeastBwd);
+  q.pad = padded(c, true);
   q.tail = !q.pad && !c.f32 && c.K % 32 == 0 && c.V % 64 && c.V > 64;
   q.whole = q.tail ? c.V / 64 * 64 : c.V;
   q.K = q.pad ? up(c.K, 64) : c.K;
@@ -250,6 +257,17 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
   float *part = reinterpret_cast<float *>(base + f.part), *logit = reinterpret_cast<float *>(base + f.logit);
   int64_t slots = 0;
   hipError_t e;
+  CeJoin j;
+  j.part = part;
+  j.logit = logit;
+  j.targets = o.targets;
+  j.M = c.M;
+  j.V = c.V;
+  j.begin = o.begin;
+  j.ignore = o.ignore;
+  j.stats = stats;
+  j.loss = loss;
+  j.lse = lse;
   if (f.w != f.x && (e = pad(pad_x(c, o, f.K, base + f.x), s)) != hipSuccess) return e;
   for (int64_t n = 0; n < c.V; n += f.piece) {
     const int64_t cols = std::min(f.piece, c.V - n), cols_pad = up(cols, 64);
@@ -296,6 +314,8 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
       p.slot0 = slots;
       p.logit = logit;
       LinChoice h = lin_choose(&p, ws, f.small ? f.part : 0);
+      if (f.small && h.tiles && columns_of(h) > 64) h.tile = {p.K % 64 ? kTile64k32 : kTile64, 1};
+      if (f.small && h.tiles && c.M <= 32 && p.K % 64 == 0) h.tile.tile = kTile32;
       if (!f.small) {   // what the workspace was measured for
         if (h.tiles && columns_of(h) < 128) h.tile = {kTile128, 1};
         if (!h.tiles && !c.f32) h.staged = {128, 1, lin_tiles_count(p, 128, 128)};
@@ -305,18 +325,7 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
     }
     if (e != hipSuccess) return e;
   }
-  CeJoin j;
-  j.part = part;
-  j.logit = logit;
-  j.targets = o.targets;
-  j.M = c.M;
-  j.V = c.V;
   j.slots = slots;
-  j.begin = o.begin;
-  j.ignore = o.ignore;
-  j.stats = stats;
-  j.loss = loss;
-  j.lse = lse;
   return timed(s, TP_KERNEL_REDUCE, 8.0 * static_cast<double>(slots) * static_cast<double>(c.M), [&] { return ce_join_launch(j, s); });
 }
 

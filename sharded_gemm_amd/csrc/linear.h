@@ -116,7 +116,7 @@ hipError_t lin_staged_launch(const LinGemm& p, const StagedShape& h, hipStream_t
 
 // The tiled bf16 kernels: 16-byte aligned operands and rows, K a multiple of 32, a
 // row-contiguous operand of whole 8-column groups.
-enum Tile { kTile256, kTile192, kTile128w, kTile128, kTile64, kTile64short, kTile64k32 };
+enum Tile { kTile256, kTile192, kTile128w, kTile128, kTile64, kTile64short, kTile64k32, kTile32 };   // kTile32: kModeStats
 struct TilePick {
   int tile;     // Tile
   int splits;   // workgroups that split a tile's K

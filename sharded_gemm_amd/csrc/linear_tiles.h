@@ -246,6 +246,9 @@ hipError_t dispatch_tiles(const LinGemm& p, const TilePick& t, hipStream_t s) {
     case kTile128: return launch_ring<128, 128, 32, 8, MODE, AT, WT, 2, 4>(p, t.splits, s);
     case kTile64: return launch_ring<64, dual ? 128 : 64, 64, 3, MODE, AT, WT, 2, 2>(p, t.splits, s);
     case kTile64short: return launch_ring<64, dual ? 128 : 64, 64, 2, MODE, AT, WT, 2, 2>(p, t.splits, s);
+    case kTile32:
+      if constexpr (MODE == kModeStats) return launch_ring<32, 64, 64, 4, MODE, AT, WT, 2, 2>(p, t.splits, s);
+      break;
     case kTile64k32: return launch_ring<64, dual ? 128 : 64, 32, 4, MODE, AT, WT, 2, 2>(p, t.splits, s);
   }
   return hipErrorInvalidValue;

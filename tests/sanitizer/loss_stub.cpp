@@ -95,9 +95,9 @@ void split(const LinGemm& p, int splits, int64_t tiles, int64_t floats) {
 }
 
 hipError_t tiles(const LinGemm& p, const TilePick& t) {
-  static const char *names[] = {"tile256", "tile192", "tile128w", "tile128", "tile64", "tile64short", "tile64k32"};
-  static const int bm[] = {256, 256, 256, 128, 64, 64, 64}, bn[] = {256, 192, 128, 128, 64, 64, 64};
-  check(t.tile >= 0 && t.tile < 7, "tile");
+  static const char *names[] = {"tile256", "tile192", "tile128w", "tile128", "tile64", "tile64short", "tile64k32", "tile32"};
+  static const int bm[] = {256, 256, 256, 128, 64, 64, 64, 32}, bn[] = {256, 192, 128, 128, 64, 64, 64, 64};
+  check(t.tile >= 0 && t.tile < 8 && (t.tile != kTile32 || p.mode == kModeStats), "tile");
   product(p, 16, bm[t.tile], bn[t.tile]);
   check(!p.f32 && p.lda % 8 == 0 && p.ldw % 8 == 0, "tiled: strides");
   check(p.K > 0 && p.K % 32 == 0, "tiled: K");
@@ -112,7 +112,7 @@ hipError_t tiles(const LinGemm& p, const TilePick& t) {
   check(t.tile >= kTile64 || t.splits == 1, "tiled: only the small tiles are split");
   const int64_t n = lin_tiles_count(p, bm[t.tile], bn[t.tile]);
   grid(n, t.splits, 512);
-  split(p, t.splits, n, 64 * bn[t.tile]);
+  split(p, t.splits, n, bm[t.tile] * bn[t.tile]);
   seen_product("", names[t.tile], 0, p, t.splits);
   return hipSuccess;
 }
@@ -193,15 +193,20 @@ hipError_t ce_logits_launch(const CeLogits& p, hipStream_t) {
   seen("logits");
   return hipSuccess;
 }
-hipError_t ce_join_launch(const CeJoin& p, hipStream_t) {
+namespace {
+void joined(const CeJoin& p) {
   check(p.slots >= 1, "slots");
-  grid(p.M < 1024 ? p.M : (p.M + 15) / 16, 1, 256);
   vec(p.part, 2 * p.slots * p.M, 4, "pairs", 8);
   vec(p.logit, p.M, 4, "logits of targets");
   vec(p.targets, p.M, 8, "targets");
   if (p.stats) vec(p.stats, 3 * p.M, 4, "stats");
   if (p.loss) vec(p.loss, p.M, 4, "loss");
   if (p.lse) vec(p.lse, p.M, 4, "lse");
+}
+}  // namespace
+hipError_t ce_join_launch(const CeJoin& p, hipStream_t) {
+  grid(p.M < 1024 ? p.M : (p.M + 15) / 16, 1, 256);
+  joined(p);
   seen("join");
   return hipSuccess;
 }

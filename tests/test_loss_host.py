@@ -71,6 +71,8 @@ def own_kernels():
             names.add(f"{tile} {mode}")
             if tile.startswith("tile64"):
                 names.add(f"{tile} {mode} split")
+    for mode in ("stats a w", "stats a w^T"):
+        names |= {f"tile32 {mode}", f"tile32 {mode} split"}
     return names
 
 
