@@ -70,56 +70,76 @@ __device__ __forceinline__ void finish(const CeJoin& p, int64_t m, f32x2 a, floa
   if (p.loss) p.loss[m] = id == p.ignore ? 0.0f : lse - logit;
 }
 
+// The same lane's value in the other lane groups of 16 that share a row: f over x of lanes l, l ^ 16, l ^ 32, l ^ 48
+// (the swaps are vector instructions; a shuffle goes through LDS).
+template <typename F>
+__device__ __forceinline__ float over_groups(float x, F&& f) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+
 // kModeStats: the statistics of a tile's rows.  Four lanes and WAVES_N waves share a
 // row: they join through `lds` (WAVES_N * BM pairs, the operand tiles' memory), so
-// that a tile leaves one pair a row: per wave, the pairs of 4096 x 768 x 50000 would
-// be 26 MB.
+// that a tile leaves one pair a row.
 //
 // A lane's share is max, fma, exp2 and add for each of its elements; the columns' bounds
-// are only checked in tiles that reach past the last one (checked everywhere: TIMES).
+// are only checked in tiles that reach past the last one.  Nothing else of a tile's
+// time overlaps this one's, so latency counts: all targets are loaded at once, all rows
+// go through each step together, and lanes join without LDS.  TIMES.
 template <int BM, int WAVES_N, int THREADS, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t slot,
                                       int wn, bool whole, RM&& rm, CN&& cn) {
   f32x2 *rows = reinterpret_cast<f32x2 *>(lds);
   const int lane = threadIdx.x & 63, N = static_cast<int>(p.cols);
+  int64_t id[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) id[i] = p.targets[rm(i) < p.M ? rm(i) : p.M - 1];
   __syncthreads();   // the operand tiles have been read
-  auto row = [&](auto checked, int i) {
+  auto all = [&](auto checked) {
     constexpr bool CHECK = decltype(checked)::value != 0;
-    const int64_t m = rm(i);
-    const int t = m < p.M ? column_of(p.targets[m], p.begin, p.cols) : -1;
-    float top = minus_inf();
+    float top[TM], s[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      top[i] = minus_inf();
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!CHECK || static_cast<int>(cn(j)) + e < N) top[i] = fmaxf(top[i], acc[i][j][e]);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) top[i] = over_groups(top[i], [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const float to = shift_of(top[i]);
+      s[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!CHECK || static_cast<int>(cn(j)) + e < N) s[i] += exp2_(fmaf(acc[i][j][e], kLog2e, -to));
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      s[i] = over_groups(s[i], [](float x, float y) { return x + y; });
+      if (lane < 16) rows[wn * BM + (rm(i) - m0)] = f32x2{top[i], s[i]};
+    }
+  };
+  if (whole) all(lin::Const<0>{});
+  else all(lin::Const<1>{});
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int t = rm(i) < p.M ? column_of(id[i], p.begin, p.cols) : -1;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int n = static_cast<int>(cn(j));
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!CHECK || n + e < N) top = fmaxf(top, acc[i][j][e]);
-      if (static_cast<unsigned>(t - n) < 4u) {   // (t is a column or -1)
-        const float z01 = t - n == 0 ? acc[i][j][0] : acc[i][j][1], z23 = t - n == 2 ? acc[i][j][2] : acc[i][j][3];
-        p.logit[m] = t - n < 2 ? z01 : z23;
+      const int at = t - static_cast<int>(cn(j));
+      if (static_cast<unsigned>(at) < 4u) {   // (t is a column or -1)
+        const float z01 = at == 0 ? acc[i][j][0] : acc[i][j][1], z23 = at == 2 ? acc[i][j][2] : acc[i][j][3];
+        p.logit[rm(i)] = at < 2 ? z01 : z23;
       }
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float to = shift_of(top);
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = static_cast<int>(cn(j));
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!CHECK || n + e < N) s += exp2_(fmaf(acc[i][j][e], kLog2e, -to));
-    }
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lane < 16) rows[wn * BM + (m - m0)] = f32x2{top, s};
-  };
-  if (whole) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) row(lin::Const<0>{}, i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) row(lin::Const<1>{}, i);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < BM; i += THREADS) {
@@ -135,21 +155,24 @@ __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&
 // products that read it.
 template <typename T, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN], RM&& rm, CN&& cn) {
+  // Every row's loads before any store, which the compiler may not move them across.
+  int64_t id[TM];
+  float lses[TM], gs[TM], ghs[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = rm(i) < p.M ? rm(i) : p.M - 1;
+    id[i] = p.targets[m];
+    lses[i] = p.lse[m];
+    gs[i] = p.g ? p.g[m * p.g_step] : 1.0f;
+    ghs[i] = p.h ? gs[i] + p.h[m * p.h_step] : gs[i];
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int64_t m = rm(i);
     if (m >= p.pad_rows) continue;
-    float g = 0.0f, gh = 0.0f, lse = 0.0f;
-    int t = -1;
-    bool on = false;
-    if (m < p.M) {
-      const int64_t id = p.targets[m];
-      on = id != p.ignore;
-      t = column_of(id, p.begin, p.cols);
-      lse = p.lse[m];
-      g = p.g ? p.g[m * p.g_step] : 1.0f;
-      gh = p.h ? g + p.h[m * p.h_step] : g;
-    }
+    const float lse = lses[i], g = gs[i], gh = ghs[i];
+    const bool on = m < p.M && id[i] != p.ignore;
+    const int t = column_of(id[i], p.begin, p.cols);
     // (z - lse) log2 e: in bf16 as one fma, whose common error of 2^-24 |lse| is far below the rounding of
     // the result; in fp32 the difference first, which is exact where z and lse are close.
     const float far = -lse * kLog2e;
