@@ -93,7 +93,14 @@ struct CePad {
 };
 hipError_t ce_pad_launch(const CePad& p, hipStream_t s);
 
-// out [M, K] (bf16, stride ld) <- from [M, K] (fp32, contiguous).
-hipError_t ce_round_launch(const float *from, void *out, int64_t M, int64_t K, int64_t ld, hipStream_t s);
+// out [M, K] <- base + sum over s < slices, in order, of part[s]; part [slices][M][K] fp32,
+// base (optional) fp32, out bf16 or fp32 (then it may be base).
+struct CeSum {
+  const float *part = nullptr, *base = nullptr;
+  void *out = nullptr;
+  int64_t M = 0, K = 0, slices = 0, base_ld = 0, out_ld = 0;
+  int32_t out_f32 = 0;
+};
+hipError_t ce_sum_launch(const CeSum& p, hipStream_t s);
 
 }  // namespace tpshard

@@ -161,12 +161,22 @@ __global__ void __launch_bounds__(kThreads) ce_pad_kernel(CePad p) {
       left > 0 ? load16<uint16_t>(static_cast<const uint16_t *>(p.from) + r * p.ld + c, left) : u32x4{0, 0, 0, 0};
 }
 
-// ---- the rounded sum over pieces ------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) ce_round_kernel(const float *from, uint16_t *out, int64_t M, int64_t K, int64_t ld) {
-  const int64_t per = (K + 3) / 4, i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= M * per) return;
-  const int64_t m = i / per, k = i % per * 4;
-  store4<uint16_t>(out, m * ld + k, load4<float>(from, m * K + k, K - k), K - k);
+// ---- dX's sum over slices and pieces ------------------------------------------------
+__global__ void __launch_bounds__(kThreads) ce_sum_kernel(CeSum p) {
+  const int64_t per = (p.K + 3) / 4, i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= p.M * per) return;
+  const int64_t m = i / per, k = i % per * 4, left = p.K - k;
+  f32x4 v = p.base ? load4<float>(p.base, m * p.base_ld + k, left) : f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int B = 4;   // slices in flight
+  for (int64_t s = 0; s < p.slices; s += B) {
+    f32x4 x[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) x[b] = load4<float>(p.part, ((s + b) * p.M + m) * p.K + k, s + b < p.slices ? left : 0);
+#pragma unroll
+    for (int b = 0; b < B; ++b) v = v + x[b];
+  }
+  if (p.out_f32) store4<float>(p.out, m * p.out_ld + k, v, left);
+  else store4<uint16_t>(p.out, m * p.out_ld + k, v, left);
 }
 
 unsigned grid_of(int64_t n, int64_t by) { return static_cast<unsigned>((n + by - 1) / by); }
@@ -202,9 +212,8 @@ hipError_t ce_pad_launch(const CePad& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t ce_round_launch(const float *from, void *out, int64_t M, int64_t K, int64_t ld, hipStream_t s) {
-  hipLaunchKernelGGL(ce_round_kernel, dim3(grid_of(M * ((K + 3) / 4), kThreads)), dim3(kThreads), 0, s, from,
-                     static_cast<uint16_t *>(out), M, K, ld);
+hipError_t ce_sum_launch(const CeSum& p, hipStream_t s) {
+  hipLaunchKernelGGL(ce_sum_kernel, dim3(grid_of(p.M * ((p.K + 3) / 4), kThreads)), dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 

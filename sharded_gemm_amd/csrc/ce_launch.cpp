@@ -164,11 +164,15 @@ int64_t columns_of(const LinChoice& h) {
 //
 // Pieces: 2^28 elements of P (512 MiB in bf16), so that dX is not read and
 // written again often: with 8192 x 4096 tokens every further piece costs 268 MB.
+// The tail comes first, so that the last piece's sum can be dX itself.
+//
+// dX has few tiles where M K is not large, and a long sum: it is cut into slices of
+// columns, each a partial dX in fp32, that a pass of its own adds up (slices below).
 struct Backward {
   int64_t rows = 0, piece = 0, whole = 0, K = 0;   // tokens of P; its columns; the vocabulary in pieces of them; K as multiplied
   bool pad = false, tail = false;                  // every piece of W is copied; the last V - whole columns are
   bool keeps = false;                              // dX is summed in the workspace
-  int64_t xt = 0, p = 0, acc = 0, x = 0, w = 0, total = 0;
+  int64_t xt = 0, p = 0, acc = 0, x = 0, w = 0, part = 0, total = 0;
 };
 
 LinGemm dx_product(const CeSizes& c, int64_t n, bool copied) {
@@ -180,6 +184,11 @@ LinGemm dx_product(const CeSizes& c, int64_t n, bool copied) {
   p.f32 = c.f32;
   p.w_t = !c.linear;
   return p;
+}
+// Whether the ping-pong kernels' 32-bit offsets reach all of both operands.
+bool spans_ok(const LinGemm& p) {
+  const int64_t a = (p.a_t ? p.K : p.M) * p.lda * 2, w = (p.w_t ? p.N : p.K) * p.ldw * 2;
+  return a < (int64_t{1} << 31) && w < (int64_t{1} << 31);
 }
 LinGemm dw_product(const CeSizes& c, int64_t n, int64_t rows) {
   LinGemm p;
@@ -195,14 +204,51 @@ LinGemm dw_product(const CeSizes& c, int64_t n, int64_t rows) {
 // f(first column, columns, columns as multiplied) of each piece, until one fails.
 template <typename F>
 hipError_t each_piece(const CeSizes& c, const Backward& b, F&& f) {
-  for (int64_t n = 0; n < c.V;) {
-    const int64_t left = n < b.whole ? b.whole - n : c.V - n, cols = std::min(left, b.piece);
-    const bool copied = b.pad || (b.tail && n >= b.whole);
-    const hipError_t e = f(n, cols, copied ? up(cols, 64) : cols);
+  if (b.tail) {
+    const hipError_t e = f(b.whole, c.V - b.whole, int64_t{64});
     if (e != hipSuccess) return e;
-    n += cols;
+  }
+  for (int64_t n = 0; n < b.whole; n += b.piece) {
+    const int64_t cols = std::min(b.whole - n, b.piece);
+    const hipError_t e = f(n, cols, b.pad ? up(cols, 64) : cols);
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+// The slices that dX's product over n columns is cut into, and its tile, where that takes
+// at most 0.9 of the estimated time (us).  A stage of 64 columns takes a 256 x 256 tile
+// 1.45, smaller ones by their area and rate; a tile's fill and drain 4; every partial is
+// written and read at 4.5 TB/s.  Uncut, fewer than 256 tiles of 128 x 128 run as 64 x 64
+// ones, whose operands come through the caches, at 0.29 a stage for each of a CU's.
+// MI355X, the backward uncut : cut (us): 4096 x 768 x 50000 1369 : 995, 2048 x 2048 x 50000 1373 :
+// 1140, 512 x 4096 x 65000 1293 : 892, 128 x 4096 x 65536 645 : 598, 300 x 8192 x 10000 383 : 338.
+TilePick slices_of(const CeSizes& c, int64_t n) {
+  TilePick best{kTile256, 1};
+  if (c.f32 || n % 64 || c.M < 128) return best;
+  struct Kind {
+    int tile, cols;
+    double stage;
+  };
+  constexpr Kind kinds[] = {{kTile256, 256, 1.45}, {kTile128w, 128, 0.85}};
+  const int64_t stages = n / 64, small = cut(c.M, 64) * cut(c.K, 64);
+  const double each = static_cast<double>(c.M) * static_cast<double>(c.K) * 8.0 / 4.5e6;
+  double uncut = 1e300, least = 1e300;
+  for (const Kind& k : kinds) {
+    const int64_t tiles = cut(c.M, 256) * cut(c.K, k.cols);
+    for (int s = 1; s <= 16 && s * 8 <= stages; ++s) {
+      const double t = static_cast<double>(cut(tiles * s, 256)) * (static_cast<double>(cut(stages, s)) * k.stage + 4.0);
+      if (s == 1) {
+        uncut = std::min(uncut, t);
+      } else if (t + static_cast<double>(s) * each + 4.0 < least) {
+        least = t + static_cast<double>(s) * each + 4.0;
+        best = {k.tile, s};
+      }
+    }
+  }
+  if (cut(c.M, 128) * cut(c.K, 128) < 256) uncut = static_cast<double>(stages) * std::max(0.5, 0.29 * static_cast<double>(cut(small, 256)));
+  if (least > 0.9 * uncut) best.splits = 1;
+  return best;
 }
 
 Backward backward_plan(const CeSizes& c, const CeBackward& b) {
@@ -220,13 +266,14 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
   q.piece = up(cut(q.whole, pieces), 64);
   q.keeps = b.dX && !c.f32 && !b.dx_f32 && (pieces > 1 || q.tail);
   const int64_t es = c.f32 ? 4 : 2;
-  int64_t joined = kTicketBytes;
+  int64_t joined = kTicketBytes, slices = 0;
   if (c.M > 0)
     (void)each_piece(c, q, [&](int64_t, int64_t cols, int64_t wide) {
       LinGemm z = logits_product(c, kModeProb, wide);
       z.K = q.K;
       joined = std::max(joined, lin_gemm_ws(z));
       if (b.dX) joined = std::max(joined, lin_gemm_ws(dx_product(c, wide, cols != wide || q.pad)));
+      if (b.dX) slices = std::max<int64_t>(slices, slices_of(c, wide).splits);
       if (b.dW) joined = std::max(joined, lin_gemm_ws(dw_product(c, cols, q.rows)));
       return hipSuccess;
     });
@@ -235,7 +282,8 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
   q.acc = q.p + up(q.rows * q.piece * es, kAlign);
   q.x = q.acc + (q.keeps ? up(c.M * c.K * 4, kAlign) : 0);
   q.w = q.x + (q.K != c.K ? up(c.M * q.K * 2, kAlign) : 0);
-  q.total = q.w + (q.pad ? q.piece * q.K * 2 : q.tail ? 64 * c.K * 2 : 0);
+  q.part = q.w + up(q.pad ? q.piece * q.K * 2 : q.tail ? 64 * c.K * 2 : 0, kAlign);
+  q.total = q.part + (slices > 1 ? slices * c.M * c.K * 4 : 0);
   return q;
 }
 
@@ -398,11 +446,46 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
       p.lda = q.piece;
       p.w = W;
       p.ldw = W_ld;
-      p.c = q.keeps ? base + q.acc : static_cast<char *>(b.dX);
-      p.ldc = q.keeps ? c.K : b.dX_ld;
-      p.c_f32 = q.keeps || b.dx_f32;
-      p.acc_c = n > 0;
-      r = timed(s, TP_KERNEL_GEMM_DGRAD, flops, [&] { return lin_gemm_launch(p, s, ws, q.xt); });
+      const bool first = n == (q.tail ? q.whole : 0), last = n < q.whole && n + cols == q.whole;
+      float *sum = q.keeps ? reinterpret_cast<float *>(base + q.acc) : static_cast<float *>(b.dX);   // of the pieces so far
+      const int64_t sum_ld = q.keeps ? c.K : b.dX_ld;
+      const TilePick t = slices_of(c, wide);
+      const LinChoice h = lin_choose(&p, nullptr, 0);
+      if (t.splits > 1 && h.tiles && spans_ok(p)) {
+        p.mode = kModeSlices;
+        p.c = base + q.part;
+        p.ldc = c.K;
+        p.c_f32 = 1;
+        r = timed(s, TP_KERNEL_GEMM_DGRAD, flops, [&] { return lin_tiles_slices(p, t, s); });
+        if (r != hipSuccess) return r;
+        CeSum u;
+        u.part = reinterpret_cast<const float *>(base + q.part);
+        u.slices = t.splits;
+        u.base = first ? nullptr : sum;
+        u.base_ld = sum_ld;
+        u.out = last ? b.dX : sum;
+        u.out_ld = last ? b.dX_ld : sum_ld;
+        u.out_f32 = last ? c.f32 || b.dx_f32 : 1;
+        u.M = c.M;
+        u.K = c.K;
+        r = timed(s, TP_KERNEL_REDUCE, 4.0 * MK * (t.splits + 1), [&] { return ce_sum_launch(u, s); });
+      } else {
+        p.c = sum;
+        p.ldc = sum_ld;
+        p.c_f32 = q.keeps || b.dx_f32 || c.f32;
+        p.acc_c = !first;
+        r = timed(s, TP_KERNEL_GEMM_DGRAD, flops, [&] { return lin_gemm_launch(p, s, ws, q.xt); });
+        if (r == hipSuccess && last && q.keeps) {
+          CeSum u;
+          u.part = sum;
+          u.slices = 1;
+          u.out = b.dX;
+          u.out_ld = b.dX_ld;
+          u.M = c.M;
+          u.K = c.K;
+          r = timed(s, TP_KERNEL_REDUCE, 6.0 * MK, [&] { return ce_sum_launch(u, s); });
+        }
+      }
       if (r != hipSuccess) return r;
     }
     if (b.dW) {
@@ -425,9 +508,7 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
     }
     return r;
   });
-  if (e != hipSuccess || !q.keeps || c.M <= 0) return e;
-  return timed(s, TP_KERNEL_REDUCE, 6.0 * MK,
-               [&] { return ce_round_launch(reinterpret_cast<const float *>(base + q.acc), b.dX, c.M, c.K, b.dX_ld, s); });
+  return e;
 }
 
 }  // namespace tpshard

@@ -17,6 +17,7 @@ enum {
   kModePair = 3,  // c = A W and c2 = A2 W2, two products of one shape in one launch
   kModeStats = 4, // logits z = A W: each tile's row maxima and sums of exponentials (CeGemm)
   kModeProb = 5,  // logits z = A W: c = the loss's gradient at z (CeGemm)
+  kModeSlices = 6, // c[s] = A W over slice s of K, fp32, each [M][ldc]: no two workgroups share a sum
 };
 
 // A workspace's first bytes are tickets (zero before and after every launch), its
@@ -72,6 +73,7 @@ struct CeGemm : LinGemm {
 // A kernel's arguments.  (By specialisation: an expression of the unnamed enum above in a
 // kernel's signature would be part of its symbol, and numbered differently in host and device
 // code.)
+// (kModeSlices takes a LinGemm.)
 template <int MODE>
 struct LinArgsOf {
   using type = LinGemm;
@@ -128,6 +130,7 @@ hipError_t lin_tiles_pair(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_stats(const CeGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_prob(const CeGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_wgrad(const LinGemm& p, const TilePick& t, hipStream_t s);   // kModeOne, a_t and w_t
+hipError_t lin_tiles_slices(const LinGemm& p, const TilePick& t, hipStream_t s);  // kModeSlices: t.splits slices, 256-row tiles
 
 // The kernel for few rows.
 constexpr int kRowsWaves = 8;   // of a workgroup, at most (measured against 4 and 16 with one token)

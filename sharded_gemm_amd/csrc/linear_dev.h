@@ -288,7 +288,7 @@ __device__ __forceinline__ void store4_c(const LinGemm& p, void *c, int64_t off,
 template <typename T, int MODE, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void epilogue(const LinGemm& p, void *c, const f32x4 (&acc)[TM][TN], RM&& rm, CN&& cn) {
   constexpr int NJ = MODE == kModeDual ? TN / 2 : TN;
-  if constexpr (MODE == kModeCat || MODE == kModePair) {
+  if constexpr (MODE == kModeCat || MODE == kModePair || MODE == kModeSlices) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll

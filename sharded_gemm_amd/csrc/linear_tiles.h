@@ -174,17 +174,17 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
   const uint32_t step = static_cast<uint32_t>((grpA ? TA::step(p.lda) : TW::step(p.ldw)) * 2);
   const void *a_base = pl.second ? p.a2 : p.a;
   const void *w_base = pl.second || WO::second((wave & 3) * W_PW) ? p.w2 : p.w;
-  const int half = static_cast<int>(p.K / BK);
+  const int half = static_cast<int>(p.K / BK), st0 = MODE == kModeSlices ? pl.st0 : 0;
   auto dma_a = [&](int q, int st, int slot_st) {
     const uint32_t src = static_cast<uint32_t>(TA::src((wave & 3) * A_PW + q, lane, pl.m0, rows_of<!AT>(p.M), p.lda) * 2);
     const bool far = MODE == kModeCat && st >= half;
-    lds_dma16_s(far ? p.a2 : a_base, src + (far ? st - half : st) * step,
+    lds_dma16_s(far ? p.a2 : a_base, src + (far ? st - half : st + st0) * step,
                 lds0 + (slot_st % SA) * TA::BYTES + ((wave & 3) * A_PW + q) * 1024);
   };
   auto dma_w = [&](int q, int st, int slot_st) {
     const uint32_t src = static_cast<uint32_t>(WO::src((wave & 3) * W_PW + q, lane, pl.n0, rows_of<WT>(p.N), p.ldw) * 2);
     const bool far = MODE == kModeCat && st >= half;
-    lds_dma16_s(far ? p.w2 : w_base, src + (far ? st - half : st) * step,
+    lds_dma16_s(far ? p.w2 : w_base, src + (far ? st - half : st + st0) * step,
                 lds0 + W_BASE + (slot_st % SW) * TW::BYTES + ((wave & 3) * W_PW + q) * 1024);
   };
   auto read_a = [&](int i, int kk, int st) {
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
 #pragma unroll
       for (int j = 0; j < C::TN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   };
-  pps_loop<C, A_PW, W_PW>(grpA, pl.st1, acc, dma_a, dma_w, read_a, read_w, init_acc);
+  pps_loop<C, A_PW, W_PW>(grpA, pl.st1 - st0, acc, dma_a, dma_w, read_a, read_w, init_acc);
 
   auto rm = [&](int i) -> int64_t { return pl.m0 + wm * C::WM + i * 16 + (lane & 15); };
   auto cn = [&](int j) -> int64_t {
@@ -209,6 +209,8 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
   if constexpr (MODE == kModeStats)
     ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, pl.n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
+  else if constexpr (MODE == kModeSlices)
+    lin::epilogue<uint16_t, MODE>(p, static_cast<float *>(p.c) + blockIdx.y * p.M * p.ldc, acc, rm, cn);
   else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
 }
 
@@ -224,9 +226,9 @@ hipError_t launch_ring(const LinGemm& p, int splits, hipStream_t s) {
 }
 
 template <int BM, int BN, int MODE, bool AT, bool WT, int WGM = 2>
-hipError_t launch_lin_pps(const LinGemm& p, hipStream_t s) {
+hipError_t launch_lin_pps(const LinGemm& p, hipStream_t s, int slices = 1) {
   hipLaunchKernelGGL((lin_pps_kernel<BM, BN, MODE, AT, WT, WGM>),
-                     dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN))), dim3(512), 0, s,
+                     dim3(static_cast<unsigned>(lin_tiles_count(p, BM, BN)), static_cast<unsigned>(slices)), dim3(512), 0, s,
                      lin_args<MODE>(p));
   return hipGetLastError();
 }

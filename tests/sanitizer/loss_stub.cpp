@@ -47,7 +47,7 @@ void seen(const std::string& s) {
   if (!g_quiet) g_seen.push_back(s);
 }
 void seen_product(const char *type, const char *kernel, int n, const LinGemm& p, int splits) {
-  static const char *names[] = {"one", "dual", "cat", "pair", "stats", "prob"};
+  static const char *names[] = {"one", "dual", "cat", "pair", "stats", "prob", "slices"};
   if (g_quiet) return;
   const std::string s = std::string(type) + kernel + (n ? std::to_string(n) : "") + " " + names[p.mode] + (p.a_t ? " a^T" : " a") + (p.w_t ? " w^T" : " w");
   if (splits > 1) g_seen.push_back(s + " split");
@@ -57,7 +57,7 @@ void seen_product(const char *type, const char *kernel, int n, const LinGemm& p,
 // A product's operands and what its epilogue touches; bm x bn: its tiles.
 void product(const LinGemm& p, int64_t align, int64_t bm, int64_t bn) {
   const int64_t es = p.f32 ? 4 : 2;
-  check(p.mode == kModeOne || p.mode == kModeStats || p.mode == kModeProb, "mode");
+  check(p.mode == kModeOne || p.mode == kModeStats || p.mode == kModeProb || p.mode == kModeSlices, "mode");
   check(p.M > 0 && p.N > 0 && p.K >= 0 && p.N < (int64_t{1} << 31), "sizes");
   need(p.a, p.a_t ? p.K : p.M, p.a_t ? p.M : p.K, p.lda, es, "A", align);
   need(p.w, p.w_t ? p.N : p.K, p.w_t ? p.K : p.N, p.ldw, es, "W", align);
@@ -68,6 +68,7 @@ void product(const LinGemm& p, int64_t align, int64_t bm, int64_t bn) {
     need(p.c, p.M, p.N, p.ldc, p.c_f32 ? 4 : 2, "C");
     return;
   }
+  if (p.mode == kModeSlices) return;
   const CeGemm& q = static_cast<const CeGemm&>(p);
   vec(q.targets, q.M, 8, "targets");
   check(q.cols > 0 && q.cols <= q.N, "columns");
@@ -173,6 +174,21 @@ hipError_t lin_tiles_wgrad(const LinGemm& p, const TilePick& t, hipStream_t) {
   check(p.a_t && p.w_t && p.mode == kModeOne, "weight gradient");
   return tiles(p, t);
 }
+hipError_t lin_tiles_slices(const LinGemm& p, const TilePick& t, hipStream_t) {
+  static const int bn[] = {256, 192, 128};
+  check(p.mode == kModeSlices && !p.a_t && !p.f32 && p.c_f32 && !p.acc_c, "slices");
+  check(t.tile == kTile256 || t.tile == kTile128w, "slices: tile");
+  product(p, 16, 256, bn[t.tile]);
+  check(p.K % 64 == 0 && t.splits > 1 && t.splits <= p.K / 64, "slices: stages");
+  check(p.lda % 8 == 0 && p.ldw % 8 == 0 && (p.w_t || p.groups || p.N % 8 == 0), "slices: operands");
+  if (!p.w_t) need(p.w, p.K, (p.N + 7) / 8 * 8, p.ldw, 2, "W's groups", 16);
+  check(p.M * p.lda * 2 < (int64_t{1} << 31) && (p.w_t ? p.N : p.K) * p.ldw * 2 < (int64_t{1} << 31), "slices: 32-bit offsets");
+  need(p.c, t.splits * p.M, p.N, p.ldc, 4, "partial sums");
+  grid(lin_tiles_count(p, 256, bn[t.tile]), t.splits, 512);
+  static const char *names[] = {"tile256", "tile192", "tile128w"};
+  seen_product("", names[t.tile], 0, p, 1);
+  return hipSuccess;
+}
 hipError_t lin_tiles_dual(const LinGemm&, const TilePick&, hipStream_t) { std::abort(); }
 hipError_t lin_tiles_cat(const LinGemm&, const TilePick&, hipStream_t) { std::abort(); }
 hipError_t lin_tiles_pair(const LinGemm&, const TilePick&, hipStream_t) { std::abort(); }
@@ -237,11 +253,13 @@ hipError_t ce_pad_launch(const CePad& p, hipStream_t) {
   seen("pad");
   return hipSuccess;
 }
-hipError_t ce_round_launch(const float *from, void *out, int64_t M, int64_t K, int64_t ld, hipStream_t) {
-  grid((M * ((K + 3) / 4) + 255) / 256, 1, 256);
-  vec(from, M * K, 4, "fp32 dX");
-  need(out, M, K, ld, 2, "dX");
-  seen("round");
+hipError_t ce_sum_launch(const CeSum& p, hipStream_t) {
+  grid((p.M * ((p.K + 3) / 4) + 255) / 256, 1, 256);
+  check(p.slices >= 1, "sum: slices");
+  vec(p.part, p.slices * p.M * p.K, 4, "partial sums");
+  if (p.base) need(p.base, p.M, p.K, p.base_ld, 4, "sum so far");
+  need(p.out, p.M, p.K, p.out_ld, p.out_f32 ? 4 : 2, "dX");
+  seen("sum");
   return hipSuccess;
 }
 

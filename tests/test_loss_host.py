@@ -61,7 +61,7 @@ def test_no_exception_leaves_a_c_entry(driver):
 
 def own_kernels():
     """What the library is compiled for beyond the linear layer's kernels, by name."""
-    names = {"logits", "join", "transpose", "round", "pad"}
+    names = {"logits", "join", "transpose", "sum", "pad"}
     for mode in ("stats a w", "stats a w^T", "prob a w", "prob a w^T", "one a^T w^T"):
         for t in ("f32",) if mode == "one a^T w^T" else ("bf16", "f32"):
             names |= {f"{t} general64 {mode}", f"{t} general64 {mode} split", f"{t} general128 {mode}"}
@@ -71,6 +71,7 @@ def own_kernels():
             names.add(f"{tile} {mode}")
             if tile.startswith("tile64"):
                 names.add(f"{tile} {mode} split")
+    names |= {f"{tile} slices a {w}" for tile in ("tile256", "tile128w") for w in ("w", "w^T")}
     for mode in ("stats a w", "stats a w^T"):
         names |= {f"tile32 {mode}", f"tile32 {mode} split"}
     return names
