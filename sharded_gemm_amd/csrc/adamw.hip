@@ -72,25 +72,29 @@ __device__ __forceinline__ void put_codes(void *p, int64_t at, uint32_t v, int64
 }
 
 // ---- codes ----------------------------------------------------------------------
+// A code that is off by one is a different state, so what leads to it is defined to the
+// bit: each operation in fp32 and rounded by itself (no fma), divisions and square
+// roots to the nearest.
+#pragma clang fp contract(off)
+
 __device__ __forceinline__ f32x4 m_of(uint32_t q, float scale) {
-  const float s = scale * (1.0f / (127.0f * 127.0f));
   f32x4 m;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float c = static_cast<float>(static_cast<int32_t>(q << (24 - 8 * e)) >> 24);
-    m[e] = c * fabsf(c) * s;
+    const float c = static_cast<float>(static_cast<int32_t>(q << (24 - 8 * e)) >> 24) * (1.0f / 127.0f);
+    m[e] = c * fabsf(c) * scale;
   }
   return m;
 }
-__device__ __forceinline__ f32x4 v_of(uint32_t q, float scale) {
-  const float s = scale * (1.0f / (255.0f * 255.0f));
-  f32x4 v;
+// sqrt(v)
+__device__ __forceinline__ f32x4 r_of(uint32_t q, float scale) {
+  f32x4 r;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float c = static_cast<float>(q >> (8 * e) & 0xffu), r = c * c * s;
-    v[e] = r * r;
+    const float c = static_cast<float>(q >> (8 * e) & 0xffu) * (1.0f / 255.0f);
+    r[e] = c * c * scale;
   }
-  return v;
+  return r;
 }
 
 // The largest magnitude of a wave's values, by their bits: a NaN is above everything.
@@ -103,26 +107,33 @@ __device__ __forceinline__ float wave_top(f32x4 x) {
   return __uint_as_float(b);
 }
 
-// 1 / top; nothing under 2^-100 is told from zero (an m that small moves no weight, and the square root of an fp32
+// 1 / top; nothing under 2^-120 is told from zero (an m that small moves no weight, and the square root of an fp32
 // is never that small).
-__device__ __forceinline__ float over(float top) { return top < 0x1p-100f ? 0.0f : __builtin_amdgcn_rcpf(top); }
+__device__ __forceinline__ float over(float top) { return top < 0x1p-120f ? 0.0f : __builtin_amdgcn_rcpf(top); }
 
-__device__ __forceinline__ uint32_t m_codes(f32x4 m, float inv) {
+// round(codes * sqrt(x / top)), inv about 1 / top: from the hardware's reciprocal and root (an ulp each, so 1e-4 of
+// a code at most) unless that is too near the middle between two codes to tell.
+__device__ __forceinline__ float code_of(float x, float top, float inv, float codes) {
+  const float c = codes * __builtin_amdgcn_sqrtf(x * inv);
+  float q = rintf(c);
+  if (fabsf(c - q) > 0.4995f && inv > 0.0f) q = rintf(codes * sqrtf(x / top));
+  return fminf(q, codes);
+}
+
+__device__ __forceinline__ uint32_t m_codes(f32x4 m, float top) {
+  const float inv = over(top);
   uint32_t q = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float c = fminf(rintf(127.0f * __builtin_amdgcn_sqrtf(fabsf(m[e]) * inv)), 127.0f);
-    q |= (static_cast<uint32_t>(static_cast<int32_t>(copysignf(c, m[e]))) & 0xffu) << (8 * e);
-  }
+  for (int e = 0; e < 4; ++e)
+    q |= (static_cast<uint32_t>(static_cast<int32_t>(copysignf(code_of(fabsf(m[e]), top, inv, 127.0f), m[e]))) & 0xffu) << (8 * e);
   return q;
 }
-__device__ __forceinline__ uint32_t r_codes(f32x4 r, float inv) {
+__device__ __forceinline__ uint32_t r_codes(f32x4 r, float top) {
+  const float inv = over(top);
   uint32_t q = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float c = fminf(rintf(255.0f * __builtin_amdgcn_sqrtf(r[e] * inv)), 255.0f);
-    q |= static_cast<uint32_t>(r[e] > 0.0f ? fmaxf(c, 1.0f) : 0.0f) << (8 * e);
-  }
+  for (int e = 0; e < 4; ++e)
+    q |= static_cast<uint32_t>(r[e] > 0.0f ? fmaxf(code_of(r[e], top, inv, 255.0f), 1.0f) : 0.0f) << (8 * e);
   return q;
 }
 
@@ -177,7 +188,8 @@ __device__ __forceinline__ void step(const AdamTensor& t, int64_t at, const Adam
     f32x4 m, v, r, p;
     if constexpr (CODES) {
       m = m_of(l.mq[q], l.ms[q]);
-      v = v_of(l.vq[q], l.vs[q]);
+      v = r_of(l.vq[q], l.vs[q]);
+      v = v * v;
     } else {
       m = l.m[q];
       v = l.v[q];
@@ -185,8 +197,8 @@ __device__ __forceinline__ void step(const AdamTensor& t, int64_t at, const Adam
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float g = l.g[q][e] * c.factor;
-      m[e] = fmaf(a.beta1, m[e], a.rest1 * g);
-      v[e] = fmaf(a.beta2, v[e], a.rest2 * g * g);
+      m[e] = a.beta1 * m[e] + a.rest1 * g;
+      v[e] = a.beta2 * v[e] + a.rest2 * g * g;
       r[e] = sqrtf(v[e]);
       const float move = c.lr1 * m[e] * __builtin_amdgcn_rcpf(fmaf(r[e], c.over2, a.eps));
       p[e] = fmaf(-shrink, l.p[q][e], l.p[q][e]) - move;
@@ -197,8 +209,8 @@ __device__ __forceinline__ void step(const AdamTensor& t, int64_t at, const Adam
     if constexpr (CODES) {
       // Lanes past the end loaded zeros, and hold zeros.
       const float top_m = wave_top(m), top_r = wave_top(r);
-      put_codes(t.m, i, m_codes(m, over(top_m)), left);
-      put_codes(t.v, i, r_codes(r, over(top_r)), left);
+      put_codes(t.m, i, m_codes(m, top_m), left);
+      put_codes(t.v, i, r_codes(r, top_r), left);
       if ((threadIdx.x & 63) == 0 && left > 0) {
         t.ms[i / kAdamBlock] = top_m;
         t.vs[i / kAdamBlock] = top_r;
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_values_kernel(AdamValuesTa
       const int64_t e = at + (q * kAdamThreads + static_cast<int>(threadIdx.x)) * 4, left = x.n - e;
       if (left <= 0) continue;
       const f32x4 m = m_of(get_codes(x.m, e, left), x.ms[e / kAdamBlock]);
-      const f32x4 v = v_of(get_codes(x.v, e, left), x.vs[e / kAdamBlock]);
+      const f32x4 r = r_of(get_codes(x.v, e, left), x.vs[e / kAdamBlock]), v = r * r;
       if (x.f32) {
         put<true>(x.m_out, e, m, left);
         put<true>(x.v_out, e, v, left);
