@@ -23,7 +23,8 @@ ARCH = "gfx950"
 SOURCES = ["plan.cpp", "checker.cpp", "api.cpp", "timing.cpp", "shard.hip", "reduce.hip", "gemm.hip", "noalloc.hip",
            "linear_api.cpp", "linear_launch.cpp", "linear_staged.hip", "linear_rows.hip", "linear_one.hip",
            "linear_dual.hip", "linear_cat.hip", "linear_pair.hip", "act_grad.hip", "grad_clip.hip",
-           "ce_api.cpp", "ce_launch.cpp", "ce.hip", "linear_ce_stats.hip", "linear_ce_prob.hip", "linear_ce_wgrad.hip", "linear_ce_slices.hip",
+           "ce_api.cpp", "ce_launch.cpp", "ce.hip", "linear_ce_stats.hip", "linear_ce_prob.hip", "linear_ce_scaled.hip",
+           "linear_ce_wgrad.hip", "linear_ce_slices.hip",
            "adamw_api.cpp", "adamw.hip"]
 
 COMMON_FLAGS = [

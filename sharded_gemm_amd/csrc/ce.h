@@ -72,8 +72,19 @@ hipError_t ce_join_launch(const CeJoin& p, hipStream_t s);
 hipError_t ce_pieces_launch(const float *stats, int64_t pieces, int64_t M, const int64_t *targets, int64_t ignore,
                             float *loss, float *lse, hipStream_t s);
 
-// xt [K, rows] <- the transpose of X, zero for ignored targets and for m >= M; tickets
-// (kMaxTickets, or null) <- 0.
+// Before the products: *scale (optional) <- what the gradient at the logits is divided by,
+// the largest finite |g| (where it is at least 2^-64 of the largest |h|, else that) over tokens that are not
+// ignored, 1 where there is none; tickets (kMaxTickets) <- 0.
+struct CeScale {
+  const int64_t *targets = nullptr;
+  int64_t M = 0, ignore = 0, g_step = 0, h_step = 0;
+  const float *g = nullptr, *h = nullptr;
+  float *scale = nullptr;
+  uint32_t *tickets = nullptr;
+};
+hipError_t ce_scale_launch(const CeScale& p, hipStream_t s);
+
+// xt [K, rows] <- the transpose of X, zero for ignored targets and for m >= M; and ce_scale_launch's work beside it.
 struct CeTranspose {
   const void *X = nullptr;
   void *xt = nullptr;
@@ -81,7 +92,7 @@ struct CeTranspose {
   const int64_t *targets = nullptr;
   int64_t ignore = 0;
   int32_t f32 = 0;
-  uint32_t *tickets = nullptr;
+  CeScale scale;
 };
 hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t s);
 
@@ -93,10 +104,10 @@ struct CePad {
 };
 hipError_t ce_pad_launch(const CePad& p, hipStream_t s);
 
-// out [M, K] <- base + sum over s < slices, in order, of part[s]; part [slices][M][K] fp32,
+// out [M, K] <- base + *alpha (null: 1) times the sum over s < slices, in order, of part[s]; part [slices][M][K] fp32,
 // base (optional) fp32, out bf16 or fp32 (then it may be base).
 struct CeSum {
-  const float *part = nullptr, *base = nullptr;
+  const float *part = nullptr, *base = nullptr, *alpha = nullptr;
   void *out = nullptr;
   int64_t M = 0, K = 0, slices = 0, base_ld = 0, out_ld = 0;
   int32_t out_f32 = 0;

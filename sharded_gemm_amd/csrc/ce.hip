@@ -117,14 +117,64 @@ __global__ void __launch_bounds__(kThreads) ce_pieces_kernel(const float *stats,
   if (loss) loss[m] = targets[m] == ignore ? 0.0f : total - logit;
 }
 
+// ---- the gradient's scale --------------------------------------------------------------
+// By one workgroup of THREADS.
+template <int THREADS>
+__device__ __forceinline__ void scale_of(const CeScale& p) {
+  for (int i = threadIdx.x; i < kMaxTickets; i += THREADS) p.tickets[i] = 0;
+  if (!p.scale) return;
+  __shared__ float tops[2][THREADS / 64];
+  float g = 0.0f, h = 0.0f;
+  auto larger = [](float top, float x) {
+    x = fabsf(x);
+    return x > top && x < __builtin_inff() ? x : top;   // (a NaN is neither)
+  };
+  constexpr int U = 8;   // tokens of a thread in flight
+  for (int64_t m0 = threadIdx.x; m0 < p.M; m0 += U * THREADS) {
+    int64_t id[U];
+    float x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * THREADS < p.M ? m0 + u * THREADS : p.M - 1;
+      id[u] = p.targets[m];
+      x[u] = p.g ? p.g[m * p.g_step] : 1.0f;
+      y[u] = p.h ? p.h[m * p.h_step] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (id[u] != p.ignore) {
+        g = larger(g, x[u]);
+        h = larger(h, y[u]);
+      }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    g = fmaxf(g, __shfl_xor(g, o));
+    h = fmaxf(h, __shfl_xor(h, o));
+  }
+  if ((threadIdx.x & 63) == 0) {
+    tops[0][threadIdx.x >> 6] = g;
+    tops[1][threadIdx.x >> 6] = h;
+  }
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < THREADS / 64; ++w) {
+    g = fmaxf(g, tops[0][w]);
+    h = fmaxf(h, tops[1][w]);
+  }
+  g = fmaxf(g, h * 0x1p-64f);
+  *p.scale = g < 0x1p-120f ? 1.0f : g;   // (its reciprocal has to be a number too)
+}
+
+__global__ void __launch_bounds__(1024) ce_scale_kernel(CeScale p) { scale_of<1024>(p); }
+
 // ---- X, transposed ------------------------------------------------------------------
 // 64 tokens x 64 columns through LDS.  T: uint16_t or uint32_t.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) ce_transpose_kernel(CeTranspose p) {
   constexpr int V = 16 / sizeof(T), E = 64, PITCH = E + 4 / sizeof(T);   // a row and a bank
   __shared__ T tile[E * PITCH];
-  if (p.tickets && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < kMaxTickets; i += kThreads) p.tickets[i] = 0;
+  if (blockIdx.x == 0) scale_of<kThreads>(p.scale);
   const int64_t tiles_k = (p.K + E - 1) / E, k0 = blockIdx.x % tiles_k * E, m0 = blockIdx.x / tiles_k * E;
 #pragma unroll
   for (int q = 0; q < E * E / V / kThreads; ++q) {
@@ -166,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) ce_sum_kernel(CeSum p) {
   const int64_t per = (p.K + 3) / 4, i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= p.M * per) return;
   const int64_t m = i / per, k = i % per * 4, left = p.K - k;
-  f32x4 v = p.base ? load4<float>(p.base, m * p.base_ld + k, left) : f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 v{0.f, 0.f, 0.f, 0.f};
   constexpr int B = 4;   // slices in flight
   for (int64_t s = 0; s < p.slices; s += B) {
     f32x4 x[B];
@@ -175,6 +225,8 @@ __global__ void __launch_bounds__(kThreads) ce_sum_kernel(CeSum p) {
 #pragma unroll
     for (int b = 0; b < B; ++b) v = v + x[b];
   }
+  if (p.alpha) v = v * *p.alpha;
+  if (p.base) v = load4<float>(p.base, m * p.base_ld + k, left) + v;
   if (p.out_f32) store4<float>(p.out, m * p.out_ld + k, v, left);
   else store4<uint16_t>(p.out, m * p.out_ld + k, v, left);
 }
@@ -197,6 +249,11 @@ hipError_t ce_join_launch(const CeJoin& p, hipStream_t s) {
 hipError_t ce_pieces_launch(const float *stats, int64_t pieces, int64_t M, const int64_t *targets, int64_t ignore,
                             float *loss, float *lse, hipStream_t s) {
   hipLaunchKernelGGL(ce_pieces_kernel, dim3(grid_of(M, kThreads)), dim3(kThreads), 0, s, stats, pieces, M, targets, ignore, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t ce_scale_launch(const CeScale& p, hipStream_t s) {
+  hipLaunchKernelGGL(ce_scale_kernel, dim3(1), dim3(1024), 0, s, p);
   return hipGetLastError();
 }
 

@@ -152,19 +152,24 @@ __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&
 }
 
 // kModeProb: the gradient at the logits, rounded to the operands' type T for the two
-// products that read it.
+// products that read it.  In bf16 it is divided by the largest |g| first, which the
+// products multiply back in fp32: most of a row's gradient is its target's entry, -g (1 -
+// p), and where all g are alike (a mean) every one of them would be rounded the same
+// way, up to 0.4 % of the result; divided, they round to -1.
 template <typename T, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN], RM&& rm, CN&& cn) {
   // Every row's loads before any store, which the compiler may not move them across.
   int64_t id[TM];
   float lses[TM], gs[TM], ghs[TM];
+  const float scale = p.scale ? *p.scale : 1.0f;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int64_t m = rm(i) < p.M ? rm(i) : p.M - 1;
     id[i] = p.targets[m];
     lses[i] = p.lse[m];
-    gs[i] = p.g ? p.g[m * p.g_step] : 1.0f;
-    ghs[i] = p.h ? gs[i] + p.h[m * p.h_step] : gs[i];
+    const float g = p.g ? p.g[m * p.g_step] : 1.0f;
+    gs[i] = g / scale;
+    ghs[i] = (p.h ? g + p.h[m * p.h_step] : g) / scale;
   }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -201,6 +206,19 @@ __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN]
       lin::store4<T>(p.c, m * p.ldc + n, y, left);
     }
   }
+}
+
+// kModeScaled.
+template <int TM, int TN, typename RM, typename CN>
+__device__ __forceinline__ void scaled(const ScaledGemm& p, const f32x4 (&acc)[TM][TN], RM&& rm, CN&& cn) {
+  const float alpha = *p.alpha;
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int64_t m = rm(i), n = cn(j), left = p.N - n;
+      if (m < p.M && left > 0) lin::store4_c(p, p.c, m * p.ldc + n, acc[i][j] * alpha, left);
+    }
 }
 
 }  // namespace ce

@@ -172,11 +172,12 @@ struct Backward {
   int64_t rows = 0, piece = 0, whole = 0, K = 0;   // tokens of P; its columns; the vocabulary in pieces of them; K as multiplied
   bool pad = false, tail = false;                  // every piece of W is copied; the last V - whole columns are
   bool keeps = false;                              // dX is summed in the workspace
-  int64_t xt = 0, p = 0, acc = 0, x = 0, w = 0, part = 0, total = 0;
+  int64_t scale = 0, xt = 0, p = 0, acc = 0, x = 0, w = 0, part = 0, total = 0;
 };
 
 LinGemm dx_product(const CeSizes& c, int64_t n, bool copied) {
   LinGemm p;
+  p.mode = c.f32 ? kModeOne : kModeScaled;
   p.groups = copied;
   p.M = c.M;
   p.N = c.K;
@@ -192,6 +193,7 @@ bool spans_ok(const LinGemm& p) {
 }
 LinGemm dw_product(const CeSizes& c, int64_t n, int64_t rows) {
   LinGemm p;
+  p.mode = c.f32 ? kModeOne : kModeScaled;
   p.groups = !c.f32;   // P's rows go on to a multiple of 64
   p.M = c.linear ? n : c.K;
   p.N = c.linear ? c.K : n;
@@ -277,7 +279,8 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
       if (b.dW) joined = std::max(joined, lin_gemm_ws(dw_product(c, cols, q.rows)));
       return hipSuccess;
     });
-  q.xt = up(joined, kAlign);
+  q.scale = up(joined, kAlign);
+  q.xt = q.scale + kAlign;
   q.p = q.xt + (b.dW ? up(c.K * q.rows * es, kAlign) : 0);
   q.acc = q.p + up(q.rows * q.piece * es, kAlign);
   q.x = q.acc + (q.keeps ? up(c.M * c.K * 4, kAlign) : 0);
@@ -385,6 +388,17 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
   char *base = static_cast<char *>(ws);
   const int64_t es = c.f32 ? 4 : 2, dw_es = b.dw_f32 ? 4 : 2;
   const double MK = static_cast<double>(c.M) * static_cast<double>(c.K);
+  float *scale = reinterpret_cast<float *>(base + q.scale);
+  CeScale g;
+  g.targets = o.targets;
+  g.M = c.M;
+  g.ignore = o.ignore;
+  g.g = b.g;
+  g.g_step = b.g_step;
+  g.h = b.h;
+  g.h_step = b.h_step;
+  g.scale = c.f32 ? nullptr : scale;
+  g.tickets = reinterpret_cast<uint32_t *>(base);
   hipError_t e;
   if (b.dW && c.M > 0) {
     CeTranspose t;
@@ -397,13 +411,25 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
     t.targets = o.targets;
     t.ignore = o.ignore;
     t.f32 = c.f32;
-    t.tickets = reinterpret_cast<uint32_t *>(base);
+    t.scale = g;
     e = timed(s, TP_KERNEL_REDUCE, 2.0 * static_cast<double>(es) * MK, [&] { return ce_transpose_launch(t, s); });
   } else {
-    e = zero_tickets_launch(reinterpret_cast<uint32_t *>(base), s);
+    e = timed(s, TP_KERNEL_REDUCE, 12.0 * static_cast<double>(c.M), [&] { return ce_scale_launch(g, s); });
   }
   if (e != hipSuccess) return e;
   if (c.M > 0 && q.K != c.K && (e = pad(pad_x(c, o, q.K, base + q.x), s)) != hipSuccess) return e;
+  // A product of the gradients: in bf16 multiplied by the scale again.
+  auto gradient = [&](const LinGemm& of, int kind, double flops) {
+    return timed(s, kind, flops, [&] {
+      if (of.mode == kModeOne && !(of.a_t && of.w_t)) return lin_gemm_launch(of, s, ws, q.scale);
+      ScaledGemm p;
+      static_cast<LinGemm&>(p) = of;
+      p.alpha = scale;
+      const LinChoice h = lin_choose(&p, ws, q.scale);
+      if (!h.tiles) return lin_staged_launch(p, h.staged, s);
+      return p.a_t ? lin_tiles_wgrad(p, h.tile, s) : lin_tiles_scaled(p, h.tile, s);
+    });
+  };
   e = each_piece(c, q, [&](int64_t n, int64_t cols, int64_t wide) {
     const double flops = 2.0 * MK * static_cast<double>(cols);
     const bool copied = q.pad || cols != wide;
@@ -435,8 +461,9 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
       p.g_step = b.g_step;
       p.h = b.h;
       p.h_step = b.h_step;
+      p.scale = g.scale;
       p.pad_rows = q.rows;
-      const LinChoice h = lin_choose(&p, ws, q.xt);
+      const LinChoice h = lin_choose(&p, ws, q.scale);
       r = timed(s, TP_KERNEL_GEMM1, flops, [&] { return h.tiles ? lin_tiles_prob(p, h.tile, s) : lin_staged_launch(p, h.staged, s); });
       if (r != hipSuccess) return r;
     }
@@ -461,6 +488,7 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
         CeSum u;
         u.part = reinterpret_cast<const float *>(base + q.part);
         u.slices = t.splits;
+        u.alpha = scale;
         u.base = first ? nullptr : sum;
         u.base_ld = sum_ld;
         u.out = last ? b.dX : sum;
@@ -474,7 +502,7 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
         p.ldc = sum_ld;
         p.c_f32 = q.keeps || b.dx_f32 || c.f32;
         p.acc_c = !first;
-        r = timed(s, TP_KERNEL_GEMM_DGRAD, flops, [&] { return lin_gemm_launch(p, s, ws, q.xt); });
+        r = gradient(p, TP_KERNEL_GEMM_DGRAD, flops);
         if (r == hipSuccess && last && q.keeps) {
           CeSum u;
           u.part = sum;
@@ -499,12 +527,11 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
       p.ldc = b.dW_ld;
       p.c_f32 = b.dw_f32;
       p.acc_c = b.accumulate;
-      if (c.M == 0) p.w_t = 0;   // a sum of nothing, on the general kernel
-      r = timed(s, TP_KERNEL_GEMM_WGRAD, flops, [&] {
-        if (!p.w_t) return lin_gemm_launch(p, s, ws, q.xt);
-        const LinChoice h = lin_choose(&p, ws, q.xt);
-        return h.tiles ? lin_tiles_wgrad(p, h.tile, s) : lin_staged_launch(p, h.staged, s);
-      });
+      if (c.M == 0) {   // a sum of nothing, on the general kernel
+        p.mode = kModeOne;
+        p.w_t = 0;
+      }
+      r = gradient(p, TP_KERNEL_GEMM_WGRAD, flops);
     }
     return r;
   });

@@ -17,6 +17,7 @@ enum {
   kModePair = 3,  // c = A W and c2 = A2 W2, two products of one shape in one launch
   kModeStats = 4, // logits z = A W: each tile's row maxima and sums of exponentials (CeGemm)
   kModeProb = 5,  // logits z = A W: c = the loss's gradient at z (CeGemm)
+  kModeScaled = 7, // c = alpha A W (ScaledGemm)
   kModeSlices = 6, // c[s] = A W over slice s of K, fp32, each [M][ldc]: no two workgroups share a sum
 };
 
@@ -65,10 +66,14 @@ struct CeGemm : LinGemm {
   float *part = nullptr;
   int64_t slot0 = 0;
   float *logit = nullptr;
-  // kModeProb: c[m, n] <- (g + h) exp(z - lse) - (id n is the target) g, 0 in the rows of ignored targets, in
+  // kModeProb: c[m, n] <- ((g + h) exp(z - lse) - (id n is the target) g) / *scale (null: 1), 0 in the rows of ignored targets, in
   // the rows M .. pad_rows - 1 and in the columns from `cols` on.  g = g[m * g_step], h likewise or 0.
-  const float *lse = nullptr, *g = nullptr, *h = nullptr;
+  const float *lse = nullptr, *g = nullptr, *h = nullptr, *scale = nullptr;
   int64_t g_step = 0, h_step = 0, ignore = 0, pad_rows = 0;
+};
+// A product whose values are multiplied by *alpha (device memory) on their way out; no bias, activation or residual.
+struct ScaledGemm : LinGemm {
+  const float *alpha = nullptr;
 };
 // A kernel's arguments.  (By specialisation: an expression of the unnamed enum above in a
 // kernel's signature would be part of its symbol, and numbered differently in host and device
@@ -85,6 +90,10 @@ struct LinArgsOf<kModeStats> {
 template <>
 struct LinArgsOf<kModeProb> {
   using type = CeGemm;
+};
+template <>
+struct LinArgsOf<kModeScaled> {
+  using type = ScaledGemm;
 };
 template <int MODE>
 using LinArgs = typename LinArgsOf<MODE>::type;
@@ -129,7 +138,8 @@ hipError_t lin_tiles_cat(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_pair(const LinGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_stats(const CeGemm& p, const TilePick& t, hipStream_t s);
 hipError_t lin_tiles_prob(const CeGemm& p, const TilePick& t, hipStream_t s);
-hipError_t lin_tiles_wgrad(const LinGemm& p, const TilePick& t, hipStream_t s);   // kModeOne, a_t and w_t
+hipError_t lin_tiles_scaled(const ScaledGemm& p, const TilePick& t, hipStream_t s);
+hipError_t lin_tiles_wgrad(const ScaledGemm& p, const TilePick& t, hipStream_t s);   // a_t and w_t
 hipError_t lin_tiles_slices(const LinGemm& p, const TilePick& t, hipStream_t s);  // kModeSlices: t.splits slices, 256-row tiles
 
 // The kernel for few rows.

@@ -1,0 +1,10 @@
+// Tiled bf16 kernels: the cross entropy's gradients' other products.
+#include "linear_tiles.h"
+
+namespace tpshard {
+
+hipError_t lin_tiles_scaled(const ScaledGemm& p, const TilePick& t, hipStream_t s) {
+  return p.w_t ? dispatch_tiles<kModeScaled, false, true>(p, t, s) : dispatch_tiles<kModeScaled, false, false>(p, t, s);
+}
+
+}  // namespace tpshard

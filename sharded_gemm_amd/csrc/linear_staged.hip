@@ -3,7 +3,7 @@
 //
 //   kModeOne  c = epi(A W)              kModeDual  c = act(A W) * (A W2)
 //   kModeCat  c = A W + A2 W2           kModePair  c = A W, c2 = A2 W2
-//   kModeStats, kModeProb: the vocabulary cross entropy's (ce_dev.h)
+//   kModeStats, kModeProb, kModeScaled: the vocabulary cross entropy's (ce_dev.h)
 //
 // A workgroup of 4 or 8 waves owns a BM x BN tile of the output (kModeDual: BM x
 // BN/2, with the gate's and the up projection's columns side by side in the W
@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_ker
   };
   if constexpr (MODE == kModeStats) ce::stats<BM, WAVES_N, THREADS>(p, smem, acc, m0, p.slot0 + n0 / BN, wn, n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<std::conditional_t<sizeof(T) == 4, float, uint16_t>>(p, acc, rm, cn);
+  else if constexpr (MODE == kModeScaled) ce::scaled(p, acc, rm, cn);
   else if constexpr (sizeof(T) == 4) epilogue<float, MODE>(p, c, acc, rm, cn);
   else epilogue<uint16_t, MODE>(p, c, acc, rm, cn);
 }
@@ -359,6 +360,8 @@ hipError_t dispatch(const LinGemm& p, const StagedShape& h, hipStream_t s) {
       if (akc) return wkc ? launch<T, true, true, kModeProb>(p, h, s) : launch<T, true, false, kModeProb>(p, h, s);
       break;
   }
+  if constexpr (sizeof(T) == 2)
+    if (p.mode == kModeScaled && akc) return wkc ? launch<T, true, true, kModeScaled>(p, h, s) : launch<T, true, false, kModeScaled>(p, h, s);
   if (p.mode == kModeOne && !akc && !wkc) return launch<T, false, false, kModeOne>(p, h, s);
   if constexpr (sizeof(T) == 4)   // (bf16: always on the tiled kernels)
     if (p.mode == kModeOne && !akc) return launch<T, false, true, kModeOne>(p, h, s);

@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N, 1) lin_ring_kernel(Lin
   if constexpr (MODE == kModeStats)
     ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, pl.n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
+  else if constexpr (MODE == kModeScaled) ce::scaled(p, acc, rm, cn);
   else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);
 }
 
@@ -209,6 +210,7 @@ __global__ void __launch_bounds__(512, 1) lin_pps_kernel(LinArgs<MODE> p) {
   if constexpr (MODE == kModeStats)
     ce::stats<BM, C::WAVES_N, C::THREADS>(p, smem, acc, pl.m0, p.slot0 + pl.n0 / BN, wn, pl.n0 + BN <= p.cols, rm, cn);
   else if constexpr (MODE == kModeProb) ce::prob<uint16_t>(p, acc, rm, cn);
+  else if constexpr (MODE == kModeScaled) ce::scaled(p, acc, rm, cn);
   else if constexpr (MODE == kModeSlices)
     lin::epilogue<uint16_t, MODE>(p, static_cast<float *>(p.c) + blockIdx.y * p.M * p.ldc, acc, rm, cn);
   else lin::epilogue<uint16_t, MODE>(p, pl.second ? p.c2 : p.c, acc, rm, cn);

@@ -47,7 +47,7 @@ void seen(const std::string& s) {
   if (!g_quiet) g_seen.push_back(s);
 }
 void seen_product(const char *type, const char *kernel, int n, const LinGemm& p, int splits) {
-  static const char *names[] = {"one", "dual", "cat", "pair", "stats", "prob", "slices"};
+  static const char *names[] = {"one", "dual", "cat", "pair", "stats", "prob", "slices", "scaled"};
   if (g_quiet) return;
   const std::string s = std::string(type) + kernel + (n ? std::to_string(n) : "") + " " + names[p.mode] + (p.a_t ? " a^T" : " a") + (p.w_t ? " w^T" : " w");
   if (splits > 1) g_seen.push_back(s + " split");
@@ -57,12 +57,16 @@ void seen_product(const char *type, const char *kernel, int n, const LinGemm& p,
 // A product's operands and what its epilogue touches; bm x bn: its tiles.
 void product(const LinGemm& p, int64_t align, int64_t bm, int64_t bn) {
   const int64_t es = p.f32 ? 4 : 2;
-  check(p.mode == kModeOne || p.mode == kModeStats || p.mode == kModeProb || p.mode == kModeSlices, "mode");
+  check(p.mode == kModeOne || p.mode == kModeStats || p.mode == kModeProb || p.mode == kModeSlices || p.mode == kModeScaled, "mode");
   check(p.M > 0 && p.N > 0 && p.K >= 0 && p.N < (int64_t{1} << 31), "sizes");
   need(p.a, p.a_t ? p.K : p.M, p.a_t ? p.M : p.K, p.lda, es, "A", align);
   need(p.w, p.w_t ? p.N : p.K, p.w_t ? p.K : p.N, p.ldw, es, "W", align);
   check(!p.aux && !p.aux2 && !p.bias && !p.res && !p.act, "a plain product");
-  if (p.mode == kModeOne) {
+  if (p.mode == kModeScaled) {
+    check(!p.f32, "scaled: bf16");
+    vec(static_cast<const ScaledGemm&>(p).alpha, 1, 4, "alpha");
+  }
+  if (p.mode == kModeOne || p.mode == kModeScaled) {
     check(!p.acc_c || p.c_f32, "only fp32 accumulates");
     check(!p.f32 || p.c_f32, "fp32 operands have an fp32 output");
     need(p.c, p.M, p.N, p.ldc, p.c_f32 ? 4 : 2, "C");
@@ -82,6 +86,8 @@ void product(const LinGemm& p, int64_t align, int64_t bm, int64_t bn) {
     check(q.c_f32 == q.f32, "P in the operands' type");
     need(q.c, q.pad_rows, q.N, q.ldc, es, "P", 16);
     vec(q.lse, q.M, 4, "lse");
+    check(!q.scale == static_cast<bool>(q.f32), "the scale is bf16's");
+    if (q.scale) vec(q.scale, 1, 4, "scale");
     if (q.g) vec(q.g, q.g_step ? q.M : 1, 4, "g");
     if (q.h) vec(q.h, q.h_step ? q.M : 1, 4, "h");
   }
@@ -151,7 +157,7 @@ hipError_t lin_staged_launch(const LinGemm& p, const StagedShape& h, hipStream_t
   product(p, 0, h.edge, h.edge);
   check(h.edge == 64 || h.splits == 1, "general: only the small tile is split");
   check(h.tiles == lin_tiles_count(p, h.edge, h.edge), "general: tiles");
-  check(!p.a_t || (p.mode == kModeOne && (p.f32 || !p.w_t)), "general: no such instance");
+  check(p.a_t ? p.mode == kModeOne && (p.f32 || !p.w_t) : p.mode != kModeScaled || !p.f32, "general: no such instance");
   grid(h.tiles, h.splits, h.edge == 128 ? 512 : 256);
   split(p, h.splits, h.tiles, 64 * 64);
   seen_product(p.f32 ? "f32 " : "bf16 ", "general", h.edge, p, h.splits);
@@ -170,8 +176,12 @@ hipError_t lin_tiles_prob(const CeGemm& p, const TilePick& t, hipStream_t) {
   check(!p.a_t && p.mode == kModeProb, "prob");
   return tiles(p, t);
 }
-hipError_t lin_tiles_wgrad(const LinGemm& p, const TilePick& t, hipStream_t) {
-  check(p.a_t && p.w_t && p.mode == kModeOne, "weight gradient");
+hipError_t lin_tiles_wgrad(const ScaledGemm& p, const TilePick& t, hipStream_t) {
+  check(p.a_t && p.w_t && p.mode == kModeScaled, "weight gradient");
+  return tiles(p, t);
+}
+hipError_t lin_tiles_scaled(const ScaledGemm& p, const TilePick& t, hipStream_t) {
+  check(!p.a_t && p.mode == kModeScaled, "scaled");
   return tiles(p, t);
 }
 hipError_t lin_tiles_slices(const LinGemm& p, const TilePick& t, hipStream_t) {
@@ -235,13 +245,28 @@ hipError_t ce_pieces_launch(const float *stats, int64_t pieces, int64_t M, const
   seen("pieces");
   return hipSuccess;
 }
+namespace {
+void scaled(const CeScale& p) {
+  vec(p.tickets, kMaxTickets, 4, "tickets");
+  if (!p.scale) return;
+  vec(p.scale, 1, 4, "scale");
+  vec(p.targets, p.M, 8, "targets");
+  if (p.g) vec(p.g, p.g_step ? p.M : p.M > 0, 4, "g");
+  if (p.h) vec(p.h, p.h_step ? p.M : p.M > 0, 4, "h");
+}
+}  // namespace
+hipError_t ce_scale_launch(const CeScale& p, hipStream_t) {
+  scaled(p);
+  seen("scale");
+  return hipSuccess;
+}
 hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t) {
   check(p.rows % 64 == 0 && p.rows >= p.M && p.M > 0, "transpose: rows");
   grid((p.K + 63) / 64 * (p.rows / 64), 1, 256);
   need(p.X, p.M, p.K, p.X_ld, p.f32 ? 4 : 2, "X");
   vec(p.xt, p.K * p.rows, p.f32 ? 4 : 2, "X^T", 16);
   vec(p.targets, p.M, 8, "targets");
-  if (p.tickets) vec(p.tickets, kMaxTickets, 4, "tickets");
+  scaled(p.scale);
   seen("transpose");
   return hipSuccess;
 }
@@ -257,6 +282,7 @@ hipError_t ce_sum_launch(const CeSum& p, hipStream_t) {
   grid((p.M * ((p.K + 3) / 4) + 255) / 256, 1, 256);
   check(p.slices >= 1, "sum: slices");
   vec(p.part, p.slices * p.M * p.K, 4, "partial sums");
+  if (p.alpha) vec(p.alpha, 1, 4, "alpha");
   if (p.base) need(p.base, p.M, p.K, p.base_ld, 4, "sum so far");
   need(p.out, p.M, p.K, p.out_ld, p.out_f32 ? 4 : 2, "dX");
   seen("sum");

@@ -248,9 +248,11 @@ def test_unpack(sizes, dtype):
     tp.tp_adamw_unpack(g.views("m"), g.views("v"), [b.t for b in m], [b.t for b in v], m_scale=g.views("ms"), v_scale=g.views("vs"))
     torch.cuda.synchronize()
     half = torch.finfo(dtype).eps / 2
+    # q / 127: two roundings (the constant's and the product's), its square twice those and one, the scale's product
+    # one: 6 u for m and for sqrt(v), whose square is off by twice that and one more.
     for i in range(len(sizes)):
-        for got, want in zip((m[i], v[i]), g.state(g.host, i)):
-            assert got.intact() and (np.abs(f64(got.t) - want) <= (half + 8 * U) * np.abs(want) + TINY).all()
+        for got, want, steps in zip((m[i], v[i]), g.state(g.host, i), (6, 13)):
+            assert got.intact() and (np.abs(f64(got.t) - want) <= (half + (steps + 1) * U) * np.abs(want) + TINY).all()
 
 
 def test_no_tensors():

@@ -450,3 +450,40 @@ def test_every_kernel(case):
     else:
         lse = lse_for(X, W)
         check_backward(X, W, t, lse, backward(X, W, t, lse, layout, piece=piece, Xd=Xd, Wd=Wd))
+
+
+@pytest.mark.parametrize("layout", [MATH, LINEAR])
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 1.0, 1e30])
+def test_gradients_alike_are_not_rounded_alike(scale, layout):
+    """One gradient for all tokens (a mean), whatever its bits: dX and dW are off by roundings that differ from element
+    to element, u of their 2-norm for the result's and under half a u for dz's, not by the rounding of that gradient."""
+    X, W, t = make(300, 128, 2000, BF16, seed=21, std=1.0)
+    lse = lse_for(X, W)
+    want = O.cross_entropy_backward(f64(X), f64(W), t.numpy(), f64(lse))
+    for f in (1.0, 1.003, 1.0039, 1.5, 1.996):
+        got = backward(X, W, t, lse, layout, g=torch.tensor([scale * f]))
+        for k in ("dX", "dW"):
+            w = want[k] * float(np.float32(scale * f))
+            assert np.linalg.norm(f64(got[k]) - w) <= 1.5 * half(BF16) / 3 ** 0.5 * np.linalg.norm(w), (f, k)
+
+
+def test_gradients_of_many_sizes():
+    """Tokens whose gradients differ by 1e6, zeros among them, and penalties far above the losses' gradients."""
+    X, W, t = make(200, 64, 500, BF16, seed=22)
+    lse = lse_for(X, W)
+    g = torch.logspace(-6, 0, 200) * (torch.arange(200) % 7 > 0)
+    for layout in (MATH, LINEAR):
+        check_backward(X, W, t, lse, backward(X, W, t, lse, layout, g=g), g=f64(g))
+        check_backward(X, W, t, lse, backward(X, W, t, lse, layout, g=g * 1e-20, h=g.flip(0)), g=f64(g * 1e-20), h=f64(g.flip(0)))
+        check_backward(X, W, t, lse, backward(X, W, t, lse, layout, g=0 * g, h=g), g=0.0, h=f64(g))
+        none = backward(X, W, t, lse, layout, g=0 * g)
+        assert bool((none["dX"] == 0).all()) and bool((none["dW"] == 0).all())
+        # An infinite gradient is its own row's.
+        bad = g.clone()
+        bad[5] = float("inf")
+        t2 = t.clone()
+        t2[5] = 3
+        got = backward(X, W, t2, lse, layout, g=bad)["dX"]
+        rest = torch.arange(200) != 5
+        check_backward(X[rest], W, t2[rest], lse[rest], dict(dX=got[rest.cuda()]), g=f64(g[rest]))
+        assert not bool(torch.isfinite(got[5]).any())

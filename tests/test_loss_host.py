@@ -62,15 +62,18 @@ def test_no_exception_leaves_a_c_entry(driver):
 def own_kernels():
     """What the library is compiled for beyond the linear layer's kernels, by name."""
     names = {"logits", "join", "transpose", "sum", "pad"}
-    for mode in ("stats a w", "stats a w^T", "prob a w", "prob a w^T", "one a^T w^T"):
-        for t in ("f32",) if mode == "one a^T w^T" else ("bf16", "f32"):
-            names |= {f"{t} general64 {mode}", f"{t} general64 {mode} split", f"{t} general128 {mode}"}
-        for tile in ("tile256", "tile192", "tile128w", "tile128", "tile64", "tile64short", "tile64k32"):
-            if mode == "one a^T w^T" and tile == "tile64k32":
+    tiles = ("tile256", "tile192", "tile128w", "tile128", "tile64", "tile64short", "tile64k32")
+    for mode in ("stats a w", "stats a w^T", "prob a w", "prob a w^T", "scaled a w", "scaled a w^T", "scaled a^T w^T"):
+        for tile in tiles:
+            if mode == "scaled a^T w^T" and tile == "tile64k32":
                 continue            # tokens come in multiples of 64
             names.add(f"{tile} {mode}")
             if tile.startswith("tile64"):
                 names.add(f"{tile} {mode} split")
+    for t, modes in (("bf16", ("stats a w", "stats a w^T", "prob a w", "prob a w^T", "scaled a w", "scaled a w^T")),
+                     ("f32", ("stats a w", "stats a w^T", "prob a w", "prob a w^T", "one a^T w^T"))):
+        for mode in modes:
+            names |= {f"{t} general64 {mode}", f"{t} general64 {mode} split", f"{t} general128 {mode}"}
     names |= {f"{tile} slices a {w}" for tile in ("tile256", "tile128w") for w in ("w", "w^T")}
     for mode in ("stats a w", "stats a w^T"):
         names |= {f"tile32 {mode}", f"tile32 {mode} split"}
