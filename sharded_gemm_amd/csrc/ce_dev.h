@@ -87,7 +87,9 @@ __device__ __forceinline__ float over_groups(float x, F&& f) {
 // A lane's share is max, fma, exp2 and add for each of its elements; the columns' bounds
 // are only checked in tiles that reach past the last one.  Nothing else of a tile's
 // time overlaps this one's, so latency counts: all targets are loaded at once, all rows
-// go through each step together, and lanes join without LDS.  TIMES.
+// go through each step together, and lanes join without LDS (4096 x 768 x 50000, W
+// [V, K]: 304 us; a row after the other, joined by shuffles, 328; with the bounds checked
+// everywhere 352.  The products alone take 260).
 template <int BM, int WAVES_N, int THREADS, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t slot,
                                       int wn, bool whole, RM&& rm, CN&& cn) {

@@ -299,3 +299,55 @@ def test_on_another_stream():
     g.step(step=1, lr=1e-3, stream=side)
     torch.cuda.synchronize()
     g.check()
+
+
+def test_two_steps_at_once():
+    """Two streams, tensors of their own, one norm and one gradient for both."""
+    a, b = Group([300_000, 17], eight=True, seed=10), Group([300_000, 17], eight=True, seed=10)
+    parts = tp.tp_grad_parts()
+    tp.tp_grad_sumsq(a.views("g"), parts)
+    torch.cuda.synchronize()
+    sides = torch.cuda.Stream(), torch.cuda.Stream()
+    for g, s in zip((a, b), sides):
+        g.dev["g"] = a.dev["g"]
+        g.step(step=1, lr=1e-3, parts=parts, max_norm=0.5, clip_eps=1e-6, stream=s)
+    torch.cuda.synchronize()
+    for k in a.dev:
+        assert all(torch.equal(x.t, y.t) for x, y in zip(a.dev[k], b.dev[k]))
+    norm = math.sqrt(sum(float((f64(x) ** 2).sum()) for x in a.host["g"]))
+    a.check(factor=float(np.float32(0.5 / (norm + 1e-6))))
+
+
+def test_a_tensor_past_32_bits():
+    """2^32 elements and some: parts of it against the same parts as tensors of their own, to the bit."""
+    n = 2 ** 32 + 777
+    announce("adamw 2^32 elements")
+    g = torch.Generator("cuda").manual_seed(3)
+    p = torch.empty(n, dtype=BF16, device="cuda").normal_(0, 0.5, generator=g)
+    d = torch.empty(n, dtype=BF16, device="cuda").normal_(0, 0.01, generator=g)
+    m, v = torch.zeros(n, dtype=torch.int8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ms, vs = torch.zeros(blocks(n), device="cuda"), torch.zeros(blocks(n), device="cuda")
+    B = tp.TP_ADAMW_BLOCK
+    spans = [(0, 70_000), (2 ** 31 // B * B - 40 * B, 80 * B), (2 ** 32 - 40 * B, 40 * B + 777)]
+    s = dict(p=[], g=[], m=[], v=[], ms=[], vs=[])
+    for at, k in spans:
+        for name, x in (("p", p), ("g", d), ("m", m), ("v", v)):
+            s[name].append(x[at:at + k].clone())
+        for name, x in (("ms", ms), ("vs", vs)):
+            s[name].append(x[at // B:at // B + blocks(k)].clone())
+    for t in (1, 2):
+        tp.tp_adamw_step([p], [d], [m], [v], m_scale=[ms], v_scale=[vs], step=t, lr=1e-2, weight_decay=0.1)
+        tp.tp_adamw_step(s["p"], s["g"], s["m"], s["v"], m_scale=s["ms"], v_scale=s["vs"], step=t, lr=1e-2, weight_decay=0.1)
+    del d
+    torch.cuda.synchronize()
+    mo, vo = torch.empty(n, dtype=BF16, device="cuda"), torch.empty(n, dtype=BF16, device="cuda")
+    tp.tp_adamw_unpack([m], [v], [mo], [vo], m_scale=[ms], v_scale=[vs])
+    smo, svo = [torch.empty_like(x) for x in s["p"]], [torch.empty_like(x) for x in s["p"]]
+    tp.tp_adamw_unpack(s["m"], s["v"], smo, svo, m_scale=s["ms"], v_scale=s["vs"])
+    torch.cuda.synchronize()
+    for i, (at, k) in enumerate(spans):
+        for big, little in ((p, s["p"]), (m, s["m"]), (v, s["v"]), (mo, smo), (vo, svo)):
+            assert torch.equal(big[at:at + k], little[i])
+        for big, little in ((ms, s["ms"]), (vs, s["vs"])):
+            assert torch.equal(big[at // B:at // B + blocks(k)], little[i])
+    assert bool((ms > 0).all()) and bool((vs > 0).all())

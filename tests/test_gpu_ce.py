@@ -487,3 +487,161 @@ def test_gradients_of_many_sizes():
         rest = torch.arange(200) != 5
         check_backward(X[rest], W, t2[rest], lse[rest], dict(dX=got[rest.cuda()]), g=f64(g[rest]))
         assert not bool(torch.isfinite(got[5]).any())
+
+
+def test_all_tokens_ignored():
+    for dtype in (BF16, F32):
+        X, W, _ = make(130, 64, 700, dtype, seed=23)
+        t = torch.full((130,), 5)
+        got = forward(X, W, t, MATH, ignore=5)
+        assert bool((got["loss"] == 0).all())
+        check_forward(X, W, t, dict(lse=got["lse"]), dtype, ignore=5)
+        both = backward(X, W, t, torch.full((130,), float("nan")), MATH, g=torch.full((130,), float("inf")), ignore=5)
+        assert bool((both["dX"] == 0).all()) and bool((both["dW"] == 0).all())
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, the same operands; against the calls one after another."""
+    shapes = [(40, 256, 30000), (900, 192, 4100)]
+    sets = []
+    for i, shape in enumerate(shapes):
+        X, W, t = make(*shape, BF16, seed=30 + i)
+        Xd, Wd, td = X.cuda(), lay(W, LINEAR), t.cuda()
+        for _ in range(2):
+            out = [torch.empty(shape[0], device="cuda") for _ in range(2)] + [torch.empty_like(Xd), torch.empty_like(Wd)]
+            calls = [tp.tp_linear_ce(Xd, Wd, td, loss=out[0], lse=out[1], weight_layout=LINEAR, prepare=True,
+                                     ws=tp.tp_linear_ce_ws(Xd, Wd, weight_layout=LINEAR)),
+                     tp.tp_linear_ce_backward(Xd, Wd, td, out[1], dX=out[2], dW=out[3], weight_layout=LINEAR, prepare=True,
+                                              ws=tp.tp_linear_ce_backward_ws(Xd, Wd, weight_layout=LINEAR, dX=out[2]))]
+            sets.append((out, calls))
+    for _, calls in sets:
+        for c in calls:
+            c()
+    torch.cuda.synchronize()
+    want = [[bits(x) for x in out] for out, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for out, _ in sets:
+        for x in out:
+            x.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (_, calls), s in zip(sets, streams):
+            for c in calls:
+                c(s)
+    torch.cuda.synchronize()
+    for (out, _), w in zip(sets, want):
+        assert all(np.array_equal(bits(x), y) for x, y in zip(out, w))
+
+
+def test_two_graphs_on_one_workspace():
+    """Of different sizes, replayed in turn."""
+    data = [make(*s, BF16, seed=40 + i) for i, s in enumerate([(3, 96, 5000), (600, 64, 2100)])]
+    dev = [(X.cuda(), lay(W, MATH), t.cuda()) for X, W, t in data]
+    ws = max((tp.tp_linear_ce_ws(X, W, weight_layout=MATH) for X, W, _ in dev), key=lambda w: w.numel())
+    bws = max((tp.tp_linear_ce_backward_ws(X, W, weight_layout=MATH, dX=X, piece=512) for X, W, _ in dev), key=lambda w: w.numel())
+    graphs = []
+    for X, W, t in dev:
+        out = [torch.empty(X.shape[0], device="cuda") for _ in range(2)] + [torch.empty_like(X), torch.empty_like(W)]
+        fwd = tp.tp_linear_ce(X, W, t, loss=out[0], lse=out[1], ws=ws, prepare=True)
+        bwd = tp.tp_linear_ce_backward(X, W, t, out[1], dX=out[2], dW=out[3], piece=512, ws=bws, prepare=True)
+        fwd()
+        bwd()
+        torch.cuda.synchronize()
+        want = [bits(x) for x in out]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s = torch.cuda.current_stream()
+            fwd(s)
+            bwd(s)
+        graphs.append((graph, out, want))
+    for _ in range(3):
+        for _, out, _ in graphs:
+            for x in out:
+                x.fill_(float("nan"))
+        for graph, _, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want in graphs:
+            assert all(np.array_equal(bits(x), w) for x, w in zip(out, want))
+
+
+@pytest.mark.parametrize("layout", [MATH, LINEAR])
+@pytest.mark.parametrize("M", [3, 600])
+def test_a_weight_past_32_bits(M, layout):
+    """5 GB of it, 2.4e9 elements: lse, loss and dX against float64 on the GPU, a piece of the vocabulary at a time; dW
+    at both ends and around element 2^31."""
+    announce(f"ce long weight {M} layout {layout}")
+    K, V = 4096, 600_000 - 8 * (M > 3)
+    g = torch.Generator("cuda").manual_seed(M)
+    X = torch.randn((M, K), generator=g, device="cuda").to(BF16)
+    W = torch.empty((K, V) if layout == MATH else (V, K), dtype=BF16, device="cuda").normal_(0, K ** -0.5, generator=g)
+
+    def part(n, m):
+        return (W[:, n:n + m] if layout == MATH else W[n:n + m].t()).double()
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    t[0], t[1], t[2] = V - 1, 0, 2 ** 31 // K
+    got = forward(X, None, t, layout, Xd=X, Wd=W)
+    step, x = 20_000, X.double()
+    each, logit, most = [], torch.empty(M, dtype=torch.float64, device="cuda"), 0.0
+    for n in range(0, V, step):
+        z = x @ part(n, step)
+        each.append(z.logsumexp(1))
+        here = (t >= n) & (t < n + z.shape[1])
+        logit[here] = z[here, t[here] - n]
+        most = max(most, float((x.abs() @ part(n, step).abs()).max()))
+    lse = torch.stack(each).logsumexp(0)
+    D = (K / 32 + 32) * U * most
+    tol = D + 64 * U + 4 * U * lse.abs()
+    assert bool(((got["lse"] - lse).abs() <= tol).all())
+    assert bool(((got["loss"] - (lse - logit)).abs() <= 2 * tol + U * (lse - logit).abs()).all())
+
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    ws = tp.tp_linear_ce_backward_ws(X, W, weight_layout=layout, dX=dX)
+    tp.tp_linear_ce_backward(X, W, t, got["lse"], dX=dX, dW=dW, weight_layout=layout, ws=ws)
+    torch.cuda.synchronize()
+    L = got["lse"].double()[:, None]
+    h = half(BF16)
+    # as check_backward: of q relatively D and the exponent's rounding, |z| <= `most`
+    dq = D + 4 * U * (1 + float(L.abs().max()) + most)
+    want, slack, ends = torch.zeros_like(x), torch.zeros_like(x), (0, 2 ** 31 // K // step * step, (V - 1) // step * step)
+    for n in range(0, V, step):
+        w = part(n, step)
+        q = (x @ w - L).exp()
+        dz = q.clone()
+        here = ((t >= n) & (t < n + w.shape[1])).nonzero()[:, 0]
+        dz[here, t[here] - n] -= 1
+        each = 1.01 * dq * q + (h + 4 * U) * dz.abs() + torch.finfo(BF16).smallest_normal
+        want += dz @ w.t().contiguous()
+        slack += (each + (V / 32 + 64) * U * dz.abs()) @ w.abs().t().contiguous()
+        if n in ends:
+            dw = (dW[:, n:n + step] if layout == MATH else dW[n:n + step].t()).double()
+            exact = x.t().contiguous() @ dz
+            tol = x.abs().t().contiguous() @ (each + (M / 32 + 64) * U * dz.abs()) + (h + U) * exact.abs() + torch.finfo(BF16).smallest_normal
+            assert bool(((dw - exact).abs() <= tol).all()), n
+    assert bool(((dX.double() - want).abs() <= slack + (h + U) * want.abs() + torch.finfo(BF16).smallest_normal).all())
+
+
+@pytest.mark.parametrize("layout", [MATH, LINEAR])
+@pytest.mark.parametrize("M", [5, 300])
+def test_strides_past_32_bits(M, layout):
+    """Rows of X, of W and of their gradients far apart: the last begin past 2^32 bytes."""
+    announce(f"ce far rows {M} layout {layout}")
+    K, V = 64, 264
+    X, W, t = make(M, K, V, BF16, seed=50 + M)
+    lse = lse_for(X, W)
+    Wl = W if layout == MATH else W.t().contiguous()
+
+    def far(m):
+        ld = 2 ** 31 // (m.shape[0] - 1) // 8 * 8 + 64
+        v = torch.empty(2 ** 31 + 2 ** 20, dtype=BF16, device="cuda").as_strided(tuple(m.shape), (ld, 1), 64)
+        v.copy_(m)
+        return v
+    for Xd, Wd in ((far(X), Wl.cuda()), (X.cuda(), far(Wl))):
+        check_forward(X, W, t, forward(X, W, t, layout, Xd=Xd, Wd=Wd), BF16)
+        check_backward(X, W, t, lse, backward(X, W, t, lse, layout, Xd=Xd, Wd=Wd))
+    dX, dW = far(torch.zeros_like(X)), far(torch.zeros_like(Wl))
+    Xd, Wd = X.cuda(), Wl.cuda()
+    tp.tp_linear_ce_backward(Xd, Wd, t.cuda(), lse.cuda(), dX=dX, dW=dW, weight_layout=layout,
+                             ws=tp.tp_linear_ce_backward_ws(Xd, Wd, weight_layout=layout, dX=dX))
+    torch.cuda.synchronize()
+    check_backward(X, W, t, lse, dict(dX=dX, dW=dW if layout == MATH else dW.t()))
