@@ -200,7 +200,7 @@ Adam adam(std::mt19937& rng, int num, bool codes) {
     tp_adamw_tensor t{};
     t.param_dtype = rng() % 2 ? TP_F32 : TP_BF16;
     t.grad_dtype = rng() % 2 ? TP_F32 : TP_BF16;
-    t.n = rng() % 4 ? static_cast<int64_t>(rng() % 20000) : 0;
+    t.n = rng() % 4 ? static_cast<int64_t>(rng() % (rng() % 16 ? 20000 : 10000000)) : 0;
     if (t.n) {
       const int64_t skew = static_cast<int64_t>(rng() % 3), scales = (t.n + TP_ADAMW_BLOCK - 1) / TP_ADAMW_BLOCK;
       t.param = dev(t.n * (t.param_dtype == TP_F32 ? 4 : 2), 4 * skew);

@@ -290,15 +290,17 @@ hipError_t ce_sum_launch(const CeSum& p, hipStream_t) {
 }
 
 hipError_t adamw_launch(const AdamTensor *ts, int64_t num, bool codes, const AdamArgs& a, hipStream_t) {
+  const int64_t chunk = adam_chunk(ts, num);
   int64_t at = 0;
   do {
     AdamTable t;
-    next_adam(ts, num, &at, &t);
+    next_adam(ts, num, &at, &t, chunk, chunk == kAdamChunk);
     check(t.num <= kMaxAdam, "tensors of a launch");
     for (int i = 0; i < t.num; ++i) {
       const AdamTensor& x = t.t[i];
       const int64_t scales = (x.n + kAdamBlock - 1) / kAdamBlock;
-      check((t.first[i + 1] - t.first[i] - 1) * kAdamChunk < x.n && (t.first[i + 1] - t.first[i]) * kAdamChunk >= x.n, "chunks");
+      const int64_t n = (t.first[i + 1] - t.first[i]) * chunk;
+      check(chunk == kAdamChunk ? n <= x.n && n + chunk > x.n : n - chunk < x.n && n >= x.n, "chunks");
       vec(x.param, x.n, x.param_f32 ? 4 : 2, "param");
       vec(x.grad, x.n, x.grad_f32 ? 4 : 2, "grad");
       vec(x.m, x.n, codes ? 1 : 4, "m");

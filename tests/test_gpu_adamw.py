@@ -351,3 +351,47 @@ def test_a_tensor_past_32_bits():
         for big, little in ((ms, s["ms"]), (vs, s["vs"])):
             assert torch.equal(big[at // B:at // B + blocks(k)], little[i])
     assert bool((ms > 0).all()) and bool((vs > 0).all())
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mixed"])
+def test_many_elements_at_once(kind, eight):
+    """Above 2^25 elements in a call chunks are longer; the same bits as from a call for each tensor."""
+    announce(f"adamw many elements {kind} eight {eight}")
+    types = dict(f32=[(F32, F32)], bf16=[(BF16, BF16)], mixed=[(F32, BF16), (BF16, F32)])[kind]
+    sizes = [2 ** 25 + 3, 5, 4096, 4097, 1024, 1023, 3000 + 257, 9_000_001, 0, 4095] + [2000 + i for i in range(60)]
+    g = torch.Generator("cuda").manual_seed(5)
+    calls = []
+    for _ in range(2):
+        g.manual_seed(5)
+        s = dict(p=[], g=[], m=[], v=[], ms=[], vs=[], c=[])
+        for i, n in enumerate(sizes):
+            pt, gt = types[i % len(types)]
+            s["p"].append(torch.randn(n, generator=g, device="cuda").to(pt))
+            s["g"].append((torch.randn(n, generator=g, device="cuda") * 0.01).to(gt))
+            s["m"].append(torch.zeros(n, dtype=torch.int8 if eight else F32, device="cuda"))
+            s["v"].append(torch.zeros(n, dtype=torch.uint8 if eight else F32, device="cuda"))
+            s["ms"].append(torch.zeros(blocks(n), device="cuda"))
+            s["vs"].append(torch.zeros(blocks(n), device="cuda"))
+            s["c"].append(torch.zeros(n, dtype=BF16, device="cuda"))
+        calls.append(s)
+    one, each = calls
+    parts = tp.tp_grad_parts()
+    tp.tp_grad_sumsq(one["g"], parts)
+    kw = dict(lr=1e-2, weight_decay=0.1, parts=parts, max_norm=3.0)
+
+    def scales(s, a, b):
+        return dict(m_scale=s["ms"][a:b], v_scale=s["vs"][a:b]) if eight else {}
+    for t in (1, 2):
+        tp.tp_adamw_step(one["p"], one["g"], one["m"], one["v"], copies=one["c"], step=t, **scales(one, 0, len(sizes)), **kw)
+        for i in range(1, len(sizes)):
+            tp.tp_adamw_step(*(each[k][i:i + 1] for k in ("p", "g", "m", "v")), copies=each["c"][i:i + 1], step=t, **scales(each, i, i + 1), **kw)
+        first = dict((k, each[k][0]) for k in each)      # in four parts, each of whole blocks
+        cuts = [0, 4096 * 2000, 4096 * 4001 + 256, 2 ** 25 - 4096, sizes[0]]
+        for a, b in zip(cuts, cuts[1:]):
+            tp.tp_adamw_step(*([first[k][a:b]] for k in ("p", "g", "m", "v")), copies=[first["c"][a:b]], step=t,
+                             **(dict(m_scale=[first["ms"][a // 256:a // 256 + blocks(b - a)]], v_scale=[first["vs"][a // 256:a // 256 + blocks(b - a)]]) if eight else {}), **kw)
+    torch.cuda.synchronize()
+    for k in one:
+        assert all(torch.equal(x, y) for x, y in zip(one[k], each[k])), k
+    assert all(bool((x != 0).any()) for x in one["m"] if x.numel())
