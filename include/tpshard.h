@@ -816,7 +816,8 @@ int tp_linear_ce_backward_ws(const tp_linear_ce_bwd_args *args, int64_t *bytes);
 /*
  * dz[m, n] = (dloss + dlse) e^(z - lse) - (n is the target) dloss, 0 for ignored
  * targets, from the product computed again, a piece of the vocabulary at a time,
- * rounded to dtype for the two products; dX = dz W^T, dW (+)= X^T dz.
+ * rounded to dtype for the two products (in bf16 after a division by the largest
+ * |dloss|, which they multiply back in fp32); dX = dz W^T, dW (+)= X^T dz.
  * Rows of X with ignored targets are not part of dW, whatever they hold.
  * Reproducible and capturable, as the forward.
  * Errors: as tp_linear_ce.

@@ -17,8 +17,8 @@ enum {
   kModePair = 3,  // c = A W and c2 = A2 W2, two products of one shape in one launch
   kModeStats = 4, // logits z = A W: each tile's row maxima and sums of exponentials (CeGemm)
   kModeProb = 5,  // logits z = A W: c = the loss's gradient at z (CeGemm)
-  kModeScaled = 7, // c = alpha A W (ScaledGemm)
   kModeSlices = 6, // c[s] = A W over slice s of K, fp32, each [M][ldc]: no two workgroups share a sum
+  kModeScaled = 7, // c = alpha A W (ScaledGemm)
 };
 
 // A workspace's first bytes are tickets (zero before and after every launch), its

@@ -1,4 +1,5 @@
-// Tiled bf16 kernels: the cross entropy's gradients' other products.
+// Tiled bf16 kernels: the cross entropy's gradients, but for a weight's that lies k-contiguous.
+// Bound by MFMA: dX of 8192 x 32768 -> 4096 1405 us (1.56 PFLOP/s).
 #include "linear_tiles.h"
 
 namespace tpshard {
