@@ -831,7 +831,8 @@ enum { TP_ADAMW_BLOCK = 256 };
  * codes, each with an fp32 scale for every TP_ADAMW_BLOCK elements (the last may be
  * short):
  *   m = scale sign(q) (q / 127)^2,  v = (scale (q / 255)^2)^2
- * to the nearest code, scale the block's largest |m| (largest sqrt(v)); a v that is
+ * to the nearest code, scale the block's largest |m| (largest sqrt(v); a block whose m
+ * are all below 2^-112 has codes of 0); a v that is
  * not zero has a code of at least 1.  Zeros everywhere are the state before the first step. */
 enum { TP_ADAMW_F32 = 0, TP_ADAMW_8BIT = 1 };
 

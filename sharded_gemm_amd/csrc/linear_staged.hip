@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "ce_dev.h"
+#include "gemm_tiles.h"
 #include "linear_dev.h"
 
 namespace tpshard {
@@ -160,8 +161,11 @@ __global__ void __launch_bounds__(threads_of(BM), waves_simd(BM)) lin_staged_ker
   int64_t tile = blockIdx.x;
   const bool second = MODE == kModePair && tile >= tiles_m * tiles_n;
   if (second) tile -= tiles_m * tiles_n;
-  // Neighbouring workgroups share a W panel (tiles walk down the rows first).
-  const int64_t m0 = tile % tiles_m * BM, n0 = tile / tiles_m * BNO;
+  // Each XCD takes a range of tiles that share panels (against tiles dealt down the rows: bf16, logits of 300 x 1021 ->
+  // 10007 31.1 -> 28.5 us, their gradient over 100 rows 67 -> 59; fp32, which waits for its products, 1 %).
+  int tm, tn;
+  tile_coords(static_cast<int>(tile), static_cast<int>(tiles_m * tiles_n), static_cast<int>(tiles_m), static_cast<int>(tiles_n), &tm, &tn);
+  const int64_t m0 = static_cast<int64_t>(tm) * BM, n0 = static_cast<int64_t>(tn) * BNO;
   const T *A = static_cast<const T *>(second ? p.a2 : p.a), *W = static_cast<const T *>(second ? p.w2 : p.w);
   const T *W2 = static_cast<const T *>(p.w2);
   void *c = second ? p.c2 : p.c;
