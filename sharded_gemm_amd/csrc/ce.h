@@ -94,7 +94,6 @@ struct CeTranspose {
   int32_t f32 = 0;
   CeScale scale;
 };
-hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t s);
 
 // to [rows, cols] (bf16, contiguous, both multiples of 8) <- from [m, n] at stride ld, zero beyond.
 struct CePad {
@@ -102,7 +101,13 @@ struct CePad {
   void *to = nullptr;
   int64_t m = 0, n = 0, ld = 0, rows = 0, cols = 0;
 };
-hipError_t ce_pad_launch(const CePad& p, hipStream_t s);
+// Up to two of them in one launch, which nothing orders; beside a transpose too (`pads` may be empty).
+struct CePads {
+  CePad pad[2];
+  int32_t num = 0;
+};
+hipError_t ce_pad_launch(const CePads& p, hipStream_t s);
+hipError_t ce_transpose_launch(const CeTranspose& p, const CePads& pads, hipStream_t s);
 
 // out [M, K] <- base + *alpha (null: 1) times the sum over s < slices, in order, of part[s]; part [slices][M][K] fp32,
 // base (optional) fp32, out bf16 or fp32 (then it may be base).

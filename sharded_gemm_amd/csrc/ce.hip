@@ -169,12 +169,30 @@ __device__ __forceinline__ void scale_of(const CeScale& p) {
 
 __global__ void __launch_bounds__(1024) ce_scale_kernel(CeScale p) { scale_of<1024>(p); }
 
-// ---- X, transposed ------------------------------------------------------------------
-// 64 tokens x 64 columns through LDS.  T: uint16_t or uint32_t.
+// ---- X, transposed, and padded copies --------------------------------------------------
+// A padded copy's part of a workgroup.
+__device__ __forceinline__ void pad_part(const CePad& p, int64_t block) {
+  const int64_t per = p.cols / 8, i = block * kThreads + threadIdx.x;
+  if (i >= p.rows * per) return;
+  const int64_t r = i / per, c = i % per * 8, left = r < p.m ? p.n - c : 0;
+  *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.to) + i * 8) =
+      left > 0 ? load16<uint16_t>(static_cast<const uint16_t *>(p.from) + r * p.ld + c, left) : u32x4{0, 0, 0, 0};
+}
+// block: counted over both.
+__device__ __forceinline__ void pad_parts(const CePads& p, int64_t block) {
+  const int64_t first = (p.pad[0].rows * (p.pad[0].cols / 8) + kThreads - 1) / kThreads;
+  if (block < first) pad_part(p.pad[0], block);
+  else pad_part(p.pad[1], block - first);
+}
+__global__ void __launch_bounds__(kThreads) ce_pad_kernel(CePads p) { pad_parts(p, blockIdx.x); }
+
+// 64 tokens x 64 columns through LDS; then the copies.  T: uint16_t or uint32_t.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) ce_transpose_kernel(CeTranspose p) {
+__global__ void __launch_bounds__(kThreads) ce_transpose_kernel(CeTranspose p, CePads pads) {
   constexpr int V = 16 / sizeof(T), E = 64, PITCH = E + 4 / sizeof(T);   // a row and a bank
   __shared__ T tile[E * PITCH];
+  const int64_t blocks = (p.K + E - 1) / E * (p.rows / E);
+  if (blockIdx.x >= blocks) return pad_parts(pads, blockIdx.x - blocks);
   if (blockIdx.x == 0) scale_of<kThreads>(p.scale);
   const int64_t tiles_k = (p.K + E - 1) / E, k0 = blockIdx.x % tiles_k * E, m0 = blockIdx.x / tiles_k * E;
 #pragma unroll
@@ -201,15 +219,6 @@ __global__ void __launch_bounds__(kThreads) ce_transpose_kernel(CeTranspose p) {
     }
     *reinterpret_cast<u32x4 *>(static_cast<T *>(p.xt) + (k0 + k) * p.rows + m0 + r) = v;
   }
-}
-
-// ---- a padded copy -------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) ce_pad_kernel(CePad p) {
-  const int64_t per = p.cols / 8, i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= p.rows * per) return;
-  const int64_t r = i / per, c = i % per * 8, left = r < p.m ? p.n - c : 0;
-  *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.to) + i * 8) =
-      left > 0 ? load16<uint16_t>(static_cast<const uint16_t *>(p.from) + r * p.ld + c, left) : u32x4{0, 0, 0, 0};
 }
 
 // ---- dX's sum over slices and pieces ------------------------------------------------
@@ -258,15 +267,25 @@ hipError_t ce_scale_launch(const CeScale& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.K + 63) / 64 * (p.rows / 64)));
-  if (p.f32) hipLaunchKernelGGL(ce_transpose_kernel<uint32_t>, grid, dim3(kThreads), 0, s, p);
-  else hipLaunchKernelGGL(ce_transpose_kernel<uint16_t>, grid, dim3(kThreads), 0, s, p);
+namespace {
+unsigned pad_blocks(const CePads& p) {
+  unsigned n = 0;
+  for (int i = 0; i < p.num; ++i) n += grid_of(p.pad[i].rows * (p.pad[i].cols / 8), kThreads);
+  return n;
+}
+}  // namespace
+
+hipError_t ce_transpose_launch(const CeTranspose& p, const CePads& pads, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.K + 63) / 64 * (p.rows / 64)) + pad_blocks(pads));
+  if (p.f32) hipLaunchKernelGGL(ce_transpose_kernel<uint32_t>, grid, dim3(kThreads), 0, s, p, pads);
+  else hipLaunchKernelGGL(ce_transpose_kernel<uint16_t>, grid, dim3(kThreads), 0, s, p, pads);
   return hipGetLastError();
 }
 
-hipError_t ce_pad_launch(const CePad& p, hipStream_t s) {
-  hipLaunchKernelGGL(ce_pad_kernel, dim3(grid_of(p.rows * (p.cols / 8), kThreads)), dim3(kThreads), 0, s, p);
+hipError_t ce_pad_launch(const CePads& p, hipStream_t s) {
+  const unsigned n = pad_blocks(p);
+  if (!n) return hipSuccess;
+  hipLaunchKernelGGL(ce_pad_kernel, dim3(n), dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 

@@ -72,8 +72,13 @@ hipError_t timed(hipStream_t s, int kind, double work, F&& f) {
   if (e == hipSuccess) timing_end(t0, s, kind, work);
   return e;
 }
-hipError_t pad(const CePad& p, hipStream_t s) {
-  return timed(s, TP_KERNEL_REDUCE, 4.0 * static_cast<double>(p.rows) * static_cast<double>(p.cols), [&] { return ce_pad_launch(p, s); });
+double bytes_of(const CePads& p) {
+  double n = 0;
+  for (int i = 0; i < p.num; ++i) n += 4.0 * static_cast<double>(p.pad[i].rows) * static_cast<double>(p.pad[i].cols);
+  return n;
+}
+hipError_t pad(const CePads& p, hipStream_t s) {
+  return p.num ? timed(s, TP_KERNEL_REDUCE, bytes_of(p), [&] { return ce_pad_launch(p, s); }) : hipSuccess;
 }
 
 // ---- forward ---------------------------------------------------------------------
@@ -263,6 +268,7 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
   const int64_t grid = ((int64_t{1} << 22) - 1) / std::max<int64_t>(1, std::max(cut(c.M, 64), cut(c.K, 64))) * 64;
   int64_t most = b.piece > 0 ? std::max<int64_t>(64, b.piece / 64 * 64)
                              : std::max<int64_t>(8192, (int64_t{1} << 28) / std::max<int64_t>(1, q.rows));
+  if (q.pad) most = std::min(most, (int64_t{1} << 30) / q.K);   // 2 GiB of W
   most = std::max<int64_t>(64, std::min(std::min(most, grid), int64_t{1} << 25) / 64 * 64);
   const int64_t pieces = cut(q.whole, most);
   q.piece = up(cut(q.whole, pieces), 64);
@@ -319,7 +325,8 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
   j.stats = stats;
   j.loss = loss;
   j.lse = lse;
-  if (f.w != f.x && (e = pad(pad_x(c, o, f.K, base + f.x), s)) != hipSuccess) return e;
+  CePads copies;
+  if (f.w != f.x) copies.pad[copies.num++] = pad_x(c, o, f.K, base + f.x);
   for (int64_t n = 0; n < c.V; n += f.piece) {
     const int64_t cols = std::min(f.piece, c.V - n), cols_pad = up(cols, 64);
     CeGemm p;
@@ -329,7 +336,9 @@ hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats
     p.w = weight_at(c, o.W, o.W_ld, n);
     p.ldw = o.W_ld;
     if (f.pad) {
-      if ((e = pad(pad_weight(c, o, n, cols, cols_pad, f.K, base + f.w), s)) != hipSuccess) return e;
+      copies.pad[copies.num++] = pad_weight(c, o, n, cols, cols_pad, f.K, base + f.w);
+      if ((e = pad(copies, s)) != hipSuccess) return e;
+      copies.num = 0;
       p.w = base + f.w;
       p.ldw = c.linear ? f.K : cols_pad;
       p.K = f.K;
@@ -400,6 +409,13 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
   g.scale = c.f32 ? nullptr : scale;
   g.tickets = reinterpret_cast<uint32_t *>(base);
   hipError_t e;
+  CePads copies;   // with the first piece's part of W
+  if (c.M > 0 && q.K != c.K) copies.pad[copies.num++] = pad_x(c, o, q.K, base + q.x);
+  const int64_t n0 = q.tail ? q.whole : 0;
+  if (c.M > 0 && (q.pad || q.tail)) {
+    const int64_t cols = std::min(c.V - n0, q.piece);
+    copies.pad[copies.num++] = pad_weight(c, o, n0, cols, up(cols, 64), q.K, base + q.w);
+  }
   if (b.dW && c.M > 0) {
     CeTranspose t;
     t.X = o.X;
@@ -412,12 +428,11 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
     t.ignore = o.ignore;
     t.f32 = c.f32;
     t.scale = g;
-    e = timed(s, TP_KERNEL_REDUCE, 2.0 * static_cast<double>(es) * MK, [&] { return ce_transpose_launch(t, s); });
-  } else {
+    e = timed(s, TP_KERNEL_REDUCE, 2.0 * static_cast<double>(es) * MK + bytes_of(copies), [&] { return ce_transpose_launch(t, copies, s); });
+  } else if ((e = pad(copies, s)) == hipSuccess) {
     e = timed(s, TP_KERNEL_REDUCE, 12.0 * static_cast<double>(c.M), [&] { return ce_scale_launch(g, s); });
   }
   if (e != hipSuccess) return e;
-  if (c.M > 0 && q.K != c.K && (e = pad(pad_x(c, o, q.K, base + q.x), s)) != hipSuccess) return e;
   // A product of the gradients: in bf16 multiplied by the scale again.
   auto gradient = [&](const LinGemm& of, int kind, double flops) {
     return timed(s, kind, flops, [&] {
@@ -437,7 +452,9 @@ hipError_t ce_backward_launch(const CeSizes& c, const CeOperands& o, const CeBac
     int64_t W_ld = o.W_ld;
     hipError_t r = hipSuccess;
     if (c.M > 0 && copied) {
-      if ((r = pad(pad_weight(c, o, n, cols, wide, q.K, base + q.w), s)) != hipSuccess) return r;
+      CePads next;
+      next.pad[next.num++] = pad_weight(c, o, n, cols, wide, q.K, base + q.w);
+      if (n != n0 && (r = pad(next, s)) != hipSuccess) return r;
       W = base + q.w;
       W_ld = c.linear ? q.K : wide;
     }

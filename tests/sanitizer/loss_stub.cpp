@@ -260,9 +260,21 @@ hipError_t ce_scale_launch(const CeScale& p, hipStream_t) {
   seen("scale");
   return hipSuccess;
 }
-hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t) {
+static int64_t padded(const CePads& pads) {
+  int64_t blocks = 0;
+  for (int i = 0; i < pads.num; ++i) {
+    const CePad& p = pads.pad[i];
+    check(p.cols % 8 == 0 && p.rows >= p.m && p.cols >= p.n && p.m > 0 && p.n > 0, "pad: sizes");
+    need(p.from, p.m, p.n, p.ld, 2, "padded from");
+    vec(p.to, p.rows * p.cols, 2, "padded copy", 16);
+    blocks += (p.rows * (p.cols / 8) + 255) / 256;
+  }
+  if (pads.num) seen("pad");
+  return blocks;
+}
+hipError_t ce_transpose_launch(const CeTranspose& p, const CePads& pads, hipStream_t) {
   check(p.rows % 64 == 0 && p.rows >= p.M && p.M > 0, "transpose: rows");
-  grid((p.K + 63) / 64 * (p.rows / 64), 1, 256);
+  grid((p.K + 63) / 64 * (p.rows / 64) + padded(pads), 1, 256);
   need(p.X, p.M, p.K, p.X_ld, p.f32 ? 4 : 2, "X");
   vec(p.xt, p.K * p.rows, p.f32 ? 4 : 2, "X^T", 16);
   vec(p.targets, p.M, 8, "targets");
@@ -270,12 +282,9 @@ hipError_t ce_transpose_launch(const CeTranspose& p, hipStream_t) {
   seen("transpose");
   return hipSuccess;
 }
-hipError_t ce_pad_launch(const CePad& p, hipStream_t) {
-  check(p.cols % 8 == 0 && p.rows >= p.m && p.cols >= p.n && p.m > 0 && p.n > 0, "pad: sizes");
-  grid((p.rows * (p.cols / 8) + 255) / 256, 1, 256);
-  need(p.from, p.m, p.n, p.ld, 2, "padded from");
-  vec(p.to, p.rows * p.cols, 2, "padded copy", 16);
-  seen("pad");
+hipError_t ce_pad_launch(const CePads& p, hipStream_t) {
+  check(p.num > 0, "no copies");
+  grid(padded(p), 1, 256);
   return hipSuccess;
 }
 hipError_t ce_sum_launch(const CeSum& p, hipStream_t) {
