@@ -395,3 +395,37 @@ def test_many_elements_at_once(kind, eight):
     for k in one:
         assert all(torch.equal(x, y) for x, y in zip(one[k], each[k])), k
     assert all(bool((x != 0).any()) for x in one["m"] if x.numel())
+
+
+@pytest.mark.parametrize("scale, n", [(s, 1 << 20) for s in (1e-30, 1e-18, 1e-14, 1e-8, 1.0, 1e15)] + [(s, (1 << 25) + 300) for s in (1e-14, 1.0)])
+def test_codes_to_the_bit(scale, n):
+    """States after a first step against the same operations in fp32 on the CPU, each rounded by itself: nothing may
+    differ, near the middle between two codes and at magnitudes where the hardware's root is not taken included."""
+    announce(f"adamw codes {scale} {n}")
+    g = Group([n], eight=True, zero=True, seed=12, copy=False, scale=scale)
+    if scale == 1.0:      # and blocks whose elements differ by up to 1e9
+        d = g.host["g"][0]
+        d[:n // 2] *= torch.pow(10.0, -9 * torch.rand(n // 2, generator=torch.Generator().manual_seed(1)))
+        g.dev["g"][0].t.copy_(d)
+    g.step(step=1, lr=1e-3)
+    torch.cuda.synchronize()
+    # numpy: its roots are rounded to the nearest (torch's, on the CPU, are off by a step now and then).
+    f = np.float32
+    d = g.host["g"][0].numpy()
+    m = d * f(1.0 - 0.9)
+    v = (d * f(1.0 - 0.999)) * d
+    for name, x, top in (("m", m, f(127)), ("v", np.sqrt(v), f(255))):
+        a = np.pad(np.abs(x), (0, -n % 256)).reshape(-1, 256)
+        s = a.max(axis=1, keepdims=True)
+        assert np.array_equal(g.dev[name + "s"][0].t.cpu().numpy(), s[:, 0])
+        with np.errstate(invalid="ignore"):
+            q = np.where(s > 0, np.rint(top * np.sqrt(a / s)), f(0)).reshape(-1)[:n]
+        q = np.maximum(q, (x > 0).astype(f)) if name == "v" else np.copysign(q, x)
+        assert q.dtype == f and np.array_equal(g.dev[name][0].t.cpu().numpy().astype(f), q)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_no_eps(eight):
+    g = Group([5000], eight=eight, seed=13)
+    g.step(step=100, lr=1e-3, eps=0.0)
+    g.check(step=100, eps=0.0)
