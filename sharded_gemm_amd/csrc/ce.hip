@@ -48,18 +48,18 @@ __global__ void __launch_bounds__(kThreads) ce_logits_kernel(CeLogits p) {
   if (lane == 0) tops[wave] = top;
   __syncthreads();
   top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const float to = shift_of(top);
+  const Against to(top);
   float s = 0.0f;
 #pragma unroll
   for (int q = 0; q < PER / 4; ++q)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s += exp2_(fmaf(v[q][e], kLog2e, -to));   // past the end: 2^-inf
+    for (int e = 0; e < 4; ++e) s += exp2_(fmaf(v[q][e], to.by, -to.to));   // past the end: 2^-inf
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   if (lane == 0) sums[wave] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    s = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    s = ((sums[0] + sums[1]) + (sums[2] + sums[3])) * exp2_(to.rest);
     *reinterpret_cast<f32x2 *>(p.part + 2 * (blockIdx.x * p.M + m)) = f32x2{top, s};
     const int t = column_of(p.targets[m], p.begin, p.n);
     if (t >= n0 && t < n0 + kCeStatCols) p.logit[m] = z[t];
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) ce_join_kernel(CeJoin p) {
   finish(p, m, a, p.logit[m]);
 }
 
-// Pieces' statistics: {max, sum of e^(z - max) (of e^z where max is not finite), target's logit or -inf}.
+// Pieces' statistics: {max, sum of e^(z - max), target's logit or -inf}.
 __global__ void __launch_bounds__(kThreads) ce_pieces_kernel(const float *stats, int64_t pieces, int64_t M,
                                                              const int64_t *targets, int64_t ignore, float *loss,
                                                              float *lse) {
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) ce_pieces_kernel(const float *stats,
   float logit = minus_inf();
   for (int64_t i = 0; i < pieces; ++i) {
     const float *p = stats + 3 * i * M + m;
-    a = join(a, f32x2{p[0], p[M] * exp2_(-rest_of(p[0]))});
+    a = join(a, f32x2{p[0], p[M]});
     // (the target's piece; its logit may be a NaN)
     logit = p[2 * M] > logit || p[2 * M] != p[2 * M] ? p[2 * M] : logit;
   }

@@ -1,13 +1,14 @@
 // Device code of the vocabulary cross entropy: row statistics of logits, how they
 // combine, and the epilogues of the products whose output are logits.
 //
-// A set of logits of one row is held as {top, s}: its maximum, and s = sum of
-// 2^(z log2 e - r) against r = top log2 e as rounded to fp32, so
-//   ln sum e^z = top + ln 2 (log2 s + (r - top log2 e)).
-// z log2 e - r is one fma: what rounding r changed is common to all terms, and the
-// last line takes it out again.  Where the maximum is not finite (or r is not) the
-// exponents are taken against 0 instead: an infinite logit makes s infinite, a NaN
-// makes it NaN, and minus infinity everywhere leaves 0.
+// A set of logits of one row is held as {top, s}: its maximum, and s = sum of e^(z - top), so
+//   ln sum e^z = top + ln s.
+// A tile's terms are 2^(z log2 e - r), one fma and exp2 each, r = top log2 e as rounded to
+// fp32: what rounding r changed is common to all of them, and one factor a row takes it out again.  From
+// |top| = 2^30 on (kFar) that factor would pass 2^64; there logits that differ do so by 64
+// and more, so the terms are 2^(z - top): one for each logit that equals the maximum, and nothing for
+// the others.  Where the maximum is infinite the exponents are taken against 0: an infinite
+// logit makes s infinite, a NaN makes it NaN, and minus infinity everywhere leaves 0.
 #pragma once
 
 #include "ce.h"
@@ -23,31 +24,30 @@ using lin::kLog2e;
 constexpr float kLn2 = 0.693147180559945309417f;
 
 __device__ __forceinline__ float minus_inf() { return -__builtin_inff(); }
-// What the exponents of a set with maximum `top` are taken against.
-__device__ __forceinline__ float shift_of(float top) {
-  const float r = top * kLog2e;
-  return __builtin_isfinite(r) ? r : 0.0f;
-}
+constexpr float kFar = 0x1p30f;
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The part of {top, s} in a sum against `to`.  A set with nothing in it (s = 0, any maximum) stays out of it.
-__device__ __forceinline__ float part_of(f32x2 a, float to) { return a[1] == 0.0f ? 0.0f : a[1] * exp2_(shift_of(a[0]) - to); }
+// How terms are taken against `top`: 2^(z by - to), times 2^rest in all.
+struct Against {
+  float by, to, rest;
+  __device__ __forceinline__ explicit Against(float top) {
+    const float t = __builtin_isinf(top) ? 0.0f : top;
+    by = fabsf(t) < kFar ? kLog2e : 1.0f;
+    to = t * by;
+    rest = fmaf(-t, by, to);
+  }
+};
 
+// (Equal maxima may be infinite ones; a set with nothing in it has minus infinity and 0.)
 __device__ __forceinline__ f32x2 join(f32x2 a, f32x2 b) {
-  const float top = fmaxf(a[0], b[0]), to = shift_of(top);
-  return f32x2{top, part_of(a, to) + part_of(b, to)};
-}
-
-// r - top log2 e, which the fma leaves unrounded (0 where the exponents were taken against 0).
-__device__ __forceinline__ float rest_of(float top) {
-  const float r = top * kLog2e;
-  return __builtin_isfinite(r) ? fmaf(-top, kLog2e, r) : 0.0f;
+  const float top = fmaxf(a[0], b[0]), low = fminf(a[0], b[0]), away = top == low ? 0.0f : low - top;
+  const bool first = a[0] == top;
+  return f32x2{top, fmaf(first ? b[1] : a[1], exp2_(away * kLog2e), first ? a[1] : b[1])};
 }
 
 // ln sum e^z of the set.
 __device__ __forceinline__ float lse_of(f32x2 a) {
-  const float base = __builtin_isfinite(a[0] * kLog2e) ? a[0] : 0.0f;
-  return fmaf(kLn2, __builtin_amdgcn_logf(a[1]) + rest_of(a[0]), base);
+  return fmaf(kLn2, __builtin_amdgcn_logf(a[1]), __builtin_isinf(a[0]) ? 0.0f : a[0]);
 }
 
 // The column of target t among the n that begin with id `begin`, or -1 (the subtraction may wrap).
@@ -62,7 +62,7 @@ __device__ __forceinline__ void finish(const CeJoin& p, int64_t m, f32x2 a, floa
   if (column_of(id, p.begin, p.V) < 0) logit = minus_inf();
   if (p.stats) {
     p.stats[m] = a[0];
-    p.stats[p.M + m] = a[1] * exp2_(rest_of(a[0]));   // against the maximum itself
+    p.stats[p.M + m] = a[1];
     p.stats[2 * p.M + m] = logit;
   }
   const float lse = lse_of(a);
@@ -115,13 +115,14 @@ __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&
     for (int i = 0; i < TM; ++i) top[i] = over_groups(top[i], [](float x, float y) { return fmaxf(x, y); });
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const float to = shift_of(top[i]);
+      const Against t(top[i]);
       s[i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (!CHECK || static_cast<int>(cn(j)) + e < N) s[i] += exp2_(fmaf(acc[i][j][e], kLog2e, -to));
+          if (!CHECK || static_cast<int>(cn(j)) + e < N) s[i] += exp2_(fmaf(acc[i][j][e], t.by, -t.to));
+      s[i] *= exp2_(t.rest);
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -177,12 +178,13 @@ __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN]
   for (int i = 0; i < TM; ++i) {
     const int64_t m = rm(i);
     if (m >= p.pad_rows) continue;
-    const float lse = lses[i], g = gs[i], gh = ghs[i];
+    const float lse = lses[i], g = gs[i];
     const bool on = m < p.M && id[i] != p.ignore;
     const int t = column_of(id[i], p.begin, p.cols);
-    // (z - lse) log2 e: in bf16 as one fma, whose common error of 2^-24 |lse| is far below the rounding of
-    // the result; in fp32 the difference first, which is exact where z and lse are close.
-    const float far = -lse * kLog2e;
+    // (z - lse) log2 e: in bf16 as one fma, as above (an infinite lse stays where it is); in fp32 the difference first, which is
+    // exact where z and lse are close.
+    const Against by(lse);
+    const float to = __builtin_isinf(lse) ? lse : by.to, gh = sizeof(T) == 4 ? ghs[i] : ghs[i] * exp2_(by.rest);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
       const int64_t n = cn(j), left = p.N - n;
@@ -191,7 +193,7 @@ __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN]
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float z = acc[i][j][e];
-        y[e] = gh * (sizeof(T) == 4 ? exp2_((z - lse) * kLog2e) : exp2_(fmaf(z, kLog2e, far)));
+        y[e] = gh * (sizeof(T) == 4 ? exp2_((z - lse) * kLog2e) : exp2_(fmaf(z, by.by, -to)));
       }
       const int at = t - static_cast<int>(n);
       if (static_cast<unsigned>(at) < 4u) {   // (t is a column or -1)
