@@ -752,13 +752,14 @@ typedef struct {
   float *lse;            /* the whole vocabulary; optional [M] */
   void *ws;              /* tp_linear_ce_ws bytes, 16-byte aligned.  Its first 4096 bytes are
                             zero before its first use, and again after every call; calls of any
-                            sizes may follow one another on it, calls that may overlap need
-                            one each */
+                            sizes that it holds may follow one another on it, calls that may
+                            overlap need one each */
   int64_t ws_bytes;
 } tp_linear_ce_args;
 
-/* Bytes of workspace the call needs.  Reads dtype, weight_layout and the sizes.
- * Host only. */
+/* Bytes of workspace the call needs; never fewer for more tokens (of one dtype, layout, V
+ * and K), so that a full batch's serves ragged ones.  Reads dtype, weight_layout and
+ * the sizes.  Host only. */
 int tp_linear_ce_ws(const tp_linear_ce_args *args, int64_t *bytes);
 
 /*

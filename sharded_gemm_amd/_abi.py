@@ -1139,7 +1139,8 @@ def _per_token(t, name, M):
 
 def tp_linear_ce_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH):
     """A workspace (uint8 tensor, its tickets zeroed on the current stream) for ``tp_linear_ce``
-    of these shapes.  It serves any number of calls one after another, also of smaller shapes."""
+    of these shapes.  It serves any number of calls one after another, of X with as many rows or
+    fewer; a call with another W is refused where it needs more."""
     import torch
     args = tp_linear_ce_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),
                              V=_weight_dims(W, weight_layout)[1], K=int(X.shape[1]))

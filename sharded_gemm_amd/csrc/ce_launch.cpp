@@ -100,6 +100,7 @@ constexpr int64_t kTileCols = 768;   // a multiple of every tile's columns
 struct Forward {
   bool rows = false, small = false, pad = false;   // the few-row kernel; tiles of 64 columns; padded copies
   int64_t piece = 0, slots = 0, K = 0;             // columns of a launch; pairs of a row at most; K as multiplied
+  int64_t held = 0;                                // columns of W that there is room for a copy of, whatever M is
   int64_t part = 0, logit = 0, logits = 0, x = 0, w = 0, total = 0;   // offsets; total: bytes
 };
 
@@ -118,7 +119,7 @@ Forward forward_plan(const CeSizes& c) {
     joined = lin_gemm_ws(one);
     if (c.V % f.piece) joined = std::max(joined, lin_gemm_ws(logits_product(c, kModeOne, c.V % f.piece)));
   } else if (f.small) {
-    f.piece = std::min(c.V, int64_t{1} << 24);   // (a launch's threads stay below 2^32)
+    f.piece = f.held = std::min(c.V, int64_t{1} << 24);   // (a launch's threads stay below 2^32)
     f.slots = cut(c.V, 64);
     LinGemm q = st;
     q.K = f.K;
@@ -127,10 +128,12 @@ Forward forward_plan(const CeSizes& c) {
   } else {
     const int64_t span = std::max(kTileCols, ((int64_t{1} << 31) - 1) / (2 * c.K));
     const int64_t grid = ((int64_t{1} << 22) - 1) / cut(c.M, 64) * 64;
-    int64_t most = std::min(c.linear && !c.f32 ? std::min(span, grid) : grid, int64_t{1} << 25);
+    int64_t most = int64_t{1} << 25;
+    if (c.linear && !c.f32) most = std::min(most, span);
     if (f.pad) most = std::min(most, std::max(16 * kTileCols, (int64_t{1} << 27) / f.K));   // 256 MiB of W
-    most = most / kTileCols * kTileCols;
-    f.piece = up(cut(c.V, cut(c.V, most)), kTileCols);
+    auto even = [&](int64_t cols) { return up(cut(c.V, cut(c.V, cols / kTileCols * kTileCols)), kTileCols); };
+    f.piece = even(std::min(most, grid));
+    f.held = even(most);
     f.slots = cut(c.V, c.f32 ? 64 : 128) + cut(c.V, f.piece);
   }
   f.part = up(std::max(joined, kTicketBytes), kAlign);
@@ -138,8 +141,30 @@ Forward forward_plan(const CeSizes& c) {
   f.logits = f.logit + up(c.M * 4, kAlign);
   f.x = f.logits + (f.rows ? up(c.M * up(f.piece, 4) * 4, kAlign) : 0);
   f.w = f.x + (f.pad && c.K != f.K ? up(c.M * f.K * 2, kAlign) : 0);
-  f.total = f.w + (f.pad ? up(std::min(f.piece, c.V), 64) * f.K * 2 : 0);
+  f.total = f.w + (f.pad ? up(std::min(f.held, c.V), 64) * f.K * 2 : 0);
   return f;
+}
+
+// What every M up to this one needs, so that a workspace of a full batch serves a ragged one: few rows
+// split K, have twice the pairs, or (fp32) keep logits, where many do not.  Between the places
+// below a plan's bytes only grow: all rows that the few-row kernel takes; whole 64s
+// of those on small tiles; the last rows without padded copies.
+int64_t forward_bytes(const CeSizes& c) {
+  int64_t need = forward_plan(c).total;
+  auto with = [&](int64_t M) {
+    if (M >= c.M) return false;
+    CeSizes d = c;
+    d.M = M;
+    const Forward f = forward_plan(d);
+    need = std::max(need, f.total);
+    return f.small;
+  };
+  if (c.f32)
+    for (int64_t M = 1; M <= 16; ++M) (void)with(M);
+  for (int64_t M : {511, 1023}) (void)with(M);
+  for (int64_t M = 64; with(M); M += 64) {
+  }
+  return need;
 }
 
 // Columns of a tile.
@@ -305,7 +330,7 @@ bool ce_sizes_ok(const CeSizes& c) {
          c.M * 8 < (int64_t{1} << 40);
 }
 
-int64_t ce_forward_ws(const CeSizes& c) { return forward_plan(c).total; }
+int64_t ce_forward_ws(const CeSizes& c) { return forward_bytes(c); }
 
 hipError_t ce_forward_launch(const CeSizes& c, const CeOperands& o, float *stats, float *loss, float *lse, void *ws,
                              hipStream_t s) {
