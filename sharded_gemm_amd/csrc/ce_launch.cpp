@@ -193,7 +193,10 @@ int64_t columns_of(const LinChoice& h) {
 // of their part of W; where X and W are padded anyway every piece is copied.
 //
 // Pieces: 2^28 elements of P (512 MiB in bf16), so that dX is not read and
-// written again often: with 8192 x 4096 tokens every further piece costs 268 MB.
+// written again often: with 8192 x 4096 tokens every further piece costs 268 MB.  A bf16 weight's
+// part of a piece stays below the 2^31 bytes that the ping-pong kernels' offsets reach, where rows are
+// columns of the vocabulary or copied ([K, V] spans all its bytes whatever the piece): in one
+// piece 800 x 12288 -> 131072 ran on 128 x 128 tiles throughout.
 // The tail comes first, so that the last piece's sum can be dX itself.
 //
 // dX has few tiles where M K is not large, and a long sum: it is cut into slices of
@@ -293,7 +296,7 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
   const int64_t grid = ((int64_t{1} << 22) - 1) / std::max<int64_t>(1, std::max(cut(c.M, 64), cut(c.K, 64))) * 64;
   int64_t most = b.piece > 0 ? std::max<int64_t>(64, b.piece / 64 * 64)
                              : std::max<int64_t>(8192, (int64_t{1} << 28) / std::max<int64_t>(1, q.rows));
-  if (q.pad) most = std::min(most, (int64_t{1} << 30) / q.K);   // 2 GiB of W
+  if (!c.f32 && (c.linear || q.pad)) most = std::min(most, ((int64_t{1} << 30) - 1) / q.K);
   most = std::max<int64_t>(64, std::min(std::min(most, grid), int64_t{1} << 25) / 64 * 64);
   const int64_t pieces = cut(q.whole, most);
   q.piece = up(cut(q.whole, pieces), 64);
@@ -305,8 +308,13 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
       LinGemm z = logits_product(c, kModeProb, wide);
       z.K = q.K;
       joined = std::max(joined, lin_gemm_ws(z));
-      if (b.dX) joined = std::max(joined, lin_gemm_ws(dx_product(c, wide, cols != wide || q.pad)));
-      if (b.dX) slices = std::max<int64_t>(slices, slices_of(c, wide).splits);
+      if (b.dX) {
+        LinGemm p = dx_product(c, wide, cols != wide || q.pad);
+        joined = std::max(joined, lin_gemm_ws(p));
+        p.lda = q.piece;
+        p.ldw = c.linear ? q.K : p.groups ? wide : c.V;   // at least
+        if (spans_ok(p)) slices = std::max<int64_t>(slices, slices_of(c, wide).splits);
+      }
       if (b.dW) joined = std::max(joined, lin_gemm_ws(dw_product(c, cols, q.rows)));
       return hipSuccess;
     });
