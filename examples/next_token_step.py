@@ -52,7 +52,7 @@ class NextToken:
         self.ws = tp.tp_linear_ce_ws(self.block.out, head, weight_layout=LINEAR)
         self.bws = tp.tp_linear_ce_backward_ws(self.block.out, head, weight_layout=LINEAR, dX=dx)
         self.parts, self.norm = tp.tp_grad_parts(), torch.empty(1, device="cuda")
-        self.count = torch.zeros(1, dtype=torch.int64, device="cuda")        # steps so far, on the device
+        self.count = torch.zeros(1, dtype=torch.int64, device="cuda")        # steps taken, on the device
         blocks = [-(-v.numel() // tp.TP_ADAMW_BLOCK) for v in self.main.values()]
         if eight:
             self.m, self.v = ([torch.zeros(v.shape, dtype=t, device="cuda") for v in self.main.values()]
@@ -91,7 +91,7 @@ class NextToken:
         self.block.backward(self.x, self.d_out)
 
     def step(self, rate, decay=0.01):
-        """One clipped AdamW step of every weight, and the products' copies of them."""
+        """One clipped AdamW step of every weight, and the products' copies of them; with gradients that are not finite, none."""
         self.count.add_(1)
         grads = [self.grads[k] for k in self.main]
         tp.tp_grad_sumsq(grads, self.parts)
@@ -99,6 +99,7 @@ class NextToken:
                          weight_decay=[0.0 if k == "bias" else decay for k in self.main],
                          copies=[self.copies.get(k) for k in self.main], parts=self.parts, max_norm=self.max_norm,
                          norm_out=self.norm, skip_nonfinite=True, **self.scales)
+        self.count.sub_(torch.isfinite(self.norm).logical_not().long())      # the states did not take that one
         return self.norm
 
 

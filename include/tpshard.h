@@ -863,7 +863,7 @@ typedef struct {
   double clip_eps;
   float *norm_out;       /* optional: the norm (with parts only) */
   int32_t skip_nonfinite;/* 1: where the norm is infinite or NaN, nothing but norm_out is written
-                            (with parts only) */
+                            (with parts only); such a step is not one to count */
 } tp_adamw_args;
 
 /*

@@ -1280,7 +1280,7 @@ def tp_adamw_step(params, grads, m, v, *, step, lr, beta1=0.9, beta2=0.999, eps=
     or one per tensor.  ``copies``: bf16 tensors (or None) that receive the new weights.  ``parts``
     (from ``tp_grad_sumsq``) and ``max_norm`` clip as ``tp_grad_clip`` does, in the same pass;
     ``norm_out`` (fp32 [1]) receives the norm, and with ``skip_nonfinite`` a step whose norm is
-    infinite or NaN changes nothing else."""
+    infinite or NaN changes nothing else (and is not one to count: take it off ``step`` again)."""
     import torch
     lib = load()
     params, grads, m, v = list(params), list(grads), list(m), list(v)
