@@ -334,8 +334,7 @@ Backward backward_plan(const CeSizes& c, const CeBackward& b) {
 bool ce_sizes_ok(const CeSizes& c) {
   // A piece of kTileCols columns against all rows, and of all of K against them, within the grid.
   return c.M < (int64_t{1} << 31) && c.V < (int64_t{1} << 31) && c.K < (int64_t{1} << 24) &&
-         cut(c.M, 64) * (kTileCols / 64) < (int64_t{1} << 22) && cut(c.M, 64) * cut(c.K, 64) < (int64_t{1} << 22) &&
-         c.M * 8 < (int64_t{1} << 40);
+         cut(c.M, 64) * (kTileCols / 64) < (int64_t{1} << 22) && cut(c.M, 64) * cut(c.K, 64) < (int64_t{1} << 22);
 }
 
 int64_t ce_forward_ws(const CeSizes& c) { return forward_bytes(c); }

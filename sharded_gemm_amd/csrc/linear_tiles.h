@@ -253,7 +253,9 @@ hipError_t dispatch_tiles(const LinGemm& p, const TilePick& t, hipStream_t s) {
     case kTile32:
       if constexpr (MODE == kModeStats) return launch_ring<32, 64, 64, 4, MODE, AT, WT, 2, 2>(p, t.splits, s);
       break;
-    case kTile64k32: return launch_ring<64, dual ? 128 : 64, 32, 4, MODE, AT, WT, 2, 2>(p, t.splits, s);
+    case kTile64k32:   // (a^T w^T: K is tokens, in multiples of 64)
+      if constexpr (!AT || !WT) return launch_ring<64, dual ? 128 : 64, 32, 4, MODE, AT, WT, 2, 2>(p, t.splits, s);
+      break;
   }
   return hipErrorInvalidValue;
 }
