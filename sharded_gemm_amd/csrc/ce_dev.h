@@ -158,7 +158,9 @@ __device__ __forceinline__ void stats(const CeGemm& p, char *lds, const f32x4 (&
 // products that read it.  In bf16 it is divided by the largest |g| first, which the
 // products multiply back in fp32: most of a row's gradient is its target's entry, -g (1 -
 // p), and where all g are alike (a mean) every one of them would be rounded the same
-// way, up to 0.4 % of the result; divided, they round to -1.
+// way, up to 0.4 % of the result; divided, they round to -1 where targets are unlikely.
+// Of likely ones what is off is independent from entry to entry: 2^-8 / sqrt(3) of the result's norm at
+// most (0.0013 measured in an fp32 dX at a mean p of 0.25, 0.0015 at 0.6).
 template <typename T, int TM, int TN, typename RM, typename CN>
 __device__ __forceinline__ void prob(const CeGemm& p, const f32x4 (&acc)[TM][TN], RM&& rm, CN&& cn) {
   // Every row's loads before any store, which the compiler may not move them across.
