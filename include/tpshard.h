@@ -810,8 +810,13 @@ typedef struct {
   int64_t ws_bytes;
 } tp_linear_ce_bwd_args;
 
-/* Bytes of workspace the call needs.  Reads dtype, weight_layout, dx_dtype, the sizes,
- * piece, and which of dX and dW are asked for (non-NULL).  Host only. */
+/* Bytes of workspace the call needs, for its own sizes (fewer tokens may need more): the
+ * gradient at a piece's logits (2^28 elements of dtype, or M x 8192 where that is more, or M x
+ * piece), X transposed (for dW), an fp32 dX (for a bf16 one of several pieces) or up to
+ * 16 (where few tokens' sum over the vocabulary is cut), copies of X and of a piece's part of W
+ * (below 2 GiB, in bf16 with sizes off the multiples that the kernels take), and where
+ * products are small their partial tiles (up to 256 MiB).  Reads dtype, weight_layout, dx_dtype, the sizes, piece, and which of dX and dW are
+ * asked for (non-NULL).  Host only. */
 int tp_linear_ce_backward_ws(const tp_linear_ce_bwd_args *args, int64_t *bytes);
 
 /*

@@ -1193,7 +1193,8 @@ def tp_ce_join(stats, targets, *, loss=None, lse=None, ignore_index=-100, stream
 
 
 def tp_linear_ce_backward_ws(X, W, *, weight_layout=TP_WEIGHTS_MATH, dX=None, dW=True, piece=0):
-    """A workspace (uint8 tensor) for ``tp_linear_ce_backward`` of these shapes.  ``dX``: the
+    """A workspace (uint8 tensor) for ``tp_linear_ce_backward`` of these shapes (others have to ask
+    anew, smaller ones too; ``tpshard.h`` says what it holds).  ``dX``: the
     tensor that is passed there (its type decides whether the sum over pieces is kept here),
     None without it; ``dW``: whether it is asked for."""
     args = tp_linear_ce_bwd_args(dtype=_dtype_code(X), weight_layout=weight_layout, M=int(X.shape[0]),

@@ -192,8 +192,9 @@ int64_t columns_of(const LinChoice& h) {
 // the vocabulary's last V % 64 columns are a piece of their own, with a padded copy
 // of their part of W; where X and W are padded anyway every piece is copied.
 //
-// Pieces: 2^28 elements of P (512 MiB in bf16), so that dX is not read and
-// written again often: with 8192 x 4096 tokens every further piece costs 268 MB.  A bf16 weight's
+// Pieces: 2^28 elements of P (512 MiB in bf16, 1 GiB in fp32), but 8192 columns at least (so with more than
+// 32768 tokens P grows with them), so that dX is not read and written again often: with 8192 x 4096
+// tokens every further piece costs 268 MB.  A bf16 weight's
 // part of a piece stays below the 2^31 bytes that the ping-pong kernels' offsets reach, where rows are
 // columns of the vocabulary or copied ([K, V] spans all its bytes whatever the piece): in one
 // piece 800 x 12288 -> 131072 ran on 128 x 128 tiles throughout.

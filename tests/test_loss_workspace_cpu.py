@@ -66,3 +66,37 @@ def test_every_token_count(dtype, layout):
             n = forward_bytes(dtype, layout, M, K, V)
             assert n >= last, (K, V, M)
             last = n
+
+
+def backward_bytes(dtype, layout, M, K, V, **kw):
+    n, a = C.c_int64(), dict(dtype=dtype, weight_layout=layout, dx_dtype=dtype, M=M, V=V, K=K, dX=16, dW=16)
+    assert _abi.load().tp_linear_ce_backward_ws(C.byref(_abi.tp_linear_ce_bwd_args(**(a | kw))), C.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("dtype", [tp.TP_BF16, tp.TP_F32])
+@pytest.mark.parametrize("M", [1, 100, 1024, 5000, 32_768, 131_072, 1_048_576])
+@pytest.mark.parametrize("K,V,odd", [(1024, 131072, False), (1024, 131001, False), (4095, 131001, True), (12288, 50000, False), (1000, 600_001, True), (300, 100, True)])
+def test_the_backward_s_bytes(M, K, V, odd, dtype, layout):
+    """What the header says it holds, part by part."""
+    if (M + 63) // 64 * ((K + 63) // 64) >= 1 << 22:
+        pytest.skip("past the grid")
+    es, rows = (2 if dtype == tp.TP_BF16 else 4), (M + 63) // 64 * 64
+    odd = dtype == tp.TP_BF16 and (odd or (layout == 0 and V % 8 != 0))
+    sums = M * K * 4 * (16 if M < 8192 else 1)
+    copies = (2 * M * (K + 63) + min(1 << 31, 2 * (K + 63) * (V + 63))) if odd else 128 * K
+    rest = sums + copies + (257 << 20)
+    p = min(rows * (V + 63), max(1 << 28, 8192 * rows)) * es
+    assert backward_bytes(dtype, layout, M, K, V) <= p + K * rows * es + rest
+    assert backward_bytes(dtype, layout, M, K, V, dW=None) <= p + rest
+    assert backward_bytes(dtype, layout, M, K, V, piece=2048) <= rows * 2048 * es + K * rows * es + rest
+    if dtype == tp.TP_BF16:
+        assert backward_bytes(dtype, layout, M, K, V, dx_dtype=tp.TP_F32) <= p + K * rows * es + rest
+
+
+def test_the_backward_s_bytes_at_sizes_that_are_stated():
+    gib = 1 << 30
+    assert abs(backward_bytes(tp.TP_BF16, 1, 131_072, 1024, 131_072) / gib - 2.75) < 0.01
+    assert abs(backward_bytes(tp.TP_F32, 1, 131_072, 1024, 131_072) / gib - 4.5) < 0.01
+    assert abs(backward_bytes(tp.TP_BF16, 1, 1024, 4095, 128_001) / gib - 1.3) < 0.05
