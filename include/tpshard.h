@@ -815,8 +815,8 @@ typedef struct {
  * piece), X transposed (for dW), an fp32 dX (for a bf16 one of several pieces) or up to
  * 16 (where few tokens' sum over the vocabulary is cut), copies of X and of a piece's part of W
  * (below 2 GiB, in bf16 with sizes off the multiples that the kernels take), and where
- * products are small their partial tiles (up to 256 MiB).  Reads dtype, weight_layout, dx_dtype, the sizes, piece, and which of dX and dW are
- * asked for (non-NULL).  Host only. */
+ * products are small their partial tiles (up to 256 MiB).  Reads dtype, weight_layout,
+ * dx_dtype, the sizes, piece, and which of dX and dW are asked for (non-NULL).  Host only. */
 int tp_linear_ce_backward_ws(const tp_linear_ce_bwd_args *args, int64_t *bytes);
 
 /*
